@@ -26,6 +26,10 @@ from ._lib import GlaChunkOptions, GlaError, status_string  # noqa: F401
 __all__ = ["gla_chunk_fwd", "gla_chunk_fwd_varlen", "gla_chunk_fwd_varlen_plan",
            "gla_chunk_fwd_plan", "gla_chunk_bwd", "gla_chunk_bwd_plan", "gla_chunk_bwd_varlen",
            "gla_chunk", "gla_chunk_varlen", "gla_gdn_fwd",
+           "gla_scan_fwd", "gla_scan_bwd", "gla_scan", "gla_scan_step", "gla_scan_fwd_varlen",
+           "gla_scan_bwd_varlen", "gla_scan_varlen", "gla_scan_checkpoints",
+           "gla_qk_norm_rope_fwd", "gla_qk_norm_rope_bwd", "gla_qk_norm_rope",
+           "gla_rope_frequencies",
            "gla_recurrent_step", "gla_last_device_status", "GlaError", "status_string",
            "library_path"]
 
@@ -418,11 +422,14 @@ def gla_chunk_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alph
 
 def gla_gdn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                 beta: torch.Tensor, scale: float | None = None, h0: torch.Tensor | None = None,
-                output_final_state: bool = True, chunked: bool = False):
+                output_final_state: bool = True, chunked: bool = False, *,
+                qk_l2norm: bool = False, norm_eps: float = 1e-6):
     """Gated delta rule (Gated DeltaNet) forward: ``(o, hT)``.
 
-    q, k ``[B,H,T,dk]`` bf16 (k as given: normalise it first); v ``[B,H,T,dv]``
-    bf16; g (log alpha) and beta ``[B,H,T]`` fp32; h0 ``[B,H,dk,dv]`` fp32 or None.
+    q, k ``[B,H,T,dk]`` bf16 (as given, or with ``qk_l2norm=True`` each row
+    divided by its length first, ``gla_qk_norm_rope_fwd`` with ``norm="l2"`` and
+    ``norm_eps``); v ``[B,H,T,dv]`` bf16; g (log alpha) and beta ``[B,H,T]`` fp32;
+    h0 ``[B,H,dk,dv]`` fp32 or None.
     ``chunked=True`` calls gla_gdn_chunk_fwd (the chunk algorithm on the tensor
     cores, dk = 128), else gla_gdn_fwd (token-recurrent).
     """
@@ -440,6 +447,8 @@ def gla_gdn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     _need(beta, "beta", torch.float32, (B, H, T), dev)
     if h0 is not None:
         _need(h0, "h0", torch.float32, (B, H, dk, dv), dev)
+    if qk_l2norm:
+        q, k = gla_qk_norm_rope_fwd(q.transpose(1, 2), k.transpose(1, 2), norm="l2", eps=norm_eps)
     if scale is None:
         scale = dk ** -0.5
     o = torch.empty(B, H, T, dv, dtype=torch.bfloat16, device=dev)
@@ -482,6 +491,391 @@ def gla_recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_al
                                            out.data_ptr(), B, H, dk, dv, _stream(dev))
     _lib.check(st, "gla_recurrent_step")
     return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+_DTYPES = {torch.bfloat16: _lib.GLA_BF16, torch.float32: _lib.GLA_F32}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+class _Scan:
+    """The sizes of a scan call, from x and (packed) the sequences' bounds."""
+
+    def __init__(self, x: torch.Tensor, cu_seqlens=None):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor")
+        if x.device.type != "cuda":
+            raise ValueError("x must be on a CUDA device")
+        self.dev, self.shape, self.dtype = x.device, tuple(x.shape), _dtype(x, "x")
+        self.D = x.shape[-1] if x.dim() else 0
+        if cu_seqlens is None:
+            if x.dim() not in (3, 4):
+                raise ValueError("x must be [B, T, D] or [B, H, T, D]")
+            lead, self.T = self.shape[:-2], self.shape[-2]
+            self.cu, self.N, self.H = None, 0, x.shape[0] * (x.shape[1] if x.dim() == 4 else 1)
+            blocks = -(-self.T // _lib.SCAN_BLOCK)
+        else:
+            if x.dim() not in (2, 3):
+                raise ValueError("x must be [T_total, D] or [H, T_total, D]")
+            cu = [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else
+                                   cu_seqlens)]
+            if len(cu) < 2:
+                raise ValueError("cu_seqlens needs at least two entries")
+            self.T = self.shape[-2]
+            if cu[0] != 0 or cu[-1] != self.T or any(b < a for a, b in zip(cu, cu[1:])):
+                raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
+            self.cu, self.N, self.H = cu, len(cu) - 1, x.shape[0] if x.dim() == 3 else 1
+            lead = (self.N,) if x.dim() == 2 else (self.N, self.H)
+            blocks = sum(-(-(b - a) // _lib.SCAN_BLOCK) for a, b in zip(cu, cu[1:]))
+        self.state = lead + (self.D,)
+        if self.cu is None:
+            self.ckpt = lead + (blocks, self.D)
+        else:
+            self.ckpt = self.shape[:-2] + (blocks, self.D)
+
+    def sizes(self):
+        if self.cu is None:
+            return self.H, self.T, self.D, self.dtype, _stream(self.dev)
+        return ((ctypes.c_int * len(self.cu))(*self.cu), self.N, self.H, self.T, self.D,
+                self.dtype, _stream(self.dev))
+
+
+def _scan_fwd(x, log_alpha, cu_seqlens, h0, output_final_state, out, final_state, checkpoints,
+              write_h=True):
+    s = _Scan(x, cu_seqlens)
+    _need(x, "x", x.dtype, s.shape, s.dev)
+    _need(log_alpha, "log_alpha", torch.float32, s.shape, s.dev)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, s.state, s.dev)
+    if write_h and out is None:
+        out = torch.empty_like(x)
+    if out is not None:
+        _need(out, "out", x.dtype, s.shape, s.dev)
+    hT = None
+    if output_final_state:
+        hT = final_state if final_state is not None else torch.empty(
+            s.state, dtype=torch.float32, device=s.dev)
+        _need(hT, "final_state", torch.float32, s.state, s.dev)
+    if checkpoints is not None:
+        _need(checkpoints, "checkpoints", torch.float32, s.ckpt, s.dev)
+    name = "gla_scan_fwd" if cu_seqlens is None else "gla_scan_fwd_varlen"
+    with torch.cuda.device(s.dev):
+        st = getattr(_lib.lib(), name)(x.data_ptr(), log_alpha.data_ptr(), _ptr(h0), _ptr(out),
+                                       _ptr(hT), _ptr(checkpoints), *s.sizes())
+    _lib.check(st, name)
+    return out, hT
+
+
+def _scan_bwd(x, log_alpha, d_h, cu_seqlens, h0, dhT, checkpoints, need_dx, need_dlog_alpha,
+              need_dh0):
+    s = _Scan(x, cu_seqlens)
+    _need(x, "x", x.dtype, s.shape, s.dev)
+    _need(log_alpha, "log_alpha", torch.float32, s.shape, s.dev)
+    if d_h is not None:
+        _need(d_h, "d_h", x.dtype, s.shape, s.dev)
+    if dhT is not None:
+        _need(dhT, "dhT", torch.float32, s.state, s.dev)
+    if checkpoints is None:
+        checkpoints = torch.empty(s.ckpt, dtype=torch.float32, device=s.dev)
+        _scan_fwd(x, log_alpha, cu_seqlens, h0, False, None, None, checkpoints, write_h=False)
+    _need(checkpoints, "checkpoints", torch.float32, s.ckpt, s.dev)
+    dx = torch.empty_like(x) if need_dx else None
+    da = torch.empty_like(log_alpha) if need_dlog_alpha else None
+    dh0 = torch.empty(s.state, dtype=torch.float32, device=s.dev) if need_dh0 else None
+    name = "gla_scan_bwd" if cu_seqlens is None else "gla_scan_bwd_varlen"
+    with torch.cuda.device(s.dev):
+        st = getattr(_lib.lib(), name)(x.data_ptr(), log_alpha.data_ptr(), checkpoints.data_ptr(),
+                                       _ptr(d_h), _ptr(dhT), _ptr(dx), _ptr(da), _ptr(dh0),
+                                       *s.sizes())
+    _lib.check(st, name)
+    return dx, da, dh0
+
+
+def gla_scan_checkpoints(x: torch.Tensor, cu_seqlens=None) -> torch.Tensor:
+    """An empty buffer for the states that enter each block of 64 tokens (fp32).
+
+    ``gla_scan_fwd`` fills it and ``gla_scan_bwd`` reads it: ``[B, ceil(T/64), D]``
+    for ``x`` ``[B, T, D]`` (``[B, H, ceil(T/64), D]`` for four dimensions); for a
+    packed batch ``[sum of ceil(length/64), D]`` (``[H, ..., D]``).
+    """
+    s = _Scan(x, cu_seqlens)
+    return torch.empty(s.ckpt, dtype=torch.float32, device=s.dev)
+
+
+def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None,
+                 output_final_state: bool = True, *, out: torch.Tensor | None = None,
+                 final_state: torch.Tensor | None = None,
+                 checkpoints: torch.Tensor | None = None):
+    """The gated linear recurrence ``h_t = exp(log_alpha_t) h_{t-1} + x_t``, elementwise.
+
+    ``x`` ``[B, T, D]`` or ``[B, H, T, D]``, bf16 or fp32; ``log_alpha`` the same
+    shape in fp32, <= 0 (-inf is a gate of zero); ``h0`` ``[B, D]`` / ``[B, H, D]``
+    fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
+    fp32 on the way, and the last one in fp32 (None when ``output_final_state`` is
+    False).  ``final_state`` may be ``h0`` itself.  ``checkpoints`` (from
+    ``gla_scan_checkpoints``) is filled for ``gla_scan_bwd``.
+    """
+    return _scan_fwd(x, log_alpha, None, h0, output_final_state, out, final_state, checkpoints)
+
+
+def gla_scan_fwd_varlen(x: torch.Tensor, log_alpha: torch.Tensor, cu_seqlens,
+                        h0: torch.Tensor | None = None, output_final_state: bool = True, *,
+                        out: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+                        checkpoints: torch.Tensor | None = None):
+    """``gla_scan_fwd`` over a packed batch: ``x`` ``[T_total, D]`` or ``[H, T_total, D]``.
+
+    Sequence ``n`` holds rows ``cu_seqlens[n] : cu_seqlens[n+1]``; ``cu_seqlens`` is a
+    host sequence of ``N + 1`` ints (list, tuple or CPU tensor).  ``h0`` and ``hT``
+    are ``[N, D]`` / ``[N, H, D]``; an empty sequence keeps its state.
+    """
+    return _scan_fwd(x, log_alpha, cu_seqlens, h0, output_final_state, out, final_state,
+                     checkpoints)
+
+
+def gla_scan_bwd(x: torch.Tensor, log_alpha: torch.Tensor, d_h: torch.Tensor | None,
+                 h0: torch.Tensor | None = None, dhT: torch.Tensor | None = None, *,
+                 checkpoints: torch.Tensor | None = None, need_dx: bool = True,
+                 need_dlog_alpha: bool = True, need_dh0: bool = True):
+    """Gradients of ``sum <d_h, h> + <dhT, hT>`` through ``gla_scan_fwd``.
+
+    ``d_h`` is like ``x`` and ``dhT`` like ``h0`` (each None: zero).  Returns
+    ``(dx, dlog_alpha, dh0)``, in ``x``'s type, fp32 and fp32; each None when not
+    needed.  ``checkpoints`` are those that ``gla_scan_fwd`` filled for the same
+    ``x``, ``log_alpha`` and ``h0``; without them a pass over ``x`` recomputes them.
+    """
+    return _scan_bwd(x, log_alpha, d_h, None, h0, dhT, checkpoints, need_dx, need_dlog_alpha,
+                     need_dh0)
+
+
+def gla_scan_bwd_varlen(x: torch.Tensor, log_alpha: torch.Tensor, d_h: torch.Tensor | None,
+                        cu_seqlens, h0: torch.Tensor | None = None,
+                        dhT: torch.Tensor | None = None, *,
+                        checkpoints: torch.Tensor | None = None, need_dx: bool = True,
+                        need_dlog_alpha: bool = True, need_dh0: bool = True):
+    """``gla_scan_bwd`` over a packed batch (shapes of ``gla_scan_fwd_varlen``)."""
+    return _scan_bwd(x, log_alpha, d_h, cu_seqlens, h0, dhT, checkpoints, need_dx,
+                     need_dlog_alpha, need_dh0)
+
+
+class _GlaScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, log_alpha, h0, cu):
+        ctx.set_materialize_grads(False)
+        ckpt = gla_scan_checkpoints(x, cu) if any(ctx.needs_input_grad) else None
+        h, hT = _scan_fwd(x, log_alpha, cu, h0, True, None, None, ckpt)
+        ctx.save_for_backward(x, log_alpha, ckpt)
+        ctx.cu = cu
+        return h, hT
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_h, dhT):
+        x, log_alpha, ckpt = ctx.saved_tensors
+        if d_h is None and dhT is None:
+            return None, None, None, None
+        d_h = None if d_h is None else d_h.to(x.dtype).contiguous()
+        dhT = None if dhT is None else dhT.float().contiguous()
+        need = ctx.needs_input_grad
+        dx, da, dh0 = _scan_bwd(x, log_alpha, d_h, ctx.cu, None, dhT, ckpt, *need[:3])
+        return dx, da, dh0, None
+
+
+def gla_scan(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None):
+    """Differentiable ``gla_scan_fwd``: ``(h, hT)`` with gradients through ``gla_scan_bwd``."""
+    return _GlaScan.apply(x, log_alpha, h0, None)
+
+
+def gla_scan_varlen(x: torch.Tensor, log_alpha: torch.Tensor, cu_seqlens,
+                    h0: torch.Tensor | None = None):
+    """Differentiable ``gla_scan_fwd_varlen``."""
+    cu = [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else cu_seqlens)]
+    return _GlaScan.apply(x, log_alpha, h0, cu)
+
+
+def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """One decode token of ``gla_scan_fwd``: ``h`` is updated in place, returns it in ``x``'s type.
+
+    x ``[B, D]`` or ``[B, H, D]`` bf16 or fp32; log_alpha and h the same shape in fp32.
+    """
+    if not isinstance(h, torch.Tensor) or h.dim() not in (2, 3):
+        raise ValueError("h must be [B, D] or [B, H, D]")
+    dev, shape = h.device, tuple(h.shape)
+    if dev.type != "cuda":
+        raise ValueError("h must be on a CUDA device")
+    _need(h, "h", torch.float32, shape, dev)
+    dtype = _dtype(x, "x")
+    _need(x, "x", x.dtype, shape, dev)
+    _need(log_alpha, "log_alpha", torch.float32, shape, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype, shape, dev)
+    with torch.cuda.device(dev):
+        st = _lib.lib().gla_scan_step(x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(),
+                                      out.data_ptr(), h.numel() // shape[-1], shape[-1], dtype,
+                                      _stream(dev))
+    _lib.check(st, "gla_scan_step")
+    return out
+
+
+_NORMS = {"rms": _lib.GLA_NORM_RMS, "l2": _lib.GLA_NORM_L2}
+
+
+class _Qk:
+    """The checked sizes, strides and options of a gla_qk_norm_rope call."""
+
+    def __init__(self, q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+        for t, name in ((q, "q"), (k, "k")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.device.type != "cuda" or t.device != q.device:
+                raise ValueError(f"{name} must be on the CUDA device of q")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must be [B, T, H, d]")
+            if t.stride(-1) != 1:
+                raise ValueError(f"{name}'s last dimension must be contiguous")
+        dev, (B, T, Hq, d), Hk = q.device, q.shape, k.shape[2]
+        if k.dtype != q.dtype:
+            raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+        if tuple(k.shape) != (B, T, Hk, d):
+            raise ValueError(f"k must have shape {(B, T, Hk, d)}, got {tuple(k.shape)}")
+        if norm not in _NORMS:
+            raise ValueError("norm must be 'rms' or 'l2'")
+        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _need(w, name, torch.float32, (d,), dev)
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+        pos_sb = 0
+        if positions is not None:
+            if not isinstance(positions, torch.Tensor):
+                raise TypeError("positions must be a torch.Tensor")
+            one = positions.dim() == 1
+            _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
+            pos_sb = 0 if one else T
+        self.dev, self.q_shape, self.k_shape = dev, (B, T, Hq, d), (B, T, Hk, d)
+        self.dims = (B, T, Hq, Hk, d, rot)
+        # a dimension of one entry is never stepped over, whatever its stride says
+        steps = [0 if n == 1 else st for t in (q, k)
+                 for n, st in zip(t.shape[:3], t.stride()[:3])]
+        self.layout = _lib.GlaQkLayout(*steps, pos_sb)
+        self.options = _lib.GlaQkOptions(dtype=_dtype(q, "q"), norm=_NORMS[norm],
+                                         interleaved=1 if interleaved else 0, eps=float(eps))
+        self.pointers = (q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                         _ptr(positions), _ptr(inv_freq))
+        self.dtype = q.dtype
+
+    def heads_first(self, shape):
+        return shape[0], shape[2], shape[1], shape[3]
+
+    def sizes(self):
+        return (*self.dims, ctypes.byref(self.layout), ctypes.byref(self.options))
+
+
+def gla_rope_frequencies(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """``base^(-2i/rot)`` for ``i < rot/2``, fp64: the angles per position of each rotated pair."""
+    if rot <= 0 or rot % 8:
+        raise ValueError("rot must be a positive multiple of 8")
+    return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+
+
+def gla_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None = None,
+                         k_weight: torch.Tensor | None = None,
+                         positions: torch.Tensor | None = None,
+                         inv_freq: torch.Tensor | None = None, *, norm: str = "rms",
+                         eps: float = 1e-6, interleaved: bool = False):
+    """Norms of the query and key rows and their rotation by position, in one pass.
+
+    q ``[B, T, Hq, d]`` and k ``[B, T, Hk, d]``, bf16 or fp32, as a projection
+    leaves them: strided views with a contiguous last dimension are read in place
+    (strides in multiples of 8 elements, 16-byte aligned).  Returns
+    ``(q', k')``, ``[B, Hq, T, d]`` and ``[B, Hk, T, d]`` contiguous, as
+    ``gla_chunk`` and ``gla_gdn_fwd`` take them.
+
+    Each row is divided by its norm (``norm="rms"``: the root of its mean square,
+    ``"l2"``: its length; ``eps`` under the root), multiplied by its weight (``[d]``
+    fp32 or None) and, with ``inv_freq`` (fp64 ``[rot/2]``, see
+    ``gla_rope_frequencies``), the pairs of its first ``rot`` values are turned by
+    ``position * inv_freq``: pairs ``(i, i + rot/2)``, or ``(2i, 2i + 1)`` when
+    ``interleaved``.  ``positions`` is int64 ``[B, T]`` or ``[T]`` (None: 0 .. T-1).
+    d and rot are multiples of 8, up to 256.
+    """
+    s = _Qk(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
+    q_out = torch.empty(s.heads_first(s.q_shape), dtype=s.dtype, device=s.dev)
+    k_out = torch.empty(s.heads_first(s.k_shape), dtype=s.dtype, device=s.dev)
+    with torch.cuda.device(s.dev):
+        st = _lib.lib().gla_qk_norm_rope_fwd(*s.pointers, q_out.data_ptr(), k_out.data_ptr(),
+                                             *s.sizes(), _stream(s.dev))
+    _lib.check(st, "gla_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_k: torch.Tensor,
+                         q_weight: torch.Tensor | None = None,
+                         k_weight: torch.Tensor | None = None,
+                         positions: torch.Tensor | None = None,
+                         inv_freq: torch.Tensor | None = None, *, norm: str = "rms",
+                         eps: float = 1e-6, interleaved: bool = False,
+                         need_dweights: bool = True):
+    """Gradients of ``<d_q, q'> + <d_k, k'>`` through ``gla_qk_norm_rope_fwd``.
+
+    d_q, d_k are contiguous like q', k'.  Returns ``(dq, dk, dq_weight, dk_weight)``:
+    contiguous ``[B, T, H, d]`` in q's type, and fp32 ``[d]`` sums over every row
+    (None without a weight, or when not needed).
+    """
+    s = _Qk(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
+    _need(d_q, "d_q", s.dtype, s.heads_first(s.q_shape), s.dev)
+    _need(d_k, "d_k", s.dtype, s.heads_first(s.k_shape), s.dev)
+    dq = torch.empty(s.q_shape, dtype=s.dtype, device=s.dev)
+    dk = torch.empty(s.k_shape, dtype=s.dtype, device=s.dev)
+    dwq, dwk = (torch.empty_like(w) if w is not None and need_dweights else None
+                for w in (q_weight, k_weight))
+    scratch, size = None, 0
+    if dwq is not None or dwk is not None:
+        size = _lib.lib().gla_qk_norm_rope_bwd_scratch(s.dims[4])
+        scratch = torch.empty(size, dtype=torch.uint8, device=s.dev)
+    with torch.cuda.device(s.dev):
+        st = _lib.lib().gla_qk_norm_rope_bwd(*s.pointers, d_q.data_ptr(), d_k.data_ptr(),
+                                             dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk),
+                                             *s.sizes(), _ptr(scratch), size, _stream(s.dev))
+    _lib.check(st, "gla_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+class _GlaQkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, kw):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.kw = kw
+        return gla_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, **kw)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_q, d_k):
+        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
+        dq, dk, dwq, dwk = gla_qk_norm_rope_bwd(
+            q, k, d_q.to(q.dtype).contiguous(), d_k.to(q.dtype).contiguous(), wq, wk, positions,
+            inv_freq, need_dweights=any(ctx.needs_input_grad[2:4]), **ctx.kw)
+        return dq, dk, dwq, dwk, None, None, None
+
+
+def gla_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                     inv_freq: torch.Tensor | None = None, *, norm: str = "rms",
+                     eps: float = 1e-6, interleaved: bool = False):
+    """Differentiable ``gla_qk_norm_rope_fwd``: gradients of q, k and the weights."""
+    return _GlaQkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq,
+                                {"norm": norm, "eps": eps, "interleaved": interleaved})
 
 
 def gla_last_device_status(device: torch.device | int | None = None) -> int:

@@ -28,8 +28,20 @@ EXPORTED = ("gla_chunk_fwd", "gla_chunk_fwd_ex", "gla_chunk_fwd_plan", "gla_chun
             "gla_chunk_fwd_host", "gla_chunk_fwd_varlen", "gla_chunk_fwd_varlen_ex",
             "gla_chunk_fwd_varlen_plan", "gla_chunk_bwd", "gla_chunk_bwd_ex",
             "gla_chunk_bwd_plan", "gla_chunk_bwd_varlen", "gla_chunk_bwd_varlen_ex",
-            "gla_gdn_fwd", "gla_gdn_chunk_fwd", "gla_recurrent_step", "gla_status_string",
+            "gla_gdn_fwd", "gla_gdn_chunk_fwd", "gla_recurrent_step",
+            "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_varlen", "gla_scan_bwd_varlen",
+            "gla_scan_step", "gla_qk_norm_rope_fwd", "gla_qk_norm_rope_bwd",
+            "gla_qk_norm_rope_bwd_scratch", "gla_status_string",
             "gla_last_device_status", "gla_version")
+
+
+# Element types (enum gla_dtype) and norms (enum gla_norm).
+GLA_BF16 = 0
+GLA_F32 = 1
+GLA_NORM_RMS = 0
+GLA_NORM_L2 = 1
+# Tokens of one block of a scan's checkpoints (GLA_SCAN_BLOCK).
+SCAN_BLOCK = 64
 
 
 class GlaChunkOptions(ctypes.Structure):
@@ -42,6 +54,18 @@ class GlaChunkDebug(ctypes.Structure):
     """gla_chunk_debug (include/gla.h): test instrumentation of the chunked forward."""
     _fields_ = [("gamma", ctypes.c_void_p), ("block_len", ctypes.c_void_p),
                 ("wait_limit_us", ctypes.c_uint), ("withhold_v", ctypes.c_int)]
+
+
+class GlaQkLayout(ctypes.Structure):
+    """gla_qk_layout (include/gla.h): strides of q, k and the positions, in elements."""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("q_sb", "q_st", "q_sh", "k_sb", "k_st", "k_sh",
+                                                 "pos_sb")]
+
+
+class GlaQkOptions(ctypes.Structure):
+    """gla_qk_options (include/gla.h)."""
+    _fields_ = [("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("eps", ctypes.c_float)]
 
 
 class GlaError(RuntimeError):
@@ -100,6 +124,24 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gla_gdn_chunk_fwd.restype = i
     lib.gla_recurrent_step.argtypes = [vp, vp, vp, fp, f, fp, vp, i, i, i, i, vp]
     lib.gla_recurrent_step.restype = i
+    lib.gla_scan_fwd.argtypes = [vp, fp, fp, vp, fp, fp, i, i, i, i, vp]
+    lib.gla_scan_fwd.restype = i
+    lib.gla_scan_bwd.argtypes = [vp, fp, fp, vp, fp, vp, fp, fp, i, i, i, i, vp]
+    lib.gla_scan_bwd.restype = i
+    lib.gla_scan_fwd_varlen.argtypes = [vp, fp, fp, vp, fp, fp, ip, i, i, i, i, i, vp]
+    lib.gla_scan_fwd_varlen.restype = i
+    lib.gla_scan_bwd_varlen.argtypes = [vp, fp, fp, vp, fp, vp, fp, fp, ip, i, i, i, i, i, vp]
+    lib.gla_scan_bwd_varlen.restype = i
+    lib.gla_scan_step.argtypes = [vp, fp, fp, vp, i, i, i, vp]
+    lib.gla_scan_step.restype = i
+    qk = [i, i, i, i, i, i, ctypes.POINTER(GlaQkLayout), ctypes.POINTER(GlaQkOptions)]
+    lib.gla_qk_norm_rope_fwd.argtypes = [vp, vp, fp, fp, vp, vp, vp, vp] + qk + [vp]
+    lib.gla_qk_norm_rope_fwd.restype = i
+    lib.gla_qk_norm_rope_bwd.argtypes = ([vp, vp, fp, fp, vp, vp, vp, vp, vp, vp, fp, fp] + qk +
+                                         [vp, ctypes.c_ulong, vp])
+    lib.gla_qk_norm_rope_bwd.restype = i
+    lib.gla_qk_norm_rope_bwd_scratch.argtypes = [i]
+    lib.gla_qk_norm_rope_bwd_scratch.restype = ctypes.c_ulong
     lib.gla_status_string.argtypes = [i]
     lib.gla_status_string.restype = ctypes.c_char_p
     lib.gla_last_device_status.argtypes = [vp]

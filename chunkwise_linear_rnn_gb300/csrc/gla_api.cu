@@ -201,6 +201,13 @@ bool dv_ok(int dv) { return dv == 64 || dv == 128 || dv == 256; }
 
 }  // namespace
 
+int usable_device(int *sm_count) {
+    DeviceInfo *dev = nullptr;
+    const int st = current_device(&dev);
+    if (st == GLA_OK) *sm_count = dev->sm_count;
+    return st;
+}
+
 int chunk_fwd_with_scratch(const void *q, const void *k, const void *v, const float *log_alpha,
                            float scale, const float *h0, void *o, float *hT, int B, int H, int T,
                            int dk, int dv, const gla_chunk_options *opts, cudaStream_t stream,
@@ -479,13 +486,14 @@ int chunk_fwd_packed(const void *q, const void *k, const void *v, const float *l
 
 extern "C" {
 
-int gla_version(void) { return 100; }
+int gla_version(void) { return 200; }
 
 const char *gla_status_string(int status) {
     switch (status) {
         case GLA_OK: return "ok";
         case GLA_ERR_ARG: return "invalid argument (null pointer, non-positive size or misaligned pointer)";
-        case GLA_ERR_SHAPE: return "unsupported head dimensions (dk in {64,128}, dv in {64,128,256})";
+        case GLA_ERR_SHAPE: return "unsupported head dimensions (dk in {64,128}, dv in {64,128,256}; "
+                                    "gla_qk_norm_rope: d and rot multiples of 8, rot <= d <= 256)";
         case GLA_ERR_DEVICE: return "no usable CUDA device (this library needs an sm_103 GB300)";
         case GLA_ERR_LAUNCH: return "a CUDA call failed while enqueuing work";
         case GLA_ERR_TIMEOUT: return "a bounded device-side wait expired";

@@ -170,4 +170,7 @@ inline size_t gdn_chunk_scratch_bytes(long long BH, int T, int dk) {
 // Enqueues the WY pre-pass and the sequential chunk kernel; returns a cudaError_t value.
 int launch_gdn_chunk(const GdnChunkLaunch &p, cudaStream_t stream);
 
+// The current device's SM count when it is an sm_103; returns a GLA status.
+int usable_device(int *sm_count);
+
 }  // namespace gla

@@ -436,6 +436,150 @@ int gla_gdn_chunk_fwd(const void *q, const void *k, const void *v, const float *
                       const float *beta, float scale, const float *h0, void *o, float *hT, int B,
                       int H, int T, int dk, int dv, cudaStream_t stream);
 
+/* Element types of the calls that take more than one (gla_scan_*, gla_qk_norm_rope_*). */
+enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
+
+/*
+ * gla_scan_* — the gated linear recurrence of one state value per channel,
+ *     h_t = exp(log_alpha_t) h_{t-1} + x_t        (elementwise over D channels),
+ * the elementwise relative of the recurrence above (the GLA page's "The Gated
+ * Recurrent Update"): a gate and a state value for each channel, no keys or
+ * queries.
+ *
+ *   x, h        : [B, T, D] dtype (GLA_BF16 or GLA_F32); B counts every leading
+ *                 dimension, so [B, H, T, d] is B * H sequences of d channels
+ *   log_alpha   : [B, T, D] fp32, <= 0; -infinity is a gate of 0 and cuts the
+ *                 sequence (h_t = x_t while h_{t-1} is finite)
+ *   h0, hT      : [B, D] fp32 (nullable; zero initial state / not written);
+ *                 hT may alias h0
+ *   checkpoints : [B, ceil(T / GLA_SCAN_BLOCK), D] fp32, the state that enters
+ *                 each block of GLA_SCAN_BLOCK tokens (entry 0 is h0); written
+ *                 by the forward when not NULL, read by the backward
+ *
+ * h is kept in fp32 from the first token to the last, and each h_t is rounded
+ * once to dtype as it is stored.  The results do not depend on the order in
+ * which the GPU runs the work: equal calls give equal bits.  No scratch, no
+ * atomics.  h may be NULL when checkpoints or hT is asked for.  No other output
+ * may overlap an input.
+ *
+ * Any D >= 1 and T >= 1, pointers aligned to their elements.  With D a multiple
+ * of 4 and every pointer at a multiple of 16 bytes, 4 channels are taken at a
+ * time; other calls take one and are slower.  Returns GLA_ERR_ARG for null
+ * required pointers, non-positive sizes, an unknown dtype, misaligned pointers
+ * or more than 2^31 thread blocks of work.
+ */
+#define GLA_SCAN_BLOCK 64
+int gla_scan_fwd(const void *x, const float *log_alpha, const float *h0, void *h, float *hT,
+                 float *checkpoints, int B, int T, int D, int dtype, cudaStream_t stream);
+
+/*
+ * gla_scan_bwd — gradients of L = sum <d_h, h> + <dhT, hT>:
+ *     g_t = d_h_t + alpha_{t+1} g_{t+1},  g_T = d_h_T + dhT,
+ *     grad_x_t = g_t,  grad_log_alpha_t = alpha_t g_t h_{t-1},  grad_h0 = alpha_1 g_1.
+ * d_h [B, T, D] dtype and dhT [B, D] fp32 are nullable (zero); grad_x (dtype),
+ * grad_log_alpha (fp32) and grad_h0 (fp32) are nullable (not written).  The
+ * h_{t-1} are recomputed in fp32 from `checkpoints`, which gla_scan_fwd wrote
+ * for the same x, log_alpha and h0 (call it with h and hT NULL where the forward
+ * kept none).  Errors as for gla_scan_fwd.
+ */
+int gla_scan_bwd(const void *x, const float *log_alpha, const float *checkpoints, const void *d_h,
+                 const float *dhT, void *grad_x, float *grad_log_alpha, float *grad_h0, int B,
+                 int T, int D, int dtype, cudaStream_t stream);
+
+/*
+ * gla_scan_fwd / gla_scan_bwd over a packed batch of N sequences of different
+ * lengths: x, h, log_alpha, d_h and their gradients are [H, T_total, D];
+ * sequence n holds rows cu_seqlens[n] : cu_seqlens[n+1] of every head; h0, hT,
+ * dhT and grad_h0 are [N, H, D]; checkpoints is [H, sum of ceil(length /
+ * GLA_SCAN_BLOCK), D], the sequences' blocks one after another.  cu_seqlens is a
+ * HOST array of N + 1 ints from 0 to T_total, nondecreasing, read during the call
+ * only (a captured call keeps its lengths).  An empty sequence has hT = h0 and
+ * grad_h0 = dhT (zero without them).
+ */
+int gla_scan_fwd_varlen(const void *x, const float *log_alpha, const float *h0, void *h,
+                        float *hT, float *checkpoints, const int *cu_seqlens, int N, int H,
+                        int T_total, int D, int dtype, cudaStream_t stream);
+int gla_scan_bwd_varlen(const void *x, const float *log_alpha, const float *checkpoints,
+                        const void *d_h, const float *dhT, void *grad_x, float *grad_log_alpha,
+                        float *grad_h0, const int *cu_seqlens, int N, int H, int T_total, int D,
+                        int dtype, cudaStream_t stream);
+
+/*
+ * gla_scan_step — one decode token of gla_scan_fwd for B streams: h (fp32
+ * [B, D]) becomes exp(log_alpha) h + x in place, and out ([B, D] dtype)
+ * receives it rounded.  x [B, D] dtype, log_alpha [B, D] fp32.
+ */
+int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, int B, int D,
+                  int dtype, cudaStream_t stream);
+
+/*
+ * gla_qk_norm_rope_* — what stands before every call above: the rows of q and k
+ * (one per token and head) divided by their norms, weighted, and rotated by
+ * position, in one pass that also turns the token-major layout of a projection
+ * into the head-first layout of this library:
+ *     y = R_p(w * x * r),   r = 1 / sqrt(sum_i x_i^2 / n + eps),
+ * with n = d (norm GLA_NORM_RMS) or n = 1 (GLA_NORM_L2: the unit keys of the
+ * gated delta rule, FlashQLA page, "Core Technical Principles").  R_p turns the
+ * pairs of the first `rot` values by the angles p * inv_freq[i], i < rot / 2:
+ * (u, v) -> (u cos - v sin, u sin + v cos), the pairs being (i, i + rot/2), or
+ * (2i, 2i + 1) when `interleaved`.  The angle is
+ * reduced in 64-bit integers: it is off by at most |p| 2^-63 + 2^-25 turns, so
+ * far positions keep the accuracy of near ones.
+ *
+ *   q, k       : [B, T, Hq, d] and [B, T, Hk, d] dtype, read through the strides
+ *                of `layout` (in elements; the last dimension is contiguous), so
+ *                that slices of a fused projection and transposed head-first
+ *                tensors are read in place
+ *   wq, wk     : [d] fp32, nullable (no weight)
+ *   positions  : int64 [B, T] (row stride layout->pos_sb, 0 for one row of T
+ *                shared by the batch), nullable: 0 .. T-1
+ *   inv_freq   : fp64 [rot / 2], device, nullable when rot = 0
+ *   q_out,k_out: [B, Hq, T, d] and [B, Hk, T, d] dtype, contiguous
+ *
+ * Sums and rotations are fp32; each value is rounded once.  d a multiple of 8 up
+ * to 256, rot a multiple of 8 up to d (GLA_ERR_SHAPE otherwise).  GLA_ERR_ARG for
+ * null required pointers, non-positive sizes, eps not in (0, 1], unknown dtype,
+ * norm or interleaved, strides that are negative or not multiples of 8 elements,
+ * inputs or outputs that are not 16-byte aligned (positions and inv_freq: 8).
+ * No output may overlap an input.
+ */
+enum gla_norm { GLA_NORM_RMS = 0, GLA_NORM_L2 = 1 };
+typedef struct gla_qk_layout {
+    long long q_sb, q_st, q_sh;   /* strides of q over batch, token, head */
+    long long k_sb, k_st, k_sh;   /* strides of k                         */
+    long long pos_sb;             /* stride of positions over the batch   */
+} gla_qk_layout;
+typedef struct gla_qk_options {
+    int dtype;         /* GLA_BF16 or GLA_F32                     */
+    int norm;          /* GLA_NORM_RMS or GLA_NORM_L2             */
+    int interleaved;   /* pairs (2i, 2i + 1) instead of halves    */
+    float eps;
+} gla_qk_options;
+int gla_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const float *wk,
+                         const long long *positions, const double *inv_freq, void *q_out,
+                         void *k_out, int B, int T, int Hq, int Hk, int d, int rot,
+                         const gla_qk_layout *layout, const gla_qk_options *options,
+                         cudaStream_t stream);
+
+/*
+ * gla_qk_norm_rope_bwd — gradients of L = <d_q, q_out> + <d_k, k_out>.  q, k, wq,
+ * wk, positions, inv_freq as in the forward (norms recomputed); d_q, d_k are
+ * contiguous like q_out, k_out; grad_q, grad_k are contiguous [B, T, H, d] dtype;
+ * grad_wq, grad_wk are [d] fp32 (NULL with wq, wk NULL).  With weights,
+ * `scratch` holds gla_qk_norm_rope_bwd_scratch(d) bytes of device memory,
+ * 16-byte aligned, for the weight gradients' partial sums (GLA_ERR_SCRATCH
+ * when scratch_bytes is smaller): each thread block sums its rows in a fixed
+ * order, and a second kernel adds the blocks', so equal calls give equal bits.
+ * Two calls that may run at the same time need scratch of their own.
+ */
+unsigned long gla_qk_norm_rope_bwd_scratch(int d);
+int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk,
+                         const long long *positions, const double *inv_freq, const void *d_q,
+                         const void *d_k, void *grad_q, void *grad_k, float *grad_wq,
+                         float *grad_wk, int B, int T, int Hq, int Hk, int d, int rot,
+                         const gla_qk_layout *layout, const gla_qk_options *options,
+                         void *scratch, unsigned long scratch_bytes, cudaStream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *gla_status_string(int status);
 

@@ -1,0 +1,183 @@
+"""Host-side checks of gla_scan_* and gla_qk_norm_rope_* that need no GPU: arguments are refused
+with the documented status before any CUDA call."""
+
+from __future__ import annotations
+
+import ctypes
+import re
+
+import pytest
+import torch
+
+import chunkwise_linear_rnn_gb300 as gla
+from chunkwise_linear_rnn_gb300 import _lib
+from chunkwise_linear_rnn_gb300.build import build
+from test_library_cpu import HEADER, P
+
+NO_GPU = not torch.cuda.is_available()
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return _lib.lib()
+
+
+def _cu(*xs):
+    return (ctypes.c_int * len(xs))(*xs)
+
+
+def _fwd(lib, **kw):
+    a = dict(x=P, la=P, h0=None, h=P, hT=None, ck=None, B=2, T=16, D=8, dtype=_lib.GLA_BF16)
+    a.update(kw)
+    return lib.gla_scan_fwd(a["x"], a["la"], a["h0"], a["h"], a["hT"], a["ck"], a["B"], a["T"],
+                            a["D"], a["dtype"], None)
+
+
+def _bwd(lib, **kw):
+    a = dict(x=P, la=P, ck=P, d=P, dT=None, dx=P, da=P, dh0=None, B=2, T=16, D=8,
+             dtype=_lib.GLA_F32)
+    a.update(kw)
+    return lib.gla_scan_bwd(a["x"], a["la"], a["ck"], a["d"], a["dT"], a["dx"], a["da"], a["dh0"],
+                            a["B"], a["T"], a["D"], a["dtype"], None)
+
+
+BAD_SIZES = [dict(B=0), dict(T=0), dict(D=0), dict(T=-1), dict(dtype=2), dict(dtype=-1),
+             dict(B=2 ** 30, D=2 ** 20)]
+
+
+@pytest.mark.parametrize("bad", BAD_SIZES + [dict(x=None), dict(la=None), dict(h=None),
+                                             dict(x=P + 1), dict(la=P + 2), dict(hT=P + 2),
+                                             dict(ck=P + 1), dict(h0=P + 3)])
+def test_scan_forward_refuses(lib, bad):
+    assert _fwd(lib, **bad) == _lib.GLA_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", BAD_SIZES + [dict(x=None), dict(la=None), dict(ck=None),
+                                             dict(dx=None, da=None), dict(x=P + 2),
+                                             dict(d=P + 2), dict(dT=P + 2), dict(dh0=P + 1)])
+def test_scan_backward_refuses(lib, bad):
+    assert _bwd(lib, **bad) == _lib.GLA_ERR_ARG
+
+
+@pytest.mark.parametrize("cu,N,T", [(_cu(0, 5, 15), 2, 16), (_cu(1, 5, 16), 2, 16),
+                                    (_cu(0, 9, 5, 16), 3, 16), (None, 2, 16), (_cu(0, 16), 0, 16),
+                                    (_cu(0, -1), 1, -1)])
+def test_packed_scans_refuse(lib, cu, N, T):
+    assert lib.gla_scan_fwd_varlen(P, P, None, P, None, None, cu, N, 1, T, 8, 0,
+                                   None) == _lib.GLA_ERR_ARG
+    assert lib.gla_scan_bwd_varlen(P, P, P, P, None, P, P, None, cu, N, 1, T, 8, 0,
+                                   None) == _lib.GLA_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", [dict(x=None), dict(la=None), dict(h=None), dict(out=None),
+                                 dict(B=0), dict(D=0), dict(dtype=7), dict(x=P + 1),
+                                 dict(h=P + 2)])
+def test_scan_step_refuses(lib, bad):
+    a = dict(x=P, la=P, h=P, out=P, B=2, D=8, dtype=0)
+    a.update(bad)
+    assert lib.gla_scan_step(a["x"], a["la"], a["h"], a["out"], a["B"], a["D"], a["dtype"],
+                             None) == _lib.GLA_ERR_ARG
+
+
+QK = dict(q=P, k=P, wq=P, wk=P, pos=P, f=P, qo=P, ko=P, B=1, T=4, Hq=2, Hk=2, d=64, rot=64,
+          lay=(64, 128, 64, 64, 128, 64, 4), opt=(0, 0, 0, 1e-6))
+
+
+def _qk(lib, **kw):
+    a = dict(QK, **kw)
+    lay = a["lay"] and ctypes.byref(_lib.GlaQkLayout(*a["lay"]))
+    opt = a["opt"] and ctypes.byref(_lib.GlaQkOptions(*a["opt"]))
+    return lib.gla_qk_norm_rope_fwd(a["q"], a["k"], a["wq"], a["wk"], a["pos"], a["f"], a["qo"],
+                                    a["ko"], a["B"], a["T"], a["Hq"], a["Hk"], a["d"], a["rot"],
+                                    lay, opt, None)
+
+
+def _qk_bwd(lib, **kw):
+    a = dict(QK, dqo=P, dko=P, dwq=P, dwk=P, scratch=P, size=None)
+    a.update(kw)
+    lay = ctypes.byref(_lib.GlaQkLayout(*a["lay"]))
+    opt = ctypes.byref(_lib.GlaQkOptions(*a["opt"]))
+    size = lib.gla_qk_norm_rope_bwd_scratch(a["d"]) if a["size"] is None else a["size"]
+    return lib.gla_qk_norm_rope_bwd(a["q"], a["k"], a["wq"], a["wk"], a["pos"], a["f"], a["dqo"],
+                                    a["dko"], a["qo"], a["ko"], a["dwq"], a["dwk"], a["B"], a["T"],
+                                    a["Hq"], a["Hk"], a["d"], a["rot"], lay, opt, a["scratch"],
+                                    size, None)
+
+
+BAD_QK = [dict(q=None), dict(k=None), dict(qo=None), dict(ko=None), dict(f=None), dict(B=0),
+          dict(T=0), dict(Hq=0), dict(Hk=0), dict(d=0), dict(rot=-8), dict(q=P + 8),
+          dict(qo=P + 2), dict(wq=P + 4), dict(pos=P + 4), dict(f=P + 4),
+          dict(lay=(64, 130, 64, 64, 128, 64, 4)), dict(lay=(64, 128, -64, 64, 128, 64, 4)),
+          dict(lay=(64, 128, 64, 64, 128, 64, -4)), dict(opt=(2, 0, 0, 1e-6)),
+          dict(opt=(0, 2, 0, 1e-6)), dict(opt=(0, 0, 2, 1e-6)), dict(opt=(0, 0, 0, 0.0)),
+          dict(opt=(0, 0, 0, float("nan"))), dict(opt=(0, 0, 0, 2.0))]
+SHAPES_QK = [dict(d=60, rot=0), dict(d=264, rot=8), dict(rot=12), dict(rot=72)]
+
+
+@pytest.mark.parametrize("bad", BAD_QK)
+def test_norm_and_rotation_refuse(lib, bad):
+    assert _qk(lib, **bad) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, **bad) == _lib.GLA_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", SHAPES_QK)
+def test_norm_and_rotation_refuse_shapes(lib, bad):
+    assert _qk(lib, **bad) == _lib.GLA_ERR_SHAPE
+    assert _qk_bwd(lib, **bad) == _lib.GLA_ERR_SHAPE
+
+
+def test_norm_and_rotation_refuse_missing_structs_and_scratch(lib):
+    assert _qk(lib, lay=None) == _lib.GLA_ERR_ARG
+    assert _qk(lib, opt=None) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, dqo=None) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, wq=None) == _lib.GLA_ERR_ARG      # a gradient of no weight
+    assert _qk_bwd(lib, scratch=None) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, scratch=P + 4) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, size=lib.gla_qk_norm_rope_bwd_scratch(64) - 1) == _lib.GLA_ERR_SCRATCH
+    assert lib.gla_qk_norm_rope_bwd_scratch(0) == 0
+
+
+@pytest.mark.skipif(not NO_GPU, reason="a GPU is present")
+def test_valid_arguments_reach_the_device_check(lib):
+    for call in (_fwd(lib), _fwd(lib, h=None, ck=P), _fwd(lib, x=P + 2, la=P + 4), _bwd(lib),
+                 _bwd(lib, d=None, dx=None), _qk(lib), _qk(lib, rot=0, f=None, pos=None, wq=None),
+                 _qk_bwd(lib), _qk_bwd(lib, dwq=None, dwk=None, scratch=None, size=0),
+                 lib.gla_scan_step(P, P, P, P, 2, 8, 1, None),
+                 lib.gla_scan_fwd_varlen(None, None, P, None, P, None, _cu(0, 0), 1, 1, 0, 8, 0,
+                                         None)):
+        assert call == _lib.GLA_ERR_DEVICE
+
+
+def test_structs_and_constants_match_the_header():
+    text = open(HEADER).read()
+    for name, struct in (("gla_qk_layout", _lib.GlaQkLayout), ("gla_qk_options",
+                                                              _lib.GlaQkOptions)):
+        body = text[text.index("typedef struct " + name):text.index("} %s;" % name)]
+        body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+        fields = [f.strip() for line in re.findall(r"(?:long long|int|float)\s+([\w, ]+);", body)
+                  for f in line.split(",")]
+        assert fields == [n for n, _ in struct._fields_]
+    assert int(re.search(r"#define GLA_SCAN_BLOCK (\d+)", text).group(1)) == _lib.SCAN_BLOCK
+
+
+def test_python_calls_refuse_cpu_tensors():
+    x = torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError):
+        gla.gla_scan_fwd(x, x)
+    with pytest.raises(ValueError):
+        gla.gla_scan_step(x[0], x[0], x[0])
+    q = torch.zeros(1, 4, 2, 64)
+    with pytest.raises(ValueError):
+        gla.gla_qk_norm_rope_fwd(q, q)
+    with pytest.raises(TypeError):
+        gla.gla_scan_fwd(None, x)
+    with pytest.raises(ValueError):
+        gla.gla_rope_frequencies(12)
+
+
+def test_frequencies():
+    f = gla.gla_rope_frequencies(16, 100.0)
+    want = [100.0 ** (-i / 8) for i in range(8)]
+    assert f.dtype == torch.float64
+    torch.testing.assert_close(f, torch.tensor(want, dtype=torch.float64), rtol=1e-14, atol=0)
