@@ -132,7 +132,10 @@ def test_checkpoints_are_the_states_that_enter_each_block():
     h, _ = gla.gla_scan_fwd(x, la, h0, checkpoints=ck)
     assert ck.shape == (2, 5, 36)
     assert torch.equal(ck[:, 0], h0)
-    assert torch.equal(ck[:, 1:], h[:, 63:256:64])
+    # a block's state may be joined from products of gates where h was walked token
+    # by token: each is within the bound of the definition
+    want, bound = (f(num(x), num(la), num(h0))[:, 63:256:64] for f in (ref.scan, ref.scan_bound))
+    ref.assert_within(ck[:, 1:], want, bound, "checkpoints")
     alone = torch.empty_like(ck)
     gla._scan_fwd(x, la, None, h0, False, None, None, alone, write_h=False)
     assert torch.equal(ck, alone)
