@@ -40,8 +40,22 @@ def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _call(name: str, device: torch.device, *args) -> None:
+    """A C entry point on the current stream of `device`; raises GlaError on a bad status."""
+    fn = getattr(_lib.lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    _lib.check(st, name)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> None:
     """Checks a tensor argument; `device` is a CUDA device, or the CPU for host entry points."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if device is not None and device.type == "cpu":
@@ -501,101 +515,89 @@ _DTYPES = {torch.bfloat16: _lib.GLA_BF16, torch.float32: _lib.GLA_F32}
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return _DTYPES[t.dtype]
+    dtype = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if dtype is None:
+        raise TypeError(f"{name} must be a torch.bfloat16 or torch.float32 tensor")
+    return dtype
 
 
-class _Scan:
-    """The sizes of a scan call, from x and (packed) the sequences' bounds."""
-
-    def __init__(self, x: torch.Tensor, cu_seqlens=None):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("x must be a torch.Tensor")
-        if x.device.type != "cuda":
-            raise ValueError("x must be on a CUDA device")
-        self.dev, self.shape, self.dtype = x.device, tuple(x.shape), _dtype(x, "x")
-        self.D = x.shape[-1] if x.dim() else 0
-        if cu_seqlens is None:
-            if x.dim() not in (3, 4):
-                raise ValueError("x must be [B, T, D] or [B, H, T, D]")
-            lead, self.T = self.shape[:-2], self.shape[-2]
-            self.cu, self.N, self.H = None, 0, x.shape[0] * (x.shape[1] if x.dim() == 4 else 1)
-            blocks = -(-self.T // _lib.SCAN_BLOCK)
-        else:
-            if x.dim() not in (2, 3):
-                raise ValueError("x must be [T_total, D] or [H, T_total, D]")
-            cu = [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else
-                                   cu_seqlens)]
-            if len(cu) < 2:
-                raise ValueError("cu_seqlens needs at least two entries")
-            self.T = self.shape[-2]
-            if cu[0] != 0 or cu[-1] != self.T or any(b < a for a, b in zip(cu, cu[1:])):
-                raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
-            self.cu, self.N, self.H = cu, len(cu) - 1, x.shape[0] if x.dim() == 3 else 1
-            lead = (self.N,) if x.dim() == 2 else (self.N, self.H)
-            blocks = sum(-(-(b - a) // _lib.SCAN_BLOCK) for a, b in zip(cu, cu[1:]))
-        self.state = lead + (self.D,)
-        if self.cu is None:
-            self.ckpt = lead + (blocks, self.D)
-        else:
-            self.ckpt = self.shape[:-2] + (blocks, self.D)
-
-    def sizes(self):
-        if self.cu is None:
-            return self.H, self.T, self.D, self.dtype, _stream(self.dev)
-        return ((ctypes.c_int * len(self.cu))(*self.cu), self.N, self.H, self.T, self.D,
-                self.dtype, _stream(self.dev))
+def _bounds(cu_seqlens) -> list:
+    """The bounds of a packed batch as ints."""
+    return [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else cu_seqlens)]
 
 
-def _scan_fwd(x, log_alpha, cu_seqlens, h0, output_final_state, out, final_state, checkpoints,
-              write_h=True):
-    s = _Scan(x, cu_seqlens)
-    _need(x, "x", x.dtype, s.shape, s.dev)
-    _need(log_alpha, "log_alpha", torch.float32, s.shape, s.dev)
+def _scan_sizes(x: torch.Tensor, cu):
+    """(shape of a state, shape of the checkpoints, the C call's sizes) of a scan over `x`."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be on a CUDA device")
+    shape, dtype = x.shape, _dtype(x, "x")
+    if cu is None:
+        if len(shape) not in (3, 4):
+            raise ValueError("x must be [B, T, D] or [B, H, T, D]")
+        lead, T, D = shape[:-2], shape[-2], shape[-1]
+        H = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+        return (*lead, D), (*lead, -(-T // _lib.SCAN_BLOCK), D), (H, T, D, dtype)
+    if len(shape) not in (2, 3):
+        raise ValueError("x must be [T_total, D] or [H, T_total, D]")
+    T, D, N = shape[-2], shape[-1], len(cu) - 1
+    if N < 1:
+        raise ValueError("cu_seqlens needs at least two entries")
+    if cu[0] != 0 or cu[-1] != T or any(b < a for a, b in zip(cu, cu[1:])):
+        raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
+    lead = shape[:-2]
+    blocks = sum(-(-(b - a) // _lib.SCAN_BLOCK) for a, b in zip(cu, cu[1:]))
+    sizes = ((ctypes.c_int * len(cu))(*cu), N, lead[0] if lead else 1, T, D, dtype)
+    return (N, *lead, D), (*lead, blocks, D), sizes
+
+
+def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkpoints,
+              write_h=True, with_checkpoints=False):
+    state, ckpt, sizes = _scan_sizes(x, cu)
+    dev = x.device
+    _need(x, "x", x.dtype, x.shape, dev)
+    _need(log_alpha, "log_alpha", torch.float32, x.shape, dev)
     if h0 is not None:
-        _need(h0, "h0", torch.float32, s.state, s.dev)
-    if write_h and out is None:
-        out = torch.empty_like(x)
+        _need(h0, "h0", torch.float32, state, dev)
     if out is not None:
-        _need(out, "out", x.dtype, s.shape, s.dev)
-    hT = None
-    if output_final_state:
-        hT = final_state if final_state is not None else torch.empty(
-            s.state, dtype=torch.float32, device=s.dev)
-        _need(hT, "final_state", torch.float32, s.state, s.dev)
-    if checkpoints is not None:
-        _need(checkpoints, "checkpoints", torch.float32, s.ckpt, s.dev)
-    name = "gla_scan_fwd" if cu_seqlens is None else "gla_scan_fwd_varlen"
-    with torch.cuda.device(s.dev):
-        st = getattr(_lib.lib(), name)(x.data_ptr(), log_alpha.data_ptr(), _ptr(h0), _ptr(out),
-                                       _ptr(hT), _ptr(checkpoints), *s.sizes())
-    _lib.check(st, name)
-    return out, hT
+        _need(out, "out", x.dtype, x.shape, dev)
+    elif write_h:
+        out = torch.empty_like(x)
+    hT = final_state if output_final_state else None
+    if hT is not None:
+        _need(hT, "final_state", torch.float32, state, dev)
+    elif output_final_state:
+        hT = torch.empty(state, dtype=torch.float32, device=dev)
+    if with_checkpoints:
+        checkpoints = torch.empty(ckpt, dtype=torch.float32, device=dev)
+    elif checkpoints is not None:
+        _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
+    _call("gla_scan_fwd" if cu is None else "gla_scan_fwd_varlen", dev, x.data_ptr(),
+          log_alpha.data_ptr(), _ptr(h0), _ptr(out), _ptr(hT), _ptr(checkpoints), *sizes)
+    return (out, hT, checkpoints) if with_checkpoints else (out, hT)
 
 
-def _scan_bwd(x, log_alpha, d_h, cu_seqlens, h0, dhT, checkpoints, need_dx, need_dlog_alpha,
-              need_dh0):
-    s = _Scan(x, cu_seqlens)
-    _need(x, "x", x.dtype, s.shape, s.dev)
-    _need(log_alpha, "log_alpha", torch.float32, s.shape, s.dev)
+def _scan_bwd(x, log_alpha, d_h, cu, h0, dhT, checkpoints, need_dx, need_dlog_alpha, need_dh0):
+    state, ckpt, sizes = _scan_sizes(x, cu)
+    dev = x.device
+    _need(x, "x", x.dtype, x.shape, dev)
+    _need(log_alpha, "log_alpha", torch.float32, x.shape, dev)
     if d_h is not None:
-        _need(d_h, "d_h", x.dtype, s.shape, s.dev)
+        _need(d_h, "d_h", x.dtype, x.shape, dev)
     if dhT is not None:
-        _need(dhT, "dhT", torch.float32, s.state, s.dev)
+        _need(dhT, "dhT", torch.float32, state, dev)
     if checkpoints is None:
-        checkpoints = torch.empty(s.ckpt, dtype=torch.float32, device=s.dev)
-        _scan_fwd(x, log_alpha, cu_seqlens, h0, False, None, None, checkpoints, write_h=False)
-    _need(checkpoints, "checkpoints", torch.float32, s.ckpt, s.dev)
+        checkpoints = _scan_fwd(x, log_alpha, cu, h0, False, None, None, None, False, True)[2]
+    else:
+        _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
     dx = torch.empty_like(x) if need_dx else None
     da = torch.empty_like(log_alpha) if need_dlog_alpha else None
-    dh0 = torch.empty(s.state, dtype=torch.float32, device=s.dev) if need_dh0 else None
-    name = "gla_scan_bwd" if cu_seqlens is None else "gla_scan_bwd_varlen"
-    with torch.cuda.device(s.dev):
-        st = getattr(_lib.lib(), name)(x.data_ptr(), log_alpha.data_ptr(), checkpoints.data_ptr(),
-                                       _ptr(d_h), _ptr(dhT), _ptr(dx), _ptr(da), _ptr(dh0),
-                                       *s.sizes())
-    _lib.check(st, name)
+    dh0 = torch.empty(state, dtype=torch.float32, device=dev) if need_dh0 else None
+    if need_dx or need_dlog_alpha or need_dh0:
+        _call("gla_scan_bwd" if cu is None else "gla_scan_bwd_varlen", dev, x.data_ptr(),
+              log_alpha.data_ptr(), checkpoints.data_ptr(), _ptr(d_h), _ptr(dhT), _ptr(dx),
+              _ptr(da), _ptr(dh0), *sizes)
     return dx, da, dh0
 
 
@@ -606,8 +608,8 @@ def gla_scan_checkpoints(x: torch.Tensor, cu_seqlens=None) -> torch.Tensor:
     for ``x`` ``[B, T, D]`` (``[B, H, ceil(T/64), D]`` for four dimensions); for a
     packed batch ``[sum of ceil(length/64), D]`` (``[H, ..., D]``).
     """
-    s = _Scan(x, cu_seqlens)
-    return torch.empty(s.ckpt, dtype=torch.float32, device=s.dev)
+    shape = _scan_sizes(x, None if cu_seqlens is None else _bounds(cu_seqlens))[1]
+    return torch.empty(shape, dtype=torch.float32, device=x.device)
 
 
 def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None,
@@ -636,7 +638,7 @@ def gla_scan_fwd_varlen(x: torch.Tensor, log_alpha: torch.Tensor, cu_seqlens,
     host sequence of ``N + 1`` ints (list, tuple or CPU tensor).  ``h0`` and ``hT``
     are ``[N, D]`` / ``[N, H, D]``; an empty sequence keeps its state.
     """
-    return _scan_fwd(x, log_alpha, cu_seqlens, h0, output_final_state, out, final_state,
+    return _scan_fwd(x, log_alpha, _bounds(cu_seqlens), h0, output_final_state, out, final_state,
                      checkpoints)
 
 
@@ -661,7 +663,7 @@ def gla_scan_bwd_varlen(x: torch.Tensor, log_alpha: torch.Tensor, d_h: torch.Ten
                         checkpoints: torch.Tensor | None = None, need_dx: bool = True,
                         need_dlog_alpha: bool = True, need_dh0: bool = True):
     """``gla_scan_bwd`` over a packed batch (shapes of ``gla_scan_fwd_varlen``)."""
-    return _scan_bwd(x, log_alpha, d_h, cu_seqlens, h0, dhT, checkpoints, need_dx,
+    return _scan_bwd(x, log_alpha, d_h, _bounds(cu_seqlens), h0, dhT, checkpoints, need_dx,
                      need_dlog_alpha, need_dh0)
 
 
@@ -669,8 +671,8 @@ class _GlaScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, log_alpha, h0, cu):
         ctx.set_materialize_grads(False)
-        ckpt = gla_scan_checkpoints(x, cu) if any(ctx.needs_input_grad) else None
-        h, hT = _scan_fwd(x, log_alpha, cu, h0, True, None, None, ckpt)
+        h, hT, ckpt = _scan_fwd(x, log_alpha, cu, h0, True, None, None, None,
+                                with_checkpoints=True)
         ctx.save_for_backward(x, log_alpha, ckpt)
         ctx.cu = cu
         return h, hT
@@ -683,9 +685,8 @@ class _GlaScan(torch.autograd.Function):
             return None, None, None, None
         d_h = None if d_h is None else d_h.to(x.dtype).contiguous()
         dhT = None if dhT is None else dhT.float().contiguous()
-        need = ctx.needs_input_grad
-        dx, da, dh0 = _scan_bwd(x, log_alpha, d_h, ctx.cu, None, dhT, ckpt, *need[:3])
-        return dx, da, dh0, None
+        return *_scan_bwd(x, log_alpha, d_h, ctx.cu, None, dhT, ckpt,
+                          *ctx.needs_input_grad[:3]), None
 
 
 def gla_scan(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None):
@@ -696,8 +697,7 @@ def gla_scan(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None =
 def gla_scan_varlen(x: torch.Tensor, log_alpha: torch.Tensor, cu_seqlens,
                     h0: torch.Tensor | None = None):
     """Differentiable ``gla_scan_fwd_varlen``."""
-    cu = [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else cu_seqlens)]
-    return _GlaScan.apply(x, log_alpha, h0, cu)
+    return _GlaScan.apply(x, log_alpha, h0, _bounds(cu_seqlens))
 
 
 def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
@@ -708,21 +708,19 @@ def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
     """
     if not isinstance(h, torch.Tensor) or h.dim() not in (2, 3):
         raise ValueError("h must be [B, D] or [B, H, D]")
-    dev, shape = h.device, tuple(h.shape)
-    if dev.type != "cuda":
+    if not h.is_cuda:
         raise ValueError("h must be on a CUDA device")
+    dev, shape, dtype = h.device, h.shape, _dtype(x, "x")
     _need(h, "h", torch.float32, shape, dev)
-    dtype = _dtype(x, "x")
     _need(x, "x", x.dtype, shape, dev)
     _need(log_alpha, "log_alpha", torch.float32, shape, dev)
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.dtype, shape, dev)
-    with torch.cuda.device(dev):
-        st = _lib.lib().gla_scan_step(x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(),
-                                      out.data_ptr(), h.numel() // shape[-1], shape[-1], dtype,
-                                      _stream(dev))
-    _lib.check(st, "gla_scan_step")
+    else:
+        _need(out, "out", x.dtype, shape, dev)
+    D = shape[-1]
+    _call("gla_scan_step", dev, x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), out.data_ptr(),
+          h.numel() // max(D, 1), D, dtype)
     return out
 
 
@@ -813,10 +811,8 @@ def gla_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tenso
     s = _Qk(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
     q_out = torch.empty(s.heads_first(s.q_shape), dtype=s.dtype, device=s.dev)
     k_out = torch.empty(s.heads_first(s.k_shape), dtype=s.dtype, device=s.dev)
-    with torch.cuda.device(s.dev):
-        st = _lib.lib().gla_qk_norm_rope_fwd(*s.pointers, q_out.data_ptr(), k_out.data_ptr(),
-                                             *s.sizes(), _stream(s.dev))
-    _lib.check(st, "gla_qk_norm_rope_fwd")
+    _call("gla_qk_norm_rope_fwd", s.dev, *s.pointers, q_out.data_ptr(), k_out.data_ptr(),
+          *s.sizes())
     return q_out, k_out
 
 
@@ -844,11 +840,8 @@ def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_
     if dwq is not None or dwk is not None:
         size = _lib.lib().gla_qk_norm_rope_bwd_scratch(s.dims[4])
         scratch = torch.empty(size, dtype=torch.uint8, device=s.dev)
-    with torch.cuda.device(s.dev):
-        st = _lib.lib().gla_qk_norm_rope_bwd(*s.pointers, d_q.data_ptr(), d_k.data_ptr(),
-                                             dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk),
-                                             *s.sizes(), _ptr(scratch), size, _stream(s.dev))
-    _lib.check(st, "gla_qk_norm_rope_bwd")
+    _call("gla_qk_norm_rope_bwd", s.dev, *s.pointers, d_q.data_ptr(), d_k.data_ptr(),
+          dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), *s.sizes(), _ptr(scratch), size)
     return dq, dk, dwq, dwk
 
 

@@ -71,7 +71,15 @@ int current_device(DeviceInfo **out) {
     return GLA_OK;
 }
 
+// The tensor-map encoder.  It is a driver call: it wants the device's context bound
+// to this thread, which a thread that has made no other call (autograd's own threads)
+// does not have yet.
 int encode_fn(EncodeTiledFn *fn) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GLA_ERR_DEVICE;
+    }
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!g_encode) {
         void *p = nullptr;
@@ -201,11 +209,22 @@ bool dv_ok(int dv) { return dv == 64 || dv == 128 || dv == 256; }
 
 }  // namespace
 
-int usable_device(int *sm_count) {
+bool tile_map(CUtensorMap *map, const void *ptr, bool f32, const long long (&dims)[3], int box_c,
+              int box_r) {
+    EncodeTiledFn enc = nullptr;
+    if (encode_fn(&enc) != GLA_OK) return false;
+    return make_map(enc, map, ptr, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    f32 ? 4 : 2, static_cast<int>(dims[0]), static_cast<int>(dims[1]),
+                    static_cast<int>(dims[2]), box_c, box_r, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+int usable_device(int *sm_count, unsigned int **status) {
     DeviceInfo *dev = nullptr;
     const int st = current_device(&dev);
-    if (st == GLA_OK) *sm_count = dev->sm_count;
-    return st;
+    if (st != GLA_OK) return st;
+    *sm_count = dev->sm_count;
+    if (status) *status = dev->status;
+    return GLA_OK;
 }
 
 int chunk_fwd_with_scratch(const void *q, const void *k, const void *v, const float *log_alpha,

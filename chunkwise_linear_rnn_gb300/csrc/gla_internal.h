@@ -170,7 +170,13 @@ inline size_t gdn_chunk_scratch_bytes(long long BH, int T, int dk) {
 // Enqueues the WY pre-pass and the sequential chunk kernel; returns a cudaError_t value.
 int launch_gdn_chunk(const GdnChunkLaunch &p, cudaStream_t stream);
 
-// The current device's SM count when it is an sm_103; returns a GLA status.
-int usable_device(int *sm_count);
+// A tensor map of a contiguous [dims[2], dims[1], dims[0]] tensor for boxes of box_r rows
+// of box_c channels of one head, laid down row by row (no swizzle, zeros outside).
+bool tile_map(CUtensorMap *map, const void *ptr, bool f32, const long long (&dims)[3], int box_c,
+              int box_r);
+
+// The current device's SM count and (when asked for) the address of its status
+// word, when it is an sm_103; returns a GLA status.
+int usable_device(int *sm_count, unsigned int **status = nullptr);
 
 }  // namespace gla

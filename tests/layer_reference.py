@@ -4,12 +4,11 @@ and how far a 32-bit computation of each may be off.
 Error bounds, with u = 2^-24 (a 32-bit rounding moves a value by at most u times itself):
 
 * the recurrence.  x_j reaches h_t through t - j gates.  Each gate is an exp
-  (within 2 roundings) and a multiplication, and each step adds once: at most 4
-  roundings a token, however the products are grouped.  A grouping into blocks adds
-  up to 2 levels of a product and a sum, and the conversion of a stored 16-bit value is
-  exact: at most 8 more.  So
+  (within 2 roundings) and a multiplication, and each step adds once: at most 4 roundings a
+  token, however the products are grouped.  A grouping into blocks adds up to 2 levels of a
+  product and a sum, and the conversion of a stored 16-bit value is exact: at most 8 more.  So
       |h_t - exact| <= u (4 N_t + 8 M_t),
-  M = the same recurrence on |x|, |h0|, and N = the recurrence on M, which weighs
+  with M = the same recurrence on |x|, |h0|, and N = the recurrence on M, which weighs
   x_j by t - j + 1.  The gradient g is the same recurrence from the end, with its own
   M and N.  dlog_alpha_t = (alpha_t g_t) h_{t-1} takes on both errors and 4 roundings.
 * a sum of n <= 256 products in 32 bits, in any order, is off by at most n u times the
@@ -85,8 +84,8 @@ def scan_backward_bound(x, log_alpha, d_h, h0=None, dhT=None):
                         None if h0 is None else np.abs(np.asarray(h0, np.float64))),
                    None if h0 is None else np.abs(np.asarray(h0, np.float64)))
     eh = _previous(scan_bound(x, log_alpha, h0), None)
-    ea = a * (eg + 4 * U * mg) * mh + a * mg * eh + 4 * U * a * mg * mh
-    return eg, ea, (a * (eg + 4 * U * mg))[..., 0, :]
+    ea = a * (eg + 3 * U * mg) * mh + a * mg * eh + U * a * mg * mh
+    return eg, ea, (a * (eg + 3 * U * mg))[..., 0, :]
 
 
 def assert_within(got: torch.Tensor, want, bound, what: str):

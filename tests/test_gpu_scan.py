@@ -399,6 +399,34 @@ def test_equal_calls_give_equal_bits_on_any_stream():
         assert all(torch.equal(a, b) for a, b in zip(g, (h, hT, *grads)))
 
 
+def test_calls_from_a_thread_that_made_no_other():
+    import threading
+    x, la, h0, d, dT = make((2,), 8, 64)
+    want = [*gla.gla_scan_fwd(x, la, h0), *gla.gla_scan_bwd(x, la, d, h0, dT)]
+    got = []
+
+    def work():
+        try:
+            got.extend([*gla.gla_scan_fwd(x, la, h0), *gla.gla_scan_bwd(x, la, d, h0, dT)])
+        except Exception as e:   # noqa: BLE001
+            got.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)), got
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("T,D", [(8, 64), (1, 8), (200, 128), (1000, 72), (300, 60)])
+def test_differentiable_sizes(T, D, dtype):
+    x, la, h0, d, dT = make((2,), T, D, dtype, seed=T)
+    leaves = [t.clone().requires_grad_() for t in (x, la, h0)]
+    grads = torch.autograd.grad(gla.gla_scan(*leaves), leaves, (d, dT))
+    check_backward(x, la, h0, d, dT, grads, f"{T}x{D}")
+
+
 def test_captured_calls_replay():
     x, la, h0, d, dT, cu = packed([300, 0, 500, 7], None, 64)
     state = h0[:, :64].clone()
