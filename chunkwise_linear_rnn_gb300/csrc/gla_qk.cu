@@ -4,7 +4,10 @@
 // and its backward: with z = R_p^T dy, g = w * z and unit = x r,
 //     dw = sum over rows of z * unit,   dx = r (g - unit * <g, unit> / n).
 //
-// One warp takes one row (a token's head); a lane takes every 32nd value.
+// A warp takes one token and walks its heads, a group of lanes (8 values to a lane) for
+// each row: the cosines and sines of the token stay in registers for all its heads.
+// Eight warps take eight neighbouring tokens, so that the head-first stores of a block are
+// contiguous runs of eight rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -18,6 +21,7 @@ namespace gla {
 namespace {
 
 constexpr int kPartials = 608;   // thread blocks of the backward, at most (4 for each of 152 SMs)
+constexpr long long kFwdBlocks = 12;   // thread blocks of the forward for each SM, at most
 
 struct QkArgs {
     const void *x[2];        // q, k
@@ -29,179 +33,396 @@ struct QkArgs {
     float *partial;          // backward with weights: [blocks][2][d]
     gla_qk_layout lay;
     int B, T, H[2], d, rot, interleaved;
+    int chunk;               // heads (q's, then k's) of a block
     float inv_n, eps;
 };
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+constexpr int kWarps = 8;
 
-__device__ __forceinline__ float warp_sum(float v) {
+// ---------------------------------------------------------------- values and pairs
+
+// Two fp32 values, for operations on both in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(Pair r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair swapped(Pair a) {
+    const float2 v = both(a);
+    return pair_of(v.y, v.x);
+}
+
+// A lane's 8 values of a row: blocks A and B of 4.  With halves, A lies in the first half of
+// the rotated part and B at the same place of the second; elsewhere B follows A.
+template <typename E>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int ia, int ib) {
+        a = *reinterpret_cast<const uint2 *>(p + ia);
+        b = *reinterpret_cast<const uint2 *>(p + ib);
+    }
+    __device__ __forceinline__ static Pair widen(unsigned w) {
+        return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ void get(Pair (&v)[4]) const {
+        v[0] = widen(a.x), v[1] = widen(a.y), v[2] = widen(b.x), v[3] = widen(b.y);
+    }
+    __device__ __forceinline__ static unsigned narrow(Pair p) {
+        const float2 v = both(p);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const unsigned *>(&h);
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *p, int ia, int ib,
+                                                 const Pair (&v)[4]) {
+        *reinterpret_cast<uint2 *>(p + ia) = make_uint2(narrow(v[0]), narrow(v[1]));
+        *reinterpret_cast<uint2 *>(p + ib) = make_uint2(narrow(v[2]), narrow(v[3]));
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p, int ia, int ib) {
+        a = *reinterpret_cast<const float4 *>(p + ia);
+        b = *reinterpret_cast<const float4 *>(p + ib);
+    }
+    __device__ __forceinline__ void get(Pair (&v)[4]) const {
+        v[0] = pair_of(a.x, a.y), v[1] = pair_of(a.z, a.w);
+        v[2] = pair_of(b.x, b.y), v[3] = pair_of(b.z, b.w);
+    }
+    __device__ __forceinline__ static void store(float *p, int ia, int ib, const Pair (&v)[4]) {
+        const float2 x = both(v[0]), y = both(v[1]), z = both(v[2]), w = both(v[3]);
+        *reinterpret_cast<float4 *>(p + ia) = make_float4(x.x, x.y, y.x, y.y);
+        *reinterpret_cast<float4 *>(p + ib) = make_float4(z.x, z.y, w.x, w.y);
+    }
+};
+
+// The sum over the lanes of a group.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int off = LANES / 2; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
 
-// A frequency as 2^64ths of a turn per position, without its whole turns: the
-// angle of any whole position is then a product modulo 2^64, with no error but
-// the frequency's own rounding times the position.
-__device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
-    const double two64 = 18446744073709551616.0;
-    const double inv_2pi = 0.15915494309189535, inv_2pi_low = -9.839338337591243e-18;   // 1 / (2 pi), in two parts
-    const double f = inv_freq * inv_2pi;
-    const double low = fma(inv_freq, inv_2pi, -f) + inv_freq * inv_2pi_low;
-    return static_cast<unsigned long long>(__double2ll_rn((f - rint(f)) * two64)) +
-           static_cast<unsigned long long>(__double2ll_rn(low * two64));
+__device__ __forceinline__ float total(const Pair (&v)[4], const Pair (&w)[4]) {
+    const float2 s = both(fma2(v[3], w[3], fma2(v[2], w[2], fma2(v[1], w[1], mul2(v[0], w[0])))));
+    return s.x + s.y;
 }
 
-__device__ __forceinline__ void angle(unsigned long long turn, long long pos, float *c, float *s) {
+// ---------------------------------------------------------------- angles
+
+// A frequency as 2^64ths of a turn per position, without its whole turns: the angle of any
+// whole position is then a product modulo 2^64.  The frequency's 53-bit significand times
+// 2^64 / (2 pi), shifted by its exponent, all in integers: off by 2^-64 of a turn for
+// frequencies up to 1, with none of the few fp64 units in it.
+__device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
+    const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(inv_freq));
+    const int e = static_cast<int>((bits >> 52) & 0x7ff) - 1023;
+    const unsigned long long m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+    const unsigned long long c = 0x28be60db9391054aull;   // 2^64 / (2 pi)
+    const unsigned long long lo = m * c, hi = __umul64hi(m, c);
+    const int s = 52 - e;
+    unsigned long long t;
+    if (s >= 128) t = 0;
+    else if (s >= 64) t = hi >> (s - 64);
+    else if (s > 0) t = (hi << (64 - s)) | (lo >> s);
+    else t = s > -64 ? lo << -s : 0;
+    return bits >> 63 ? 0 - t : t;
+}
+
+__device__ __forceinline__ float2 cos_sin(unsigned long long turn, long long pos) {
     const long long a = static_cast<long long>(turn * static_cast<unsigned long long>(pos));
     // the top 32 bits, a signed fraction of half a turn in [-1, 1)
-    sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, s, c);
+    float2 r;
+    sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &r.y, &r.x);
+    return r;
 }
 
-// Element i's partner in its pair, the pair's number, and +1 for a second member.
-__device__ __forceinline__ int partner(const QkArgs &p, int i, int *pair, bool *second) {
-    if (p.interleaved) {
-        *pair = i >> 1;
-        *second = i & 1;
-        return i ^ 1;
+// A lane's part of every row: its values, and its four pairs' angles.
+template <bool HALVES>
+struct Lane {
+    int ia, ib;              // its blocks of 4 values
+    bool there, turns;       // it has values; they are rotated
+    unsigned long long turn[4];
+
+    __device__ __forceinline__ Lane(const QkArgs &p, int j) {
+        there = 8 * j < p.d;
+        turns = 8 * j < p.rot;
+        ia = 8 * j;
+        ib = ia + 4;
+        if (HALVES && turns) ia = 4 * j, ib = 4 * j + p.rot / 2;
+        if (!there) ia = 0, ib = 4;   // reads what another lane reads, writes nothing
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn[i] = turns ? turn_of(p.inv_freq[4 * j + i]) : 0;
     }
-    *second = i >= p.rot / 2;
-    *pair = *second ? i - p.rot / 2 : i;
-    return *second ? i - p.rot / 2 : i + p.rot / 2;
-}
-
-struct Row {
-    int which, h, b, t;
 };
 
-__device__ __forceinline__ Row row_of(const QkArgs &p, long long r) {
-    const int heads = p.H[0] + p.H[1];
-    Row o;
-    const int h = static_cast<int>(r % heads);
-    const long long token = r / heads;
-    o.which = h >= p.H[0];
-    o.h = o.which ? h - p.H[0] : h;
-    o.b = static_cast<int>(token / p.T);
-    o.t = static_cast<int>(token % p.T);
-    return o;
-}
+// The cosines and sines of a token: c, s of the lane's pairs, two by two for halves, each
+// twice for neighbours.
+template <bool HALVES>
+struct Angles {
+    Pair c[HALVES ? 2 : 4], s[HALVES ? 2 : 4];
 
-template <typename E>
-__device__ __forceinline__ const E *row_in(const QkArgs &p, const Row &o) {
-    const E *x = static_cast<const E *>(p.x[o.which]);
-    return o.which ? x + o.b * p.lay.k_sb + o.t * p.lay.k_st + o.h * p.lay.k_sh
-                   : x + o.b * p.lay.q_sb + o.t * p.lay.q_st + o.h * p.lay.q_sh;
-}
-
-__device__ __forceinline__ size_t row_head_first(const QkArgs &p, const Row &o) {
-    return ((static_cast<size_t>(o.b) * p.H[o.which] + o.h) * p.T + o.t) * p.d;
-}
-
-__device__ __forceinline__ long long position_of(const QkArgs &p, const Row &o) {
-    return p.pos ? p.pos[o.b * p.lay.pos_sb + o.t] : o.t;
-}
-
-template <typename E>
-__global__ void __launch_bounds__(256) qk_fwd_kernel(const __grid_constant__ QkArgs p,
-                                                     long long rows) {
-    const int lane = threadIdx.x & 31;
-    for (long long r = blockIdx.x * 8LL + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8LL) {
-        const Row o = row_of(p, r);
-        const E *x = row_in<E>(p, o);
-        const float *w = p.w[o.which];
-        E *y = static_cast<E *>(p.y[o.which]) + row_head_first(p, o);
-        const long long pos = position_of(p, o);
-        float sum = 0.f;
-        for (int i = lane; i < p.d; i += 32) sum = fmaf(to_f32(x[i]), to_f32(x[i]), sum);
-        const float rn = 1.f / sqrtf(fmaf(warp_sum(sum), p.inv_n, p.eps));
-        for (int i = lane; i < p.d; i += 32) {
-            float v = to_f32(x[i]) * rn * (w ? w[i] : 1.f);
-            if (i < p.rot) {
-                int pair;
-                bool second;
-                const int j = partner(p, i, &pair, &second);
-                const float u = to_f32(x[j]) * rn * (w ? w[j] : 1.f);
-                float c, s;
-                angle(turn_of(p.inv_freq[pair]), pos, &c, &s);
-                v = second ? fmaf(u, s, v * c) : fmaf(-u, s, v * c);
+    __device__ __forceinline__ void at(const Lane<HALVES> &l, long long pos) {
+        float2 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = cos_sin(l.turn[i], pos);
+#pragma unroll
+        for (int i = 0; i < (HALVES ? 2 : 4); ++i) {
+            const float2 a = HALVES ? v[2 * i] : v[i], b = HALVES ? v[2 * i + 1] : v[i];
+            c[i] = pair_of(a.x, b.x);
+            // neighbours: (u, v) c + (v, u) (-s, s)
+            s[i] = pair_of(HALVES ? a.y : -a.y, b.y);
+        }
+    }
+    // Turns the four pairs by their angles, or back.
+    template <bool BACK>
+    __device__ __forceinline__ void turn(Pair (&v)[4]) const {
+        const Pair minus = pair_of(-1.f, -1.f);
+        if constexpr (HALVES) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Pair u = v[i], w = v[i + 2], ms = mul2(s[i], minus);
+                v[i] = fma2(w, BACK ? s[i] : ms, mul2(u, c[i]));
+                v[i + 2] = fma2(u, BACK ? ms : s[i], mul2(w, c[i]));
             }
-            put(y + i, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = fma2(swapped(v[i]), BACK ? mul2(s[i], minus) : s[i], mul2(v[i], c[i]));
+        }
+    }
+};
+
+// ---------------------------------------------------------------- the kernels
+
+// Loads the lane's weights (1 without a weight).
+__device__ __forceinline__ void weights(const float *w, int ia, int ib, Pair (&v)[4]) {
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pair_of(1.f, 1.f);
+        return;
+    }
+    Eight<float> e;
+    e.load(w, ia, ib);
+    e.get(v);
+}
+
+// Heads [from, to) of q (which = 0) or k of those that the block takes.
+struct Heads {
+    int from, to;
+};
+__device__ __forceinline__ Heads heads_of(const QkArgs &p, int which) {
+    const int a = blockIdx.y * p.chunk - (which ? p.H[0] : 0);
+    return {max(a, 0), min(a + p.chunk, p.H[which])};
+}
+
+// n / T, in 32 bits where they are enough.
+__device__ __forceinline__ int batch_of(const QkArgs &p, long long n, long long tokens) {
+    return tokens >> 32 ? static_cast<int>(n / p.T)
+                        : static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(p.T));
+}
+
+template <typename E, int LANES, bool HALVES>
+__global__ void __launch_bounds__(32 * kWarps, 3) qk_fwd_kernel(const __grid_constant__ QkArgs p) {
+    constexpr int ROWS = 32 / LANES, AHEAD = 4;   // rows of a warp at once, and loads ahead
+    const int lane = threadIdx.x & 31, row = lane / LANES;
+    const Lane<HALVES> l(p, lane % LANES);
+    const long long tokens = static_cast<long long>(p.B) * p.T;
+    for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
+         n += static_cast<long long>(gridDim.x) * kWarps) {
+        const int b = batch_of(p, n, tokens), t = static_cast<int>(n - static_cast<long long>(b) * p.T);
+        Angles<HALVES> turn;
+        if (p.rot) turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const Heads hs = heads_of(p, which);
+            if (hs.from >= hs.to) continue;
+            const long long sh = which ? p.lay.k_sh : p.lay.q_sh;
+            const E *x = static_cast<const E *>(p.x[which]) +
+                         (which ? b * p.lay.k_sb + t * p.lay.k_st : b * p.lay.q_sb + t * p.lay.q_st);
+            const size_t out_h = static_cast<size_t>(p.T) * p.d;
+            E *y = static_cast<E *>(p.y[which]) + static_cast<size_t>(b) * p.H[which] * out_h +
+                   static_cast<size_t>(t) * p.d;
+            Pair w[4];
+            weights(p.w[which], l.ia, l.ib, w);
+#pragma unroll 1
+            for (int h0 = hs.from + row; h0 < hs.to + row; h0 += ROWS * AHEAD) {
+                Eight<E> raw[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    // past the end: the last head again, not stored
+                    const int h = min(h0 + i * ROWS, hs.to - 1);
+                    raw[i].load(x + h * sh, l.ia, l.ib);
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int h = h0 + i * ROWS;
+                    Pair v[4];
+                    raw[i].get(v);
+                    const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
+                    const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+                    const Pair rr = pair_of(r, r);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = mul2(mul2(v[k], rr), w[k]);
+                    if (l.turns) turn.template turn<false>(v);
+                    if (l.there && h < hs.to) Eight<E>::store(y + h * out_h, l.ia, l.ib, v);
+                }
+            }
         }
     }
 }
 
-template <typename E>
-__global__ void __launch_bounds__(256) qk_bwd_kernel(const __grid_constant__ QkArgs p,
-                                                     long long rows) {
-    __shared__ float s_dw[8][2][256];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float dw[2][8] = {};
-    for (long long r = blockIdx.x * 8LL + warp; r < rows; r += gridDim.x * 8LL) {
-        const Row o = row_of(p, r);
-        const E *x = row_in<E>(p, o);
-        const float *w = p.w[o.which];
-        const E *dy = static_cast<const E *>(p.dy[o.which]) + row_head_first(p, o);
-        E *dx = static_cast<E *>(p.y[o.which]) +
-                ((static_cast<size_t>(o.b) * p.T + o.t) * p.H[o.which] + o.h) * p.d;
-        const long long pos = position_of(p, o);
-        float sum = 0.f, dot = 0.f, z[8], xv[8];
+template <typename E, int LANES, bool HALVES>
+__global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_constant__ QkArgs p) {
+    constexpr int ROWS = 32 / LANES, AHEAD = 2;
+    __shared__ __align__(16) float s_dw[kWarps * ROWS][8 * LANES];
+    const int lane = threadIdx.x & 31, row = lane / LANES;
+    const Lane<HALVES> l(p, lane % LANES);
+    const long long tokens = static_cast<long long>(p.B) * p.T;
+    Pair dw[2][4];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            const int i = lane + 32 * m;
-            z[m] = xv[m] = 0.f;
-            if (i >= p.d) continue;
-            xv[m] = to_f32(x[i]);
-            z[m] = to_f32(dy[i]);
-            if (i < p.rot) {
-                int pair;
-                bool second;
-                const int j = partner(p, i, &pair, &second);
-                const float u = to_f32(dy[j]);
-                float c, s;
-                angle(turn_of(p.inv_freq[pair]), pos, &c, &s);
-                z[m] = second ? fmaf(-u, s, z[m] * c) : fmaf(u, s, z[m] * c);
+    for (int k = 0; k < 4; ++k) dw[0][k] = dw[1][k] = pair_of(0.f, 0.f);
+    for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
+         n += static_cast<long long>(gridDim.x) * kWarps) {
+        const int b = batch_of(p, n, tokens), t = static_cast<int>(n - static_cast<long long>(b) * p.T);
+        Angles<HALVES> turn;
+        if (p.rot) turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const Heads hs = heads_of(p, which);
+            if (hs.from >= hs.to) continue;
+            const long long sh = which ? p.lay.k_sh : p.lay.q_sh;
+            const E *x = static_cast<const E *>(p.x[which]) +
+                         (which ? b * p.lay.k_sb + t * p.lay.k_st : b * p.lay.q_sb + t * p.lay.q_st);
+            const size_t out_h = static_cast<size_t>(p.T) * p.d;
+            const E *dy = static_cast<const E *>(p.dy[which]) +
+                          static_cast<size_t>(b) * p.H[which] * out_h + static_cast<size_t>(t) * p.d;
+            E *dx = static_cast<E *>(p.y[which]) + static_cast<size_t>(n) * p.H[which] * p.d;
+            Pair w[4];
+            weights(p.w[which], l.ia, l.ib, w);
+#pragma unroll 1
+            for (int h0 = hs.from + row; h0 < hs.to + row; h0 += ROWS * AHEAD) {
+                Eight<E> raw_x[AHEAD], raw_d[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int h = min(h0 + i * ROWS, hs.to - 1);
+                    raw_x[i].load(x + h * sh, l.ia, l.ib);
+                    raw_d[i].load(dy + h * out_h, l.ia, l.ib);
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int h = h0 + i * ROWS;
+                    const bool mine = l.there && h < hs.to;
+                    Pair v[4], z[4], g[4];
+                    raw_x[i].get(v);
+                    raw_d[i].get(z);
+                    if (l.turns) turn.template turn<true>(z);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) g[k] = mul2(z[k], w[k]);
+                    const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
+                    const float dot = group_sum<LANES>(l.there ? total(g, v) : 0.f);
+                    const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+                    const float along = -(dot * r) * p.inv_n;   // - <g, unit> / n
+                    const Pair rr = pair_of(r, r), aa = pair_of(along, along);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const Pair unit = mul2(v[k], rr);
+                        if (mine) dw[which][k] = fma2(z[k], unit, dw[which][k]);
+                        v[k] = mul2(fma2(unit, aa, g[k]), rr);
+                    }
+                    if (mine) Eight<E>::store(dx + static_cast<size_t>(h) * p.d, l.ia, l.ib, v);
+                }
             }
-            sum = fmaf(xv[m], xv[m], sum);
-            dot = fmaf(z[m] * (w ? w[i] : 1.f), xv[m], dot);
-        }
-        const float rn = 1.f / sqrtf(fmaf(warp_sum(sum), p.inv_n, p.eps));
-        const float back = warp_sum(dot) * rn * p.inv_n;   // <g, unit> / n
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            const int i = lane + 32 * m;
-            if (i >= p.d) continue;
-            const float unit = xv[m] * rn;
-            if (o.which) dw[1][m] = fmaf(z[m], unit, dw[1][m]);
-            else dw[0][m] = fmaf(z[m], unit, dw[0][m]);
-            put(dx + i, rn * (z[m] * (w ? w[i] : 1.f) - unit * back));
         }
     }
     if (!p.partial) return;
+    // the block's sums: the warps' and groups' one after another, q then k
+    const size_t block = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        s_dw[warp][0][lane + 32 * m] = dw[0][m];
-        s_dw[warp][1][lane + 32 * m] = dw[1][m];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.d; i += 256) {
-        float v = 0.f;
-        for (int k = 0; k < 8; ++k) v += s_dw[k][i / p.d][i % p.d];
-        p.partial[static_cast<size_t>(blockIdx.x) * 2 * p.d + i] = v;
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+        if (l.there)
+            Eight<float>::store(s_dw[(threadIdx.x >> 5) * ROWS + row], l.ia, l.ib, dw[which]);
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.d; i += 32 * kWarps) {
+            float v = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < kWarps * ROWS; ++k) v += s_dw[k][i];
+            p.partial[(block * 2 + which) * p.d + i] = v;
+        }
     }
 }
 
 // The blocks' partial weight gradients, added in order in fp64.
-__global__ void __launch_bounds__(64) qk_weight_grad_kernel(const float *partial, int blocks, int d,
-                                                            float *gq, float *gk) {
-    const int i = blockIdx.x * 64 + threadIdx.x;
-    if (i >= 2 * d) return;
+__global__ void __launch_bounds__(1024) qk_weight_grad_kernel(const float *partial, int blocks,
+                                                              int d, float *gq, float *gk) {
+    __shared__ double s_sum[32][17];
+    const int c = threadIdx.x & 15, part = threadIdx.x >> 4;   // 16 columns, 64 parts
+    const int i = blockIdx.x * 16 + c;
     double v = 0.0;
-    for (int b = 0; b < blocks; ++b) v += partial[static_cast<size_t>(b) * 2 * d + i];
-    float *g = i < d ? gq + i : gk + (i - d);
-    if (i < d ? gq != nullptr : gk != nullptr) *g = static_cast<float>(v);
+#pragma unroll 4
+    for (int b = part; b < blocks; b += 64) v += partial[static_cast<size_t>(b) * 2 * d + i];
+    if (part >= 32) s_sum[part - 32][c] = v;
+    __syncthreads();
+    if (part < 32) s_sum[part][c] += v;
+    __syncthreads();
+    if (part != 0) return;
+    v = 0.0;
+    for (int k = 0; k < 32; ++k) v += s_sum[k][c];
+    float *g = i < d ? gq : gk;
+    if (g) g[i < d ? i : i - d] = static_cast<float>(v);
+}
+
+// The work of a call as a grid: eight tokens to a block, and the heads in as many chunks
+// (of whole rounds of the warps' rows) as fill the device with small batches.  `most`:
+// blocks at most, the rest of the tokens taken by the same blocks.
+dim3 grid_of(QkArgs &a, int rows, long long most, int sms) {
+    const long long tokens = static_cast<long long>(a.B) * a.T;
+    const long long groups = (tokens + kWarps - 1) / kWarps;
+    const int heads = a.H[0] + a.H[1], rounds = (heads + rows - 1) / rows;
+    const long long want = std::max<long long>(1, (4LL * sms + groups - 1) / groups);
+    const int chunks = static_cast<int>(std::min<long long>({want, rounds, 65535, most}));
+    a.chunk = (rounds + chunks - 1) / chunks * rows;
+    const int y = (heads + a.chunk - 1) / a.chunk;
+    return dim3(static_cast<unsigned>(std::max<long long>(1, std::min(groups, most / y))), y);
+}
+
+template <typename E, bool BACKWARD>
+int launch(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
+    const bool halves = a.rot > 0 && !a.interleaved;
+    const auto go = [&](auto kernel, int rows) {
+        *grid = grid_of(a, rows, most, sms);
+        kernel<<<*grid, 32 * kWarps, 0, stream>>>(a);
+        return static_cast<int>(cudaGetLastError());
+    };
+    if constexpr (BACKWARD) {
+        if (a.d <= 64) return halves ? go(qk_bwd_kernel<E, 8, true>, 4) : go(qk_bwd_kernel<E, 8, false>, 4);
+        if (a.d <= 128) return halves ? go(qk_bwd_kernel<E, 16, true>, 2) : go(qk_bwd_kernel<E, 16, false>, 2);
+        return halves ? go(qk_bwd_kernel<E, 32, true>, 1) : go(qk_bwd_kernel<E, 32, false>, 1);
+    } else {
+        if (a.d <= 64) return halves ? go(qk_fwd_kernel<E, 8, true>, 4) : go(qk_fwd_kernel<E, 8, false>, 4);
+        if (a.d <= 128) return halves ? go(qk_fwd_kernel<E, 16, true>, 2) : go(qk_fwd_kernel<E, 16, false>, 2);
+        return halves ? go(qk_fwd_kernel<E, 32, true>, 1) : go(qk_fwd_kernel<E, 32, false>, 1);
+    }
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -270,11 +491,11 @@ int gla_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
-    const long long rows = static_cast<long long>(B) * T * (Hq + Hk);
-    const unsigned grid = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, 16LL * sms));
-    if (options->dtype == GLA_BF16) qk_fwd_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, rows);
-    else qk_fwd_kernel<float><<<grid, 256, 0, stream>>>(a, rows);
-    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+    dim3 grid;
+    const int e = options->dtype == GLA_BF16
+                      ? launch<__nv_bfloat16, false>(a, kFwdBlocks * sms, sms, &grid, stream)
+                      : launch<float, false>(a, kFwdBlocks * sms, sms, &grid, stream);
+    return e == 0 ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 unsigned long gla_qk_norm_rope_bwd_scratch(int d) {
@@ -307,13 +528,14 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
-    const long long rows = static_cast<long long>(B) * T * (Hq + Hk);
-    const unsigned grid = static_cast<unsigned>(std::min<long long>((rows + 7) / 8, kPartials));
-    if (options->dtype == GLA_BF16) qk_bwd_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, rows);
-    else qk_bwd_kernel<float><<<grid, 256, 0, stream>>>(a, rows);
-    if (weights && cudaGetLastError() == cudaSuccess)
-        qk_weight_grad_kernel<<<(2 * d + 63) / 64, 64, 0, stream>>>(a.partial, grid, d, grad_wq,
-                                                                     grad_wk);
+    dim3 grid;
+    const int e = options->dtype == GLA_BF16
+                      ? launch<__nv_bfloat16, true>(a, kPartials, sms, &grid, stream)
+                      : launch<float, true>(a, kPartials, sms, &grid, stream);
+    if (e != 0) return GLA_ERR_LAUNCH;
+    if (weights)
+        qk_weight_grad_kernel<<<2 * d / 16, 1024, 0, stream>>>(a.partial, grid.x * grid.y, d, grad_wq,
+                                                               grad_wk);
     return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
 }
 

@@ -523,8 +523,8 @@ int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, in
  * pairs of the first `rot` values by the angles p * inv_freq[i], i < rot / 2:
  * (u, v) -> (u cos - v sin, u sin + v cos), the pairs being (i, i + rot/2), or
  * (2i, 2i + 1) when `interleaved`.  The angle is
- * reduced in 64-bit integers: it is off by at most |p| 2^-63 + 2^-25 turns, so
- * far positions keep the accuracy of near ones.
+ * reduced in 64-bit integers: it is off by at most 2^-25 + |p| 2^-63 turns for
+ * frequencies up to 1, so far positions keep the accuracy of near ones.
  *
  *   q, k       : [B, T, Hq, d] and [B, T, Hk, d] dtype, read through the strides
  *                of `layout` (in elements; the last dimension is contiguous), so
