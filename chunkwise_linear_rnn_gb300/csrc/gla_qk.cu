@@ -21,7 +21,7 @@ namespace gla {
 namespace {
 
 constexpr int kPartials = 608;   // thread blocks of the backward, at most (4 for each of 152 SMs)
-constexpr long long kFwdBlocks = 12;   // thread blocks of the forward for each SM, at most
+constexpr long long kFwdBlocks = 8;   // thread blocks of the forward for each SM, at most
 
 struct QkArgs {
     const void *x[2];        // q, k
@@ -148,22 +148,33 @@ __device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
     return bits >> 63 ? 0 - t : t;
 }
 
-__device__ __forceinline__ float2 cos_sin(unsigned long long turn, long long pos) {
-    const long long a = static_cast<long long>(turn * static_cast<unsigned long long>(pos));
-    // the top 32 bits, a signed fraction of half a turn in [-1, 1)
-    float2 r;
-    sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 4.656612873077393e-10f, &r.y, &r.x);
-    return r;
+// cos and sin of a phase in 2^32nds of a turn: the nearest quarter by integers, then
+// Chebyshev fits in the square of what is left, |x| <= 1/2 quarters (sin = x S(x^2), cos =
+// 1 + x^2 C(x^2); each within a rounding of 2^-24).
+__device__ __forceinline__ float2 cos_sin(unsigned phase) {
+    const unsigned quarter = (phase + 0x20000000u) >> 30;
+    const float x = static_cast<float>(static_cast<int>(phase - (quarter << 30))) * 9.313225746154785e-10f;
+    const float z = x * x;
+    const float s = x * fmaf(fmaf(fmaf(-4.6021174639463425e-3f, z, 7.968020439147949e-2f), z,
+                                  -0.6459634900093079f), z, 1.5707963705062866f);
+    const float c = fmaf(fmaf(fmaf(fmaf(9.06734901946038e-4f, z, -2.086152695119381e-2f), z,
+                                   0.253669410943985f), z, -1.2337005138397217f), z, 1.f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return make_float2(__uint_as_float(__float_as_uint(a) ^ ((quarter + 1) << 30 & 0x80000000u)),
+                       __uint_as_float(__float_as_uint(b) ^ (quarter << 30 & 0x80000000u)));
 }
 
-// A lane's part of every row: its values, and its four pairs' angles.
-template <bool HALVES>
+// A lane's part of every row: its values, and the angles that it works out for itself and the
+// same lanes of the warp's other groups.
+template <int LANES, bool HALVES>
 struct Lane {
+    static constexpr int kRows = 32 / LANES, kOwn = 4 / kRows;   // groups; angles of each
     int ia, ib;              // its blocks of 4 values
     bool there, turns;       // it has values; they are rotated
-    unsigned long long turn[4];
+    unsigned long long turn[kOwn];
 
-    __device__ __forceinline__ Lane(const QkArgs &p, int j) {
+    __device__ __forceinline__ Lane(const QkArgs &p, int lane) {
+        const int j = lane % LANES;
         there = 8 * j < p.d;
         turns = 8 * j < p.rot;
         ia = 8 * j;
@@ -171,43 +182,55 @@ struct Lane {
         if (HALVES && turns) ia = 4 * j, ib = 4 * j + p.rot / 2;
         if (!there) ia = 0, ib = 4;   // reads what another lane reads, writes nothing
 #pragma unroll
-        for (int i = 0; i < 4; ++i) turn[i] = turns ? turn_of(p.inv_freq[4 * j + i]) : 0;
+        for (int i = 0; i < kOwn; ++i)
+            turn[i] = turns ? turn_of(p.inv_freq[4 * j + lane / LANES * kOwn + i]) : 0;
     }
 };
 
-// The cosines and sines of a token: c, s of the lane's pairs, two by two for halves, each
-// twice for neighbours.
-template <bool HALVES>
+// The cosines and sines of a token: c, s of the lane's pairs, two by two for halves (with -s in
+// m), each twice for neighbours (u, v) -> (u, v) c + (v, u) (-s, s) (with (s, -s) in m).
+template <int LANES, bool HALVES>
 struct Angles {
-    Pair c[HALVES ? 2 : 4], s[HALVES ? 2 : 4];
+    Pair c[HALVES ? 2 : 4], s[HALVES ? 2 : 4], m[HALVES ? 2 : 4];
 
-    __device__ __forceinline__ void at(const Lane<HALVES> &l, long long pos) {
-        float2 v[4];
+    __device__ __forceinline__ void at(const Lane<LANES, HALVES> &l, long long pos) {
+        using L = Lane<LANES, HALVES>;
+        float2 own[L::kOwn], v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = cos_sin(l.turn[i], pos);
+        for (int i = 0; i < L::kOwn; ++i)
+            own[i] = cos_sin(static_cast<unsigned>(
+                (l.turn[i] * static_cast<unsigned long long>(pos)) >> 32));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = own[i % L::kOwn];
+            if constexpr (L::kRows > 1) {
+                const int from = i / L::kOwn * LANES + (threadIdx.x & (LANES - 1));
+                v[i].x = __shfl_sync(0xffffffffu, v[i].x, from);
+                v[i].y = __shfl_sync(0xffffffffu, v[i].y, from);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < (HALVES ? 2 : 4); ++i) {
             const float2 a = HALVES ? v[2 * i] : v[i], b = HALVES ? v[2 * i + 1] : v[i];
             c[i] = pair_of(a.x, b.x);
-            // neighbours: (u, v) c + (v, u) (-s, s)
             s[i] = pair_of(HALVES ? a.y : -a.y, b.y);
+            m[i] = pair_of(HALVES ? -a.y : a.y, -b.y);
         }
     }
     // Turns the four pairs by their angles, or back.
     template <bool BACK>
     __device__ __forceinline__ void turn(Pair (&v)[4]) const {
-        const Pair minus = pair_of(-1.f, -1.f);
         if constexpr (HALVES) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const Pair u = v[i], w = v[i + 2], ms = mul2(s[i], minus);
-                v[i] = fma2(w, BACK ? s[i] : ms, mul2(u, c[i]));
-                v[i + 2] = fma2(u, BACK ? ms : s[i], mul2(w, c[i]));
+                const Pair u = v[i], w = v[i + 2];
+                v[i] = fma2(w, BACK ? s[i] : m[i], mul2(u, c[i]));
+                v[i + 2] = fma2(u, BACK ? m[i] : s[i], mul2(w, c[i]));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = fma2(swapped(v[i]), BACK ? mul2(s[i], minus) : s[i], mul2(v[i], c[i]));
+                v[i] = fma2(swapped(v[i]), BACK ? m[i] : s[i], mul2(v[i], c[i]));
         }
     }
 };
@@ -241,16 +264,17 @@ __device__ __forceinline__ int batch_of(const QkArgs &p, long long n, long long 
                         : static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(p.T));
 }
 
-template <typename E, int LANES, bool HALVES>
-__global__ void __launch_bounds__(32 * kWarps, 3) qk_fwd_kernel(const __grid_constant__ QkArgs p) {
+// PART: only the first rot < d values are rotated, so that some lanes rotate and some do not.
+template <typename E, int LANES, bool HALVES, bool PART>
+__global__ void __launch_bounds__(32 * kWarps, 4) qk_fwd_kernel(const __grid_constant__ QkArgs p) {
     constexpr int ROWS = 32 / LANES, AHEAD = 4;   // rows of a warp at once, and loads ahead
     const int lane = threadIdx.x & 31, row = lane / LANES;
-    const Lane<HALVES> l(p, lane % LANES);
+    const Lane<LANES, HALVES> l(p, lane);
     const long long tokens = static_cast<long long>(p.B) * p.T;
     for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
          n += static_cast<long long>(gridDim.x) * kWarps) {
         const int b = batch_of(p, n, tokens), t = static_cast<int>(n - static_cast<long long>(b) * p.T);
-        Angles<HALVES> turn;
+        Angles<LANES, HALVES> turn;
         if (p.rot) turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
@@ -264,39 +288,51 @@ __global__ void __launch_bounds__(32 * kWarps, 3) qk_fwd_kernel(const __grid_con
                    static_cast<size_t>(t) * p.d;
             Pair w[4];
             weights(p.w[which], l.ia, l.ib, w);
+            const auto finish = [&](const Eight<E> &raw, E *to, bool mine) {
+                Pair v[4];
+                raw.get(v);
+                const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
+                const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+                const Pair rr = pair_of(r, r);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = mul2(mul2(v[k], rr), w[k]);
+                if (PART ? l.turns : p.rot > 0) turn.template turn<false>(v);
+                if (mine) Eight<E>::store(to, l.ia, l.ib, v);
+            };
+            int h = hs.from;
 #pragma unroll 1
-            for (int h0 = hs.from + row; h0 < hs.to + row; h0 += ROWS * AHEAD) {
+            for (; h + ROWS * AHEAD <= hs.to; h += ROWS * AHEAD) {
                 Eight<E> raw[AHEAD];
+                const E *from = x + (h + row) * sh;
+                E *to = y + (h + row) * out_h;
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    // past the end: the last head again, not stored
-                    const int h = min(h0 + i * ROWS, hs.to - 1);
-                    raw[i].load(x + h * sh, l.ia, l.ib);
+                    raw[i].load(from, l.ia, l.ib);
+                    from += ROWS * sh;
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int h = h0 + i * ROWS;
-                    Pair v[4];
-                    raw[i].get(v);
-                    const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
-                    const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
-                    const Pair rr = pair_of(r, r);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = mul2(mul2(v[k], rr), w[k]);
-                    if (l.turns) turn.template turn<false>(v);
-                    if (l.there && h < hs.to) Eight<E>::store(y + h * out_h, l.ia, l.ib, v);
+                    finish(raw[i], to, l.there);
+                    to += ROWS * out_h;
                 }
+            }
+            // the last heads, a round at a time; lanes past the end take the last head again
+#pragma unroll 1
+            for (; h < hs.to; h += ROWS) {
+                Eight<E> raw;
+                raw.load(x + min(h + row, hs.to - 1) * sh, l.ia, l.ib);
+                finish(raw, y + (h + row) * out_h, l.there && h + row < hs.to);
             }
         }
     }
 }
 
-template <typename E, int LANES, bool HALVES>
+template <typename E, int LANES, bool HALVES, bool PART>
 __global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_constant__ QkArgs p) {
     constexpr int ROWS = 32 / LANES, AHEAD = 2;
     __shared__ __align__(16) float s_dw[kWarps * ROWS][8 * LANES];
     const int lane = threadIdx.x & 31, row = lane / LANES;
-    const Lane<HALVES> l(p, lane % LANES);
+    const Lane<LANES, HALVES> l(p, lane);
     const long long tokens = static_cast<long long>(p.B) * p.T;
     Pair dw[2][4];
 #pragma unroll
@@ -304,7 +340,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_con
     for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
          n += static_cast<long long>(gridDim.x) * kWarps) {
         const int b = batch_of(p, n, tokens), t = static_cast<int>(n - static_cast<long long>(b) * p.T);
-        Angles<HALVES> turn;
+        Angles<LANES, HALVES> turn;
         if (p.rot) turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
@@ -319,38 +355,54 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_con
             E *dx = static_cast<E *>(p.y[which]) + static_cast<size_t>(n) * p.H[which] * p.d;
             Pair w[4];
             weights(p.w[which], l.ia, l.ib, w);
+            const auto finish = [&](const Eight<E> &raw_x, const Eight<E> &raw_d, E *to, bool mine) {
+                Pair v[4], z[4], g[4];
+                raw_x.get(v);
+                raw_d.get(z);
+                if (PART ? l.turns : p.rot > 0) turn.template turn<true>(z);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] = mul2(z[k], w[k]);
+                const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
+                const float dot = group_sum<LANES>(l.there ? total(g, v) : 0.f);
+                const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
+                const float along = -(dot * r) * p.inv_n;   // - <g, unit> / n
+                const Pair rr = pair_of(r, r), aa = pair_of(along, along);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const Pair unit = mul2(v[k], rr);
+                    if (mine) dw[which][k] = fma2(z[k], unit, dw[which][k]);
+                    v[k] = mul2(fma2(unit, aa, g[k]), rr);
+                }
+                if (mine) Eight<E>::store(to, l.ia, l.ib, v);
+            };
+            int h = hs.from;
 #pragma unroll 1
-            for (int h0 = hs.from + row; h0 < hs.to + row; h0 += ROWS * AHEAD) {
+            for (; h + ROWS * AHEAD <= hs.to; h += ROWS * AHEAD) {
                 Eight<E> raw_x[AHEAD], raw_d[AHEAD];
+                const E *from = x + (h + row) * sh, *from_d = dy + (h + row) * out_h;
+                E *to = dx + static_cast<size_t>(h + row) * p.d;
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int h = min(h0 + i * ROWS, hs.to - 1);
-                    raw_x[i].load(x + h * sh, l.ia, l.ib);
-                    raw_d[i].load(dy + h * out_h, l.ia, l.ib);
+                    raw_x[i].load(from, l.ia, l.ib);
+                    raw_d[i].load(from_d, l.ia, l.ib);
+                    from += ROWS * sh;
+                    from_d += ROWS * out_h;
                 }
 #pragma unroll
                 for (int i = 0; i < AHEAD; ++i) {
-                    const int h = h0 + i * ROWS;
-                    const bool mine = l.there && h < hs.to;
-                    Pair v[4], z[4], g[4];
-                    raw_x[i].get(v);
-                    raw_d[i].get(z);
-                    if (l.turns) turn.template turn<true>(z);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) g[k] = mul2(z[k], w[k]);
-                    const float sum = group_sum<LANES>(l.there ? total(v, v) : 0.f);
-                    const float dot = group_sum<LANES>(l.there ? total(g, v) : 0.f);
-                    const float r = rsqrtf(fmaf(sum, p.inv_n, p.eps));
-                    const float along = -(dot * r) * p.inv_n;   // - <g, unit> / n
-                    const Pair rr = pair_of(r, r), aa = pair_of(along, along);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const Pair unit = mul2(v[k], rr);
-                        if (mine) dw[which][k] = fma2(z[k], unit, dw[which][k]);
-                        v[k] = mul2(fma2(unit, aa, g[k]), rr);
-                    }
-                    if (mine) Eight<E>::store(dx + static_cast<size_t>(h) * p.d, l.ia, l.ib, v);
+                    finish(raw_x[i], raw_d[i], to, l.there);
+                    to += ROWS * p.d;
                 }
+            }
+            // the last heads, a round at a time; lanes past the end take the last head again
+#pragma unroll 1
+            for (; h < hs.to; h += ROWS) {
+                Eight<E> raw_x, raw_d;
+                const int last = min(h + row, hs.to - 1);
+                raw_x.load(x + last * sh, l.ia, l.ib);
+                raw_d.load(dy + last * out_h, l.ia, l.ib);
+                finish(raw_x, raw_d, dx + static_cast<size_t>(h + row) * p.d,
+                       l.there && h + row < hs.to);
             }
         }
     }
@@ -406,23 +458,28 @@ dim3 grid_of(QkArgs &a, int rows, long long most, int sms) {
     return dim3(static_cast<unsigned>(std::max<long long>(1, std::min(groups, most / y))), y);
 }
 
+template <typename E, int LANES, bool HALVES, bool PART, bool BACKWARD>
+int launch_one(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
+    *grid = grid_of(a, 32 / LANES, most, sms);
+    if constexpr (BACKWARD) qk_bwd_kernel<E, LANES, HALVES, PART><<<*grid, 32 * kWarps, 0, stream>>>(a);
+    else qk_fwd_kernel<E, LANES, HALVES, PART><<<*grid, 32 * kWarps, 0, stream>>>(a);
+    return static_cast<int>(cudaGetLastError());
+}
+
+template <typename E, int LANES, bool BACKWARD>
+int launch_lanes(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
+    const bool halves = !a.interleaved, part = a.rot > 0 && a.rot < a.d;
+    if (halves) return part ? launch_one<E, LANES, true, true, BACKWARD>(a, most, sms, grid, stream)
+                            : launch_one<E, LANES, true, false, BACKWARD>(a, most, sms, grid, stream);
+    return part ? launch_one<E, LANES, false, true, BACKWARD>(a, most, sms, grid, stream)
+                : launch_one<E, LANES, false, false, BACKWARD>(a, most, sms, grid, stream);
+}
+
 template <typename E, bool BACKWARD>
 int launch(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
-    const bool halves = a.rot > 0 && !a.interleaved;
-    const auto go = [&](auto kernel, int rows) {
-        *grid = grid_of(a, rows, most, sms);
-        kernel<<<*grid, 32 * kWarps, 0, stream>>>(a);
-        return static_cast<int>(cudaGetLastError());
-    };
-    if constexpr (BACKWARD) {
-        if (a.d <= 64) return halves ? go(qk_bwd_kernel<E, 8, true>, 4) : go(qk_bwd_kernel<E, 8, false>, 4);
-        if (a.d <= 128) return halves ? go(qk_bwd_kernel<E, 16, true>, 2) : go(qk_bwd_kernel<E, 16, false>, 2);
-        return halves ? go(qk_bwd_kernel<E, 32, true>, 1) : go(qk_bwd_kernel<E, 32, false>, 1);
-    } else {
-        if (a.d <= 64) return halves ? go(qk_fwd_kernel<E, 8, true>, 4) : go(qk_fwd_kernel<E, 8, false>, 4);
-        if (a.d <= 128) return halves ? go(qk_fwd_kernel<E, 16, true>, 2) : go(qk_fwd_kernel<E, 16, false>, 2);
-        return halves ? go(qk_fwd_kernel<E, 32, true>, 1) : go(qk_fwd_kernel<E, 32, false>, 1);
-    }
+    if (a.d <= 64) return launch_lanes<E, 8, BACKWARD>(a, most, sms, grid, stream);
+    if (a.d <= 128) return launch_lanes<E, 16, BACKWARD>(a, most, sms, grid, stream);
+    return launch_lanes<E, 32, BACKWARD>(a, most, sms, grid, stream);
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
