@@ -16,11 +16,12 @@
 
 #include "gla.h"
 #include "gla_internal.h"
+#include "gla_ptx.cuh"
 
 namespace gla {
 namespace {
 
-constexpr int kPartials = 608;   // thread blocks of the backward, at most (4 for each of 152 SMs)
+constexpr int kPartials = 304;   // thread blocks of the backward, at most (2 for each of 152 SMs)
 constexpr long long kFwdBlocks = 8;   // thread blocks of the forward for each SM, at most
 
 struct QkArgs {
@@ -79,6 +80,10 @@ struct Eight<__nv_bfloat16> {
         a = *reinterpret_cast<const uint2 *>(p + ia);
         b = *reinterpret_cast<const uint2 *>(p + ib);
     }
+    __device__ __forceinline__ void load_two(const void *pa, const void *pb) {
+        a = *static_cast<const uint2 *>(pa);
+        b = *static_cast<const uint2 *>(pb);
+    }
     __device__ __forceinline__ static Pair widen(unsigned w) {
         return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
@@ -102,6 +107,10 @@ struct Eight<float> {
     __device__ __forceinline__ void load(const float *p, int ia, int ib) {
         a = *reinterpret_cast<const float4 *>(p + ia);
         b = *reinterpret_cast<const float4 *>(p + ib);
+    }
+    __device__ __forceinline__ void load_two(const void *pa, const void *pb) {
+        a = *static_cast<const float4 *>(pa);
+        b = *static_cast<const float4 *>(pb);
     }
     __device__ __forceinline__ void get(Pair (&v)[4]) const {
         v[0] = pair_of(a.x, a.y), v[1] = pair_of(a.z, a.w);
@@ -327,38 +336,119 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qk_fwd_kernel(const __grid_con
     }
 }
 
+// Values copied to shared memory in the background.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
+}
+
+// The rounds of a warp, one after another: a token's heads of q, then of k, then the next
+// token.  x and dy point at this lane's row.
+template <typename E, int ROWS>
+struct Rounds {
+    long long n;             // token
+    int h, to;               // head of the round, and the part's end
+    bool of_k;
+    const E *x, *dy;
+    long long step, dy_step;
+
+    __device__ __forceinline__ void begin(const QkArgs &p, long long token, long long tokens,
+                                          int row) {
+        n = token;
+        const Heads q = heads_of(p, 0);
+        part(p, q.from >= q.to, tokens, row);
+    }
+    __device__ __forceinline__ void part(const QkArgs &p, bool k, long long tokens, int row) {
+        of_k = k;
+        if (n >= tokens) return;
+        const Heads hs = heads_of(p, k);
+        h = hs.from;
+        to = hs.to;
+        const int b = batch_of(p, n, tokens);
+        const long long t = n - static_cast<long long>(b) * p.T;
+        const long long sh = k ? p.lay.k_sh : p.lay.q_sh;
+        const long long out_h = static_cast<long long>(p.T) * p.d;
+        x = static_cast<const E *>(k ? p.x[1] : p.x[0]) + (h + row) * sh +
+            (k ? b * p.lay.k_sb + t * p.lay.k_st : b * p.lay.q_sb + t * p.lay.q_st);
+        dy = static_cast<const E *>(k ? p.dy[1] : p.dy[0]) +
+             (static_cast<long long>(b) * (k ? p.H[1] : p.H[0]) + h + row) * out_h + t * p.d;
+        step = ROWS * sh;
+        dy_step = ROWS * out_h;
+    }
+    __device__ __forceinline__ void next(const QkArgs &p, long long tokens, int row) {
+        h += ROWS;
+        x += step;
+        dy += dy_step;
+        if (h < to) return;
+        const Heads k = heads_of(p, 1);
+        if (!of_k && k.from < k.to) part(p, true, tokens, row);
+        else begin(p, n + static_cast<long long>(gridDim.x) * kWarps, tokens, row);
+    }
+};
+
+// Backward.  A queue of DEPTH rounds of x and dy for each warp is on its way to shared
+// memory: each lane copies and reads its own values, so that no barrier stands between.
 template <typename E, int LANES, bool HALVES, bool PART>
-__global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_constant__ QkArgs p) {
-    constexpr int ROWS = 32 / LANES, AHEAD = 2;
-    __shared__ __align__(16) float s_dw[kWarps * ROWS][8 * LANES];
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    qk_bwd_kernel(const __grid_constant__ QkArgs p) {
+    constexpr int ROWS = 32 / LANES, DEPTH = sizeof(E) == 2 ? 4 : 3;
+    constexpr int PIECE = 4 * sizeof(E), PIECES = 4;   // a lane's blocks A and B of x and of dy
+    __shared__ __align__(16) unsigned char s_queue[kWarps][DEPTH][PIECES][32][PIECE];
+    static_assert(sizeof(s_queue) >= sizeof(float) * kWarps * ROWS * 8 * LANES, "the sums' space");
     const int lane = threadIdx.x & 31, row = lane / LANES;
     const Lane<LANES, HALVES> l(p, lane);
     const long long tokens = static_cast<long long>(p.B) * p.T;
+    auto *queue = s_queue[threadIdx.x >> 5];
+
+    Rounds<E, ROWS> ask;
+    ask.begin(p, blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5), tokens, row);
+    const auto request = [&](int slot) {
+        if (ask.n < tokens) {
+            if (ask.h + row < ask.to) {   // the others' values go nowhere
+                const uint32_t to = smem_u32(&queue[slot][0][lane][0]);
+                copy_async<PIECE>(to, ask.x + l.ia);
+                copy_async<PIECE>(to + 32 * PIECE, ask.x + l.ib);
+                copy_async<PIECE>(to + 64 * PIECE, ask.dy + l.ia);
+                copy_async<PIECE>(to + 96 * PIECE, ask.dy + l.ib);
+            }
+            ask.next(p, tokens, row);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) request(i);
+
     Pair dw[2][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) dw[0][k] = dw[1][k] = pair_of(0.f, 0.f);
+    int slot = 0;
     for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
          n += static_cast<long long>(gridDim.x) * kWarps) {
-        const int b = batch_of(p, n, tokens), t = static_cast<int>(n - static_cast<long long>(b) * p.T);
         Angles<LANES, HALVES> turn;
-        if (p.rot) turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
+        if (p.rot) {
+            const int b = batch_of(p, n, tokens);
+            const long long t = n - static_cast<long long>(b) * p.T;
+            turn.at(l, p.pos ? p.pos[b * p.lay.pos_sb + t] : t);
+        }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const Heads hs = heads_of(p, which);
             if (hs.from >= hs.to) continue;
-            const long long sh = which ? p.lay.k_sh : p.lay.q_sh;
-            const E *x = static_cast<const E *>(p.x[which]) +
-                         (which ? b * p.lay.k_sb + t * p.lay.k_st : b * p.lay.q_sb + t * p.lay.q_st);
-            const size_t out_h = static_cast<size_t>(p.T) * p.d;
-            const E *dy = static_cast<const E *>(p.dy[which]) +
-                          static_cast<size_t>(b) * p.H[which] * out_h + static_cast<size_t>(t) * p.d;
-            E *dx = static_cast<E *>(p.y[which]) + static_cast<size_t>(n) * p.H[which] * p.d;
+            E *dx = static_cast<E *>(p.y[which]) + (n * p.H[which] + hs.from + row) * p.d;
             Pair w[4];
             weights(p.w[which], l.ia, l.ib, w);
-            const auto finish = [&](const Eight<E> &raw_x, const Eight<E> &raw_d, E *to, bool mine) {
+#pragma unroll 1
+            for (int h = hs.from; h < hs.to; h += ROWS) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
                 Pair v[4], z[4], g[4];
-                raw_x.get(v);
-                raw_d.get(z);
+                Eight<E> raw;
+                raw.load_two(&queue[slot][0][lane][0], &queue[slot][1][lane][0]);
+                raw.get(v);
+                raw.load_two(&queue[slot][2][lane][0], &queue[slot][3][lane][0]);
+                raw.get(z);
+                request(slot);
+                slot = slot == DEPTH - 1 ? 0 : slot + 1;
+                const bool mine = l.there && h + row < hs.to;
                 if (PART ? l.turns : p.rot > 0) turn.template turn<true>(z);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) g[k] = mul2(z[k], w[k]);
@@ -373,39 +463,14 @@ __global__ void __launch_bounds__(32 * kWarps, 2) qk_bwd_kernel(const __grid_con
                     if (mine) dw[which][k] = fma2(z[k], unit, dw[which][k]);
                     v[k] = mul2(fma2(unit, aa, g[k]), rr);
                 }
-                if (mine) Eight<E>::store(to, l.ia, l.ib, v);
-            };
-            int h = hs.from;
-#pragma unroll 1
-            for (; h + ROWS * AHEAD <= hs.to; h += ROWS * AHEAD) {
-                Eight<E> raw_x[AHEAD], raw_d[AHEAD];
-                const E *from = x + (h + row) * sh, *from_d = dy + (h + row) * out_h;
-                E *to = dx + static_cast<size_t>(h + row) * p.d;
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    raw_x[i].load(from, l.ia, l.ib);
-                    raw_d[i].load(from_d, l.ia, l.ib);
-                    from += ROWS * sh;
-                    from_d += ROWS * out_h;
-                }
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    finish(raw_x[i], raw_d[i], to, l.there);
-                    to += ROWS * p.d;
-                }
-            }
-            // the last heads, a round at a time; lanes past the end take the last head again
-#pragma unroll 1
-            for (; h < hs.to; h += ROWS) {
-                Eight<E> raw_x, raw_d;
-                const int last = min(h + row, hs.to - 1);
-                raw_x.load(x + last * sh, l.ia, l.ib);
-                raw_d.load(dy + last * out_h, l.ia, l.ib);
-                finish(raw_x, raw_d, dx + static_cast<size_t>(h + row) * p.d,
-                       l.there && h + row < hs.to);
+                if (mine) Eight<E>::store(dx, l.ia, l.ib, v);
+                dx += ROWS * p.d;
             }
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    auto *s_dw = reinterpret_cast<float(*)[8 * LANES]>(&s_queue[0][0][0][0][0]);
     if (!p.partial) return;
     // the block's sums: the warps' and groups' one after another, q then k
     const size_t block = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
