@@ -17,6 +17,7 @@ bf16; log_alpha ``[B,H,T,dk]`` fp32; o ``[B,H,T,dv]`` bf16; h0 / hT
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -727,57 +728,52 @@ def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
 _NORMS = {"rms": _lib.GLA_NORM_RMS, "l2": _lib.GLA_NORM_L2}
 
 
-class _Qk:
-    """The checked sizes, strides and options of a gla_qk_norm_rope call."""
+@functools.lru_cache(maxsize=256)
+def _qk_structs(*args):
+    """The C call's layout and options for these strides and options."""
+    return (ctypes.byref(_lib.GlaQkLayout(*args[:7])),
+            ctypes.byref(_lib.GlaQkOptions(dtype=args[7], norm=args[8], interleaved=args[9],
+                                           eps=args[10])))
 
-    def __init__(self, q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
-        for t, name in ((q, "q"), (k, "k")):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must be a torch.Tensor")
-            if t.device.type != "cuda" or t.device != q.device:
-                raise ValueError(f"{name} must be on the CUDA device of q")
-            if t.dim() != 4:
-                raise ValueError(f"{name} must be [B, T, H, d]")
-            if t.stride(-1) != 1:
-                raise ValueError(f"{name}'s last dimension must be contiguous")
-        dev, (B, T, Hq, d), Hk = q.device, q.shape, k.shape[2]
-        if k.dtype != q.dtype:
-            raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
-        if tuple(k.shape) != (B, T, Hk, d):
-            raise ValueError(f"k must have shape {(B, T, Hk, d)}, got {tuple(k.shape)}")
-        if norm not in _NORMS:
-            raise ValueError("norm must be 'rms' or 'l2'")
-        for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if w is not None:
-                _need(w, name, torch.float32, (d,), dev)
-        rot = 0
-        if inv_freq is not None:
-            rot = 2 * inv_freq.numel()
-            _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
-        pos_sb = 0
-        if positions is not None:
-            if not isinstance(positions, torch.Tensor):
-                raise TypeError("positions must be a torch.Tensor")
-            one = positions.dim() == 1
-            _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
-            pos_sb = 0 if one else T
-        self.dev, self.q_shape, self.k_shape = dev, (B, T, Hq, d), (B, T, Hk, d)
-        self.dims = (B, T, Hq, Hk, d, rot)
-        # a dimension of one entry is never stepped over, whatever its stride says
-        steps = [0 if n == 1 else st for t in (q, k)
-                 for n, st in zip(t.shape[:3], t.stride()[:3])]
-        self.layout = _lib.GlaQkLayout(*steps, pos_sb)
-        self.options = _lib.GlaQkOptions(dtype=_dtype(q, "q"), norm=_NORMS[norm],
-                                         interleaved=1 if interleaved else 0, eps=float(eps))
-        self.pointers = (q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight),
-                         _ptr(positions), _ptr(inv_freq))
-        self.dtype = q.dtype
 
-    def heads_first(self, shape):
-        return shape[0], shape[2], shape[1], shape[3]
-
-    def sizes(self):
-        return (*self.dims, ctypes.byref(self.layout), ctypes.byref(self.options))
+def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+    """Checks the arguments of a gla_qk_norm_rope call: (the inputs' pointers, the C call's
+    sizes)."""
+    for t, name in ((q, "q"), (k, "k")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda or t.device != q.device:
+            raise ValueError(f"{name} must be on the CUDA device of q")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, T, H, d]")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}'s last dimension must be contiguous")
+    dev, (B, T, Hq, d), Hk = q.device, q.shape, k.shape[2]
+    dtype = _dtype(q, "q")
+    if k.dtype is not q.dtype:
+        raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+    if k.shape != (B, T, Hk, d):
+        raise ValueError(f"k must have shape {(B, T, Hk, d)}, got {tuple(k.shape)}")
+    if norm not in _NORMS:
+        raise ValueError("norm must be 'rms' or 'l2'")
+    if q_weight is not None:
+        _need(q_weight, "q_weight", torch.float32, (d,), dev)
+    if k_weight is not None:
+        _need(k_weight, "k_weight", torch.float32, (d,), dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+    pos_sb = 0
+    if positions is not None:
+        one = isinstance(positions, torch.Tensor) and positions.dim() == 1
+        _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
+        pos_sb = 0 if one else T
+    # a dimension of one entry is never stepped over, whatever its stride says
+    steps = [0 if n == 1 else st for t in (q, k) for n, st in zip(t.shape[:3], t.stride())]
+    structs = _qk_structs(*steps, pos_sb, dtype, _NORMS[norm], 1 if interleaved else 0, float(eps))
+    return ((q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+             _ptr(inv_freq)), (B, T, Hq, Hk, d, rot, *structs))
 
 
 def gla_rope_frequencies(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -808,11 +804,12 @@ def gla_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tenso
     ``interleaved``.  ``positions`` is int64 ``[B, T]`` or ``[T]`` (None: 0 .. T-1).
     d and rot are multiples of 8, up to 256.
     """
-    s = _Qk(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
-    q_out = torch.empty(s.heads_first(s.q_shape), dtype=s.dtype, device=s.dev)
-    k_out = torch.empty(s.heads_first(s.k_shape), dtype=s.dtype, device=s.dev)
-    _call("gla_qk_norm_rope_fwd", s.dev, *s.pointers, q_out.data_ptr(), k_out.data_ptr(),
-          *s.sizes())
+    pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
+                                interleaved)
+    B, T, Hq, Hk, d = sizes[:5]
+    q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
+    k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=q.device)
+    _call("gla_qk_norm_rope_fwd", q.device, *pointers, q_out.data_ptr(), k_out.data_ptr(), *sizes)
     return q_out, k_out
 
 
@@ -829,19 +826,22 @@ def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_
     contiguous ``[B, T, H, d]`` in q's type, and fp32 ``[d]`` sums over every row
     (None without a weight, or when not needed).
     """
-    s = _Qk(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved)
-    _need(d_q, "d_q", s.dtype, s.heads_first(s.q_shape), s.dev)
-    _need(d_k, "d_k", s.dtype, s.heads_first(s.k_shape), s.dev)
-    dq = torch.empty(s.q_shape, dtype=s.dtype, device=s.dev)
-    dk = torch.empty(s.k_shape, dtype=s.dtype, device=s.dev)
-    dwq, dwk = (torch.empty_like(w) if w is not None and need_dweights else None
-                for w in (q_weight, k_weight))
+    pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
+                                interleaved)
+    B, T, Hq, Hk, d = sizes[:5]
+    dev = q.device
+    _need(d_q, "d_q", q.dtype, (B, Hq, T, d), dev)
+    _need(d_k, "d_k", q.dtype, (B, Hk, T, d), dev)
+    dq = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
+    dk = torch.empty((B, T, Hk, d), dtype=q.dtype, device=dev)
+    dwq = torch.empty_like(q_weight) if q_weight is not None and need_dweights else None
+    dwk = torch.empty_like(k_weight) if k_weight is not None and need_dweights else None
     scratch, size = None, 0
     if dwq is not None or dwk is not None:
-        size = _lib.lib().gla_qk_norm_rope_bwd_scratch(s.dims[4])
-        scratch = torch.empty(size, dtype=torch.uint8, device=s.dev)
-    _call("gla_qk_norm_rope_bwd", s.dev, *s.pointers, d_q.data_ptr(), d_k.data_ptr(),
-          dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), *s.sizes(), _ptr(scratch), size)
+        size = _lib.lib().gla_qk_norm_rope_bwd_scratch(d)
+        scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+    _call("gla_qk_norm_rope_bwd", dev, *pointers, d_q.data_ptr(), d_k.data_ptr(), dq.data_ptr(),
+          dk.data_ptr(), _ptr(dwq), _ptr(dwk), *sizes, _ptr(scratch), size)
     return dq, dk, dwq, dwk
 
 
