@@ -41,15 +41,42 @@ def _stream(device: torch.device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(_lib.lib(), name)
+
+
 def _call(name: str, device: torch.device, *args) -> None:
     """A C entry point on the current stream of `device`; raises GlaError on a bad status."""
-    fn = getattr(_lib.lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
-    _lib.check(st, name)
+            st = _entry(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, name)
+
+
+def _once(backward):
+    """`backward` of an autograd.Function whose gradients have no derivative of their own.
+
+    A plain backward pass runs it as it is; one that builds a graph of the gradients gets
+    torch's wrapper, which refuses the second derivative when it is asked for.
+    """
+    refusing = torch.autograd.function.once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return (refusing if torch.is_grad_enabled() else backward)(ctx, *grads)
+
+    return run
+
+
+def _like(grad, dtype):
+    """A gradient as the kernels take it: contiguous, of this type; None stays None."""
+    if grad is None or grad.dtype is dtype and grad.is_contiguous():
+        return grad
+    return grad.to(dtype).contiguous()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> None:
@@ -592,6 +619,13 @@ def _scan_bwd(x, log_alpha, d_h, cu, h0, dhT, checkpoints, need_dx, need_dlog_al
         checkpoints = _scan_fwd(x, log_alpha, cu, h0, False, None, None, None, False, True)[2]
     else:
         _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
+    return _scan_grads(x, log_alpha, d_h, cu, dhT, checkpoints, state, sizes, need_dx,
+                       need_dlog_alpha, need_dh0)
+
+
+def _scan_grads(x, log_alpha, d_h, cu, dhT, checkpoints, state, sizes, need_dx, need_dlog_alpha,
+                need_dh0):
+    dev = x.device
     dx = torch.empty_like(x) if need_dx else None
     da = torch.empty_like(log_alpha) if need_dlog_alpha else None
     dh0 = torch.empty(state, dtype=torch.float32, device=dev) if need_dh0 else None
@@ -675,19 +709,20 @@ class _GlaScan(torch.autograd.Function):
         h, hT, ckpt = _scan_fwd(x, log_alpha, cu, h0, True, None, None, None,
                                 with_checkpoints=True)
         ctx.save_for_backward(x, log_alpha, ckpt)
-        ctx.cu = cu
+        ctx.cu, ctx.sizes = cu, _scan_sizes(x, cu)[2]
         return h, hT
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, d_h, dhT):
         x, log_alpha, ckpt = ctx.saved_tensors
         if d_h is None and dhT is None:
             return None, None, None, None
-        d_h = None if d_h is None else d_h.to(x.dtype).contiguous()
-        dhT = None if dhT is None else dhT.float().contiguous()
-        return *_scan_bwd(x, log_alpha, d_h, ctx.cu, None, dhT, ckpt,
-                          *ctx.needs_input_grad[:3]), None
+        need = ctx.needs_input_grad
+        lead = ckpt.shape[:-2] if ctx.cu is None else (len(ctx.cu) - 1, *ckpt.shape[:-2])
+        return (*_scan_grads(x, log_alpha, _like(d_h, x.dtype), ctx.cu, _like(dhT, torch.float32),
+                             ckpt, (*lead, x.shape[-1]), ctx.sizes, need[0], need[1], need[2]),
+                None)
 
 
 def gla_scan(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None):
@@ -732,7 +767,7 @@ _NORMS = {"rms": _lib.GLA_NORM_RMS, "l2": _lib.GLA_NORM_L2}
 def _qk_structs(*args):
     """The C call's layout and options for these strides and options."""
     return (ctypes.byref(_lib.GlaQkLayout(*args[:7])),
-            ctypes.byref(_lib.GlaQkOptions(dtype=args[7], norm=args[8], interleaved=args[9],
+            ctypes.byref(_lib.GlaQkOptions(dtype=args[7], norm=args[8], interleaved=int(args[9]),
                                            eps=args[10])))
 
 
@@ -742,18 +777,19 @@ def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interlea
     for t, name in ((q, "q"), (k, "k")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda or t.device != q.device:
-            raise ValueError(f"{name} must be on the CUDA device of q")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [B, T, H, d]")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}'s last dimension must be contiguous")
-    dev, (B, T, Hq, d), Hk = q.device, q.shape, k.shape[2]
-    dtype = _dtype(q, "q")
+    dev, dtype = q.device, _dtype(q, "q")
+    qn, kn, qs, ks = q.shape, k.shape, q.stride(), k.stride()
+    if not q.is_cuda or k.device != dev:
+        raise ValueError("q and k must be on the same CUDA device")
+    if len(qn) != 4 or len(kn) != 4:
+        raise ValueError("q and k must be [B, T, H, d]")
+    if qs[3] != 1 or ks[3] != 1:
+        raise ValueError("the last dimension of q and k must be contiguous")
+    B, T, Hq, d = qn
     if k.dtype is not q.dtype:
         raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
-    if k.shape != (B, T, Hk, d):
-        raise ValueError(f"k must have shape {(B, T, Hk, d)}, got {tuple(k.shape)}")
+    if kn[0] != B or kn[1] != T or kn[3] != d:
+        raise ValueError(f"k must have shape {(B, T, kn[2], d)}, got {tuple(kn)}")
     if norm not in _NORMS:
         raise ValueError("norm must be 'rms' or 'l2'")
     if q_weight is not None:
@@ -770,10 +806,20 @@ def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interlea
         _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
         pos_sb = 0 if one else T
     # a dimension of one entry is never stepped over, whatever its stride says
-    steps = [0 if n == 1 else st for t in (q, k) for n, st in zip(t.shape[:3], t.stride())]
-    structs = _qk_structs(*steps, pos_sb, dtype, _NORMS[norm], 1 if interleaved else 0, float(eps))
+    structs = _qk_structs(qs[0] if B != 1 else 0, qs[1] if T != 1 else 0, qs[2] if Hq != 1 else 0,
+                          ks[0] if B != 1 else 0, ks[1] if T != 1 else 0,
+                          ks[2] if kn[2] != 1 else 0, pos_sb, dtype, _NORMS[norm],
+                          bool(interleaved), eps)
     return ((q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-             _ptr(inv_freq)), (B, T, Hq, Hk, d, rot, *structs))
+             _ptr(inv_freq)), (B, T, Hq, kn[2], d, rot, *structs))
+
+
+def _qk_fwd(q, pointers, sizes):
+    B, T, Hq, Hk, d = sizes[:5]
+    q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
+    k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=q.device)
+    _call("gla_qk_norm_rope_fwd", q.device, *pointers, q_out.data_ptr(), k_out.data_ptr(), *sizes)
+    return q_out, k_out
 
 
 def gla_rope_frequencies(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -804,13 +850,8 @@ def gla_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tenso
     ``interleaved``.  ``positions`` is int64 ``[B, T]`` or ``[T]`` (None: 0 .. T-1).
     d and rot are multiples of 8, up to 256.
     """
-    pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
-                                interleaved)
-    B, T, Hq, Hk, d = sizes[:5]
-    q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device)
-    k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=q.device)
-    _call("gla_qk_norm_rope_fwd", q.device, *pointers, q_out.data_ptr(), k_out.data_ptr(), *sizes)
-    return q_out, k_out
+    return _qk_fwd(q, *_qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
+                                 interleaved))
 
 
 def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_k: torch.Tensor,
@@ -829,16 +870,21 @@ def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_
     pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
                                 interleaved)
     B, T, Hq, Hk, d = sizes[:5]
+    _need(d_q, "d_q", q.dtype, (B, Hq, T, d), q.device)
+    _need(d_k, "d_k", q.dtype, (B, Hk, T, d), q.device)
+    return _qk_grads(q, d_q, d_k, q_weight, k_weight, pointers, sizes, need_dweights)
+
+
+def _qk_grads(q, d_q, d_k, q_weight, k_weight, pointers, sizes, need_dweights):
+    B, T, Hq, Hk, d = sizes[:5]
     dev = q.device
-    _need(d_q, "d_q", q.dtype, (B, Hq, T, d), dev)
-    _need(d_k, "d_k", q.dtype, (B, Hk, T, d), dev)
     dq = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
     dk = torch.empty((B, T, Hk, d), dtype=q.dtype, device=dev)
     dwq = torch.empty_like(q_weight) if q_weight is not None and need_dweights else None
     dwk = torch.empty_like(k_weight) if k_weight is not None and need_dweights else None
     scratch, size = None, 0
     if dwq is not None or dwk is not None:
-        size = _lib.lib().gla_qk_norm_rope_bwd_scratch(d)
+        size = _entry("gla_qk_norm_rope_bwd_scratch")(d)
         scratch = torch.empty(size, dtype=torch.uint8, device=dev)
     _call("gla_qk_norm_rope_bwd", dev, *pointers, d_q.data_ptr(), d_k.data_ptr(), dq.data_ptr(),
           dk.data_ptr(), _ptr(dwq), _ptr(dwk), *sizes, _ptr(scratch), size)
@@ -847,19 +893,22 @@ def gla_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_
 
 class _GlaQkNormRope(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, kw):
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+        pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
+                                    interleaved)
         ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-        ctx.kw = kw
-        return gla_qk_norm_rope_fwd(q, k, q_weight, k_weight, positions, inv_freq, **kw)
+        ctx.sizes = sizes
+        return _qk_fwd(q, pointers, sizes)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, d_q, d_k):
-        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
-        dq, dk, dwq, dwk = gla_qk_norm_rope_bwd(
-            q, k, d_q.to(q.dtype).contiguous(), d_k.to(q.dtype).contiguous(), wq, wk, positions,
-            inv_freq, need_dweights=any(ctx.needs_input_grad[2:4]), **ctx.kw)
-        return dq, dk, dwq, dwk, None, None, None
+        saved = ctx.saved_tensors
+        q, wq, wk = saved[0], saved[2], saved[3]
+        need = ctx.needs_input_grad
+        grads = _qk_grads(q, _like(d_q, q.dtype), _like(d_k, q.dtype), wq, wk,
+                          [_ptr(t) for t in saved], ctx.sizes, need[2] or need[3])
+        return (*grads, None, None, None, None, None)
 
 
 def gla_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None = None,
@@ -867,8 +916,8 @@ def gla_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | 
                      inv_freq: torch.Tensor | None = None, *, norm: str = "rms",
                      eps: float = 1e-6, interleaved: bool = False):
     """Differentiable ``gla_qk_norm_rope_fwd``: gradients of q, k and the weights."""
-    return _GlaQkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq,
-                                {"norm": norm, "eps": eps, "interleaved": interleaved})
+    return _GlaQkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
+                                interleaved)
 
 
 def gla_last_device_status(device: torch.device | int | None = None) -> int:

@@ -242,7 +242,7 @@ def sequences(cu, H):
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("H", [None, 3])
-@pytest.mark.parametrize("D", [36, 130, 33])
+@pytest.mark.parametrize("D", [36, 130, 33, 72, 128])
 def test_packed(D, H, dtype):
     x, la, h0, d, dT, cu = packed([5, 0, 1, 64, 300, 65, 0, 1, 700], H, D, dtype, seed=D)
     ck = gla.gla_scan_checkpoints(x, cu)
@@ -258,6 +258,52 @@ def test_packed(D, H, dtype):
         check_forward(*one, h[rows], hT[state], f"sequence {state}")
         check_backward(*one, d[rows], dT[state], (grads[0][rows], grads[1][rows], grads[2][state]),
                        f"sequence {state}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("D", [8, 40, 44, 64, 200, 21])
+def test_packed_long_and_short(D, dtype):
+    """Long sequences among short ones: blocks side by side in time whose tiles end in the
+    next sequence, or lie beyond the end."""
+    x, la, h0, d, dT, cu = packed([2, 4000, 0, 129, 6001, 1, 128, 2500], None, D, dtype, seed=D)
+    ck = gla.gla_scan_checkpoints(x, cu)
+    h, hT = gla.gla_scan_fwd_varlen(x, la, cu, h0, checkpoints=ck)
+    grads = gla.gla_scan_bwd_varlen(x, la, d, cu, h0, dT, checkpoints=ck)
+    for rows, state, length in sequences(cu, None):
+        if length:
+            one = [x[rows], la[rows], h0[state]]
+            check_forward(*one, h[rows], hT[state], f"sequence {state}")
+            check_backward(*one, d[rows], dT[state],
+                           (grads[0][rows], grads[1][rows], grads[2][state]), f"sequence {state}")
+
+
+@pytest.mark.parametrize("T,D", [(1000, 32), (5000, 8), (20000, 16), (700, 1024)])
+def test_state_in_place_over_many_blocks(T, D):
+    x, la, h0, _, _ = make((1,), T, D)
+    h, hT = gla.gla_scan_fwd(x, la, h0)
+    for _ in range(20):
+        state = h0.clone()
+        got, last = gla.gla_scan_fwd(x, la, state, final_state=state)
+        assert torch.equal(got, h) and torch.equal(last, hT)
+
+
+def test_only_what_is_asked_for_is_written():
+    x, la, h0, d, dT = make((2,), 333, 64)
+    whole, hT = gla.gla_scan_fwd(x, la, h0)
+    ck = gla.gla_scan_checkpoints(x)
+    none, last = gla._scan_fwd(x, la, None, h0, True, None, None, ck, write_h=False)
+    assert none is None and torch.equal(last, hT)
+    for dtype_of, size in ((torch.bfloat16, x.numel()), (torch.float32, x.numel())):
+        guard = torch.full((size + 256,), 7.0, dtype=dtype_of, device=DEV)
+        out = guard[128:128 + size].view(x.shape)
+        if dtype_of is torch.bfloat16:
+            gla.gla_scan_fwd(x, la, h0, out=out)
+            assert torch.equal(out, whole)
+        else:
+            xf = x.float()
+            gla.gla_scan_fwd(xf, la, h0, out=out)
+            check_forward(xf, la, h0, out, None, "guarded")
+        assert (guard[:128] == 7).all() and (guard[128 + size:] == 7).all()
 
 
 def test_packed_without_states():
