@@ -6,9 +6,12 @@
 // registers, its threads a few tokens each; each maps the state before its tokens to
 // the state after them, and these maps are joined over the block and, where few
 // sequences leave the device idle, over a cluster of blocks that stand side by side
-// in time.  The blocks walk the sequence together, tile after tile.  No block waits
-// for another but at its cluster's barrier, nothing is added in an order that the
-// scheduler chooses, and no memory but the arguments is used.
+// in time.  The blocks walk the sequence together, tile after tile.  A block waits for
+// others of its own cluster only (and never longer than the library's limit), nothing is
+// added in an order that the scheduler chooses, and no memory but the arguments is used.
+//
+// Both directions are bound by HBM: 8 bytes an element forward (bf16 x, fp32 gates, bf16
+// h), 14 backward, against about 20 instructions.  @FIG@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -316,24 +319,27 @@ __device__ __forceinline__ void exchange_send(Exchange<CH> &x, int b, unsigned r
                      : "memory");
 }
 
+__device__ __forceinline__ bool exchange_done(uint64_t *bar, unsigned parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // Waits for every block's pairs of buffer b, the n-th tile that uses it.  After a wait that
 // ran out (`*dead`) no other is made: the status word says so, the results are
 // unspecified, and every block still comes to its end.
 template <int CH>
-__device__ __forceinline__ void exchange_wait(Exchange<CH> &x, int b, unsigned n, unsigned cl,
-                                              bool *dead, unsigned *status) {
-    if (*dead) return;
+__device__ __forceinline__ void exchange_wait(Exchange<CH> &x, int b, unsigned n, bool *dead,
+                                              unsigned *status) {
+    if (*dead || exchange_done(&x.bar[b], n & 1)) return;
     const unsigned long long start = global_timer_ns();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_u32(&x.bar[b])), "r"(n & 1)
-            : "memory");
-        if (done) return;
+    while (!exchange_done(&x.bar[b], n & 1)) {
         if (global_timer_ns() - start > kWaitLimitNs) {
             atomicOr(status, kStatusTimeout);
             *dead = true;
@@ -363,7 +369,7 @@ template <int STAGES>
 __device__ __forceinline__ void copies_drain(uint64_t *bars, unsigned tiles, unsigned *status) {
     for (int i = 0; i < STAGES; ++i)
         if (tiles > static_cast<unsigned>(i))
-            mbar_wait_bounded(&bars[i], ((tiles - 1 - i) / STAGES) & 1, status);
+            mbar_wait_bounded(&bars[i], ((tiles - 1 - i) / (STAGES ? STAGES : 1)) & 1, status);
 }
 
 // One stage of the forward's queue: a tile of log_alpha and x as TMA lays it down.  Rows and
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     const auto enter = [&](unsigned k, float *start_of) {
         if (tid >= CH) return;
         const int b = k % kBuffers;
-        exchange_wait<CH>(s_x, b, k / kBuffers, o.cl, &dead, p.status);
+        exchange_wait<CH>(s_x, b, k / kBuffers, &dead, p.status);
         float start = carry;
         for (unsigned j = 0; j < o.cl; ++j) {
             const float2 q = s_x.pair[b][j][tid];
@@ -759,7 +765,7 @@ __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
     const auto enter = [&](unsigned k, float *start_of) {
         if (tid >= CH) return;
         const int b = k % kBuffers;
-        exchange_wait<CH>(s_x, b, k / kBuffers, o.cl, &dead, p.status);
+        exchange_wait<CH>(s_x, b, k / kBuffers, &dead, p.status);
         float start = carry;
         for (unsigned j = o.cl; j-- > 0;) {
             const float2 q = s_x.pair[b][j][tid];
@@ -879,7 +885,6 @@ __global__ void __launch_bounds__(256)
     store<VEC>(h + i, s);
     store<VEC>(out + i, s);
 }
-
 
 // Whether every address is a multiple of `n` bytes (a null pointer is).
 template <typename... P>
