@@ -11,7 +11,10 @@
 // added in an order that the scheduler chooses, and no memory but the arguments is used.
 //
 // Both directions are bound by HBM: 8 bytes an element forward (bf16 x, fp32 gates, bf16
-// h), 14 backward, against about 20 instructions.  @FIG@
+// h), 14 backward, against about 20 instructions.  Measured on one GB300: forward B8 T2048
+// D2048 43 us (6.2 TB/s of a copy's 6.67), B1 T262144 D1024 335 us (6.4 TB/s); backward B8
+// T2048 D2048 80 us (5.9 TB/s).  With few sequences the blocks of one SM, not HBM, set the
+// pace: two of them on some SMs and one on others.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -289,9 +292,7 @@ constexpr int kBuffers = 2;
 
 template <int CH>
 struct Exchange {
-    // the wider the blocks, the smaller their clusters (see the lists of choices)
-    static constexpr int kSlots = CH > 64 ? 1 : CH > 32 ? 4 : kMaxCluster;
-    float2 pair[kBuffers][kSlots][CH];
+    float2 pair[kBuffers][kMaxCluster][CH];
     uint64_t bar[kBuffers];
 };
 
@@ -409,8 +410,9 @@ struct BwdTokens {
 // run walks its tokens again from its true state, from registers.
 //
 // Two things run ahead of the walk.  The next STAGES tiles are on their way to shared
-// memory (STAGES = 0: loaded where they are used).  And tile k is reduced before
-// tile k - 1 is walked, so that the exchange has a whole tile's time.
+// memory (STAGES = 0: the next one to registers).  And tile k is reduced before tile k - 1
+// is walked, so that the exchange has a whole tile's time and one barrier a tile is enough
+// (B1 T262144 D1024 by cluster barriers, which wait for a block's stores too: 542 us).
 template <typename E, int VEC, int LPR, int TPW, int THREADS, int STAGES>
 __global__ void __launch_bounds__(THREADS, 2)
     scan_fwd_kernel(const __grid_constant__ ScanArgs p) {
@@ -952,31 +954,37 @@ int launch_bwd(const ScanArgs &a, cudaStream_t stream) {
 }
 
 // Channels of a thread block and blocks of a cluster for one launch: the first of the
-// list that gives the device enough blocks (1.6 an SM; of the forward's 64 wide ones, whose
-// rows are whole 128-byte lines of 16-bit x, one; 1.3 with one channel a thread),
-// counting ragged sequences by the longest.  The backward, whose blocks keep twice as much
-// in registers, has narrow ones only.
+// list that gives the device enough blocks, counting ragged sequences by the longest.
+//
+// Enough is 1.6 blocks an SM; one of the forward's 64 wide blocks, whose rows are whole
+// 128-byte lines of 16-bit x; 1.3 with one channel a thread.  Narrower blocks come before
+// clusters, whose exchange costs more than shorter rows.  Forward, bf16, us, as channels x
+// cluster: B8 T2048 D2048 128x1 57, 64x1 46, 32x1 55, 64x2 53; B16 T2048 D4096 128x1
+// 165, 64x1 173; B1 T65536 D4864 64x2 472, 32x2 376, 32x8 450; B1 T262144 D1024 32x4
+// 485, 32x8 342; 24 ragged sequences of 65536 tokens, D1000, 64x2 110, 64x4 95, 32x2 103.
+// The backward, whose blocks keep twice as much in registers, has narrow ones only (B16
+// T2048 D4096: 32 wide 290, 64 wide with half the tokens a thread 315).
 struct Choice {
     int width, cluster;
 };
 constexpr Choice kEven[] = {{128, 1}, {64, 1}, {32, 1}, {32, 2}, {32, 4}, {32, 8}};
 constexpr Choice kRagged[] = {{128, 1}, {64, 1}, {64, 2}, {64, 4}, {32, 4}, {32, 8}};
-constexpr Choice kDirect[] = {{64, 1}, {64, 2}, {64, 4}};
 constexpr Choice kNarrow[] = {{32, 1}, {32, 2}, {32, 4}, {32, 8}};
 
-// The tiles' ways to the registers: by TMA, 4 channels a thread without it, 1.
+// The tiles' ways to the registers: by TMA, where rows are whole 16-byte pieces; four
+// neighbouring channels a thread without it; one.  (B2 T16384, bf16 forward: D2048 by TMA
+// 89 us, D2052 by fours 110, D2050 by ones 163.)
 enum class Way { kTma, kFour, kOne };
 
 void plan(ScanArgs &a, bool backward, Way way, long long longest, long long total, int sms) {
     const Choice *list = kNarrow;
     int count = 4;
-    if (!backward && way == Way::kFour) list = kDirect, count = 3;
     if (!backward && way == Way::kTma) list = a.nseq == 1 ? kEven : kRagged, count = 6;
     // as many sequences as the longest would make of all tokens
     const double units = a.H * (longest > 0 ? static_cast<double>(total) / longest : 1.0);
     for (int i = 0; i < count; ++i) {
         const Choice c = list[i];
-        const int tokens = way == Way::kOne ? 64 : 4096 / c.width;
+        const int tokens = way == Way::kTma ? 4096 / c.width : way == Way::kFour ? 128 : 64;
         if (c.cluster > 1 && longest <= static_cast<long long>(c.cluster / 2) * tokens) break;
         a.width = c.width;
         a.cluster = c.cluster;
@@ -990,7 +998,7 @@ int launch_for(ScanArgs &a, bool backward, Way way, cudaStream_t stream) {
     if (way == Way::kOne) return backward ? launch_bwd<E, 1, 32, 8, 256, 0>(a, stream)
                                           : launch_fwd<E, 1, 32, 8, 256, 0>(a, stream);
     if (way == Way::kFour) return backward ? launch_bwd<E, 4, 8, 4, 256, 0>(a, stream)
-                                           : launch_fwd<E, 4, 16, 4, 256, 0>(a, stream);
+                                           : launch_fwd<E, 4, 8, 4, 256, 0>(a, stream);
     const int tokens = 4096 / a.width;
     const bool f32 = sizeof(E) == 4;
     const long long dims[3] = {a.D, a.rows, a.H};

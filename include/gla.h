@@ -1,6 +1,9 @@
 /*
  * gla.h — C ABI of the GB300 (sm_103a) gated linear attention library: the
- * chunked forward, its backward, and the decode step.
+ * chunked forward, its backward, and the decode step; and, further down, the
+ * gated delta rule, the gated linear recurrence of one value per channel
+ * (gla_scan_*), and the norms of q and k with their rotation by position
+ * (gla_qk_norm_rope_*).  What follows here is about the first.
  *
  * The operation (from "Gated Linear Attention (GLA): Mathematical Foundations,
  * Data-Dependent Gating, Chunkwise Parallel Forms, and Sub-Quadratic Sequence
@@ -458,15 +461,19 @@ enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
  *
  * h is kept in fp32 from the first token to the last, and each h_t is rounded
  * once to dtype as it is stored.  The results do not depend on the order in
- * which the GPU runs the work: equal calls give equal bits.  No scratch, no
- * atomics.  h may be NULL when checkpoints or hT is asked for.  No other output
- * may overlap an input.
+ * which the GPU runs the work: equal calls give equal bits.  The calls use no
+ * scratch.  h may be NULL when checkpoints or hT is asked for.  No other output
+ * may overlap an input.  A bounded device wait that expires leaves the outputs
+ * unspecified and is reported by gla_last_device_status (GLA_ERR_TIMEOUT).
+ * Accuracy: with M the recurrence on |x|, |h0| and N the recurrence on M,
+ * |h - exact| <= 2^-24 (4 N + 8 M) before the rounding to dtype.
  *
- * Any D >= 1 and T >= 1, pointers aligned to their elements.  With D a multiple
- * of 4 and every pointer at a multiple of 16 bytes, 4 channels are taken at a
- * time; other calls take one and are slower.  Returns GLA_ERR_ARG for null
- * required pointers, non-positive sizes, an unknown dtype, misaligned pointers
- * or more than 2^31 thread blocks of work.
+ * Any D >= 1 and T >= 1, pointers aligned to their elements.  Fastest with every
+ * pointer at a multiple of 16 bytes and D a multiple of 8 (4 for GLA_F32), next
+ * with D a multiple of 4; other calls take one channel at a time and need up to
+ * twice the time.  Returns GLA_ERR_ARG for null required pointers, non-positive
+ * sizes, an unknown dtype, misaligned pointers or more than 2^31 thread blocks
+ * of work.
  */
 #define GLA_SCAN_BLOCK 64
 int gla_scan_fwd(const void *x, const float *log_alpha, const float *h0, void *h, float *hT,
