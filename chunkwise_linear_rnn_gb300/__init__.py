@@ -73,10 +73,28 @@ def _once(backward):
 
 
 def _like(grad, dtype):
-    """A gradient as the kernels take it: contiguous, of this type; None stays None."""
-    if grad is None or grad.dtype is dtype and grad.is_contiguous():
-        return grad
-    return grad.to(dtype).contiguous()
+    """A gradient as the kernels take it: contiguous, of this type, at a multiple of 16 bytes;
+    None stays None."""
+    if grad is None:
+        return None
+    if grad.dtype is not dtype or not grad.is_contiguous():
+        grad = grad.to(dtype).contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
+def _apart(out, name: str, *inputs) -> None:
+    """Refuses an output that the caller gave and that shares memory with an input."""
+    first, last = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and first < t.data_ptr() + t.numel() * t.element_size() and \
+                t.data_ptr() < last:
+            raise ValueError(f"{name} must not share memory with an input")
+
+
+def _ints(*sizes) -> None:
+    """Refuses sizes that the C calls' ints do not hold."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes must be below 2^31")
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> None:
@@ -566,6 +584,7 @@ def _scan_sizes(x: torch.Tensor, cu):
             raise ValueError("x must be [B, T, D] or [B, H, T, D]")
         lead, T, D = shape[:-2], shape[-2], shape[-1]
         H = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+        _ints(H, T, D)
         return (*lead, D), (*lead, -(-T // _lib.SCAN_BLOCK), D), (H, T, D, dtype)
     if len(shape) not in (2, 3):
         raise ValueError("x must be [T_total, D] or [H, T_total, D]")
@@ -575,6 +594,7 @@ def _scan_sizes(x: torch.Tensor, cu):
     if cu[0] != 0 or cu[-1] != T or any(b < a for a, b in zip(cu, cu[1:])):
         raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
     lead = shape[:-2]
+    _ints(T, D, *lead)
     blocks = sum(-(-(b - a) // _lib.SCAN_BLOCK) for a, b in zip(cu, cu[1:]))
     sizes = ((ctypes.c_int * len(cu))(*cu), N, lead[0] if lead else 1, T, D, dtype)
     return (N, *lead, D), (*lead, blocks, D), sizes
@@ -590,17 +610,21 @@ def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkp
         _need(h0, "h0", torch.float32, state, dev)
     if out is not None:
         _need(out, "out", x.dtype, x.shape, dev)
+        _apart(out, "out", x, log_alpha, h0)
     elif write_h:
         out = torch.empty_like(x)
     hT = final_state if output_final_state else None
     if hT is not None:
         _need(hT, "final_state", torch.float32, state, dev)
+        _apart(hT, "final_state", x, log_alpha, None if h0 is None or
+               h0.data_ptr() == hT.data_ptr() else h0)
     elif output_final_state:
         hT = torch.empty(state, dtype=torch.float32, device=dev)
     if with_checkpoints:
         checkpoints = torch.empty(ckpt, dtype=torch.float32, device=dev)
     elif checkpoints is not None:
         _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
+        _apart(checkpoints, "checkpoints", x, log_alpha, h0)
     _call("gla_scan_fwd" if cu is None else "gla_scan_fwd_varlen", dev, x.data_ptr(),
           log_alpha.data_ptr(), _ptr(h0), _ptr(out), _ptr(hT), _ptr(checkpoints), *sizes)
     return (out, hT, checkpoints) if with_checkpoints else (out, hT)
@@ -619,13 +643,6 @@ def _scan_bwd(x, log_alpha, d_h, cu, h0, dhT, checkpoints, need_dx, need_dlog_al
         checkpoints = _scan_fwd(x, log_alpha, cu, h0, False, None, None, None, False, True)[2]
     else:
         _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
-    return _scan_grads(x, log_alpha, d_h, cu, dhT, checkpoints, state, sizes, need_dx,
-                       need_dlog_alpha, need_dh0)
-
-
-def _scan_grads(x, log_alpha, d_h, cu, dhT, checkpoints, state, sizes, need_dx, need_dlog_alpha,
-                need_dh0):
-    dev = x.device
     dx = torch.empty_like(x) if need_dx else None
     da = torch.empty_like(log_alpha) if need_dlog_alpha else None
     dh0 = torch.empty(state, dtype=torch.float32, device=dev) if need_dh0 else None
@@ -657,7 +674,8 @@ def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | No
     shape in fp32, <= 0 (-inf is a gate of zero); ``h0`` ``[B, D]`` / ``[B, H, D]``
     fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
     fp32 on the way, and the last one in fp32 (None when ``output_final_state`` is
-    False).  ``final_state`` may be ``h0`` itself.  ``checkpoints`` (from
+    False).  ``final_state`` may be ``h0`` itself; no other output may share memory
+    with an input.  ``checkpoints`` (from
     ``gla_scan_checkpoints``) is filled for ``gla_scan_bwd``.
     """
     return _scan_fwd(x, log_alpha, None, h0, output_final_state, out, final_state, checkpoints)
@@ -709,7 +727,7 @@ class _GlaScan(torch.autograd.Function):
         h, hT, ckpt = _scan_fwd(x, log_alpha, cu, h0, True, None, None, None,
                                 with_checkpoints=True)
         ctx.save_for_backward(x, log_alpha, ckpt)
-        ctx.cu, ctx.sizes = cu, _scan_sizes(x, cu)[2]
+        ctx.cu = cu
         return h, hT
 
     @staticmethod
@@ -718,11 +736,9 @@ class _GlaScan(torch.autograd.Function):
         x, log_alpha, ckpt = ctx.saved_tensors
         if d_h is None and dhT is None:
             return None, None, None, None
-        need = ctx.needs_input_grad
-        lead = ckpt.shape[:-2] if ctx.cu is None else (len(ctx.cu) - 1, *ckpt.shape[:-2])
-        return (*_scan_grads(x, log_alpha, _like(d_h, x.dtype), ctx.cu, _like(dhT, torch.float32),
-                             ckpt, (*lead, x.shape[-1]), ctx.sizes, need[0], need[1], need[2]),
-                None)
+        # checked again: what was saved may come back elsewhere (hooks on saved tensors)
+        return (*_scan_bwd(x, log_alpha, _like(d_h, x.dtype), ctx.cu, None,
+                           _like(dhT, torch.float32), ckpt, *ctx.needs_input_grad[:3]), None)
 
 
 def gla_scan(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | None = None):
@@ -755,8 +771,10 @@ def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
     else:
         _need(out, "out", x.dtype, shape, dev)
     D = shape[-1]
+    B = h.numel() // max(D, 1)
+    _ints(B, D)
     _call("gla_scan_step", dev, x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), out.data_ptr(),
-          h.numel() // max(D, 1), D, dtype)
+          B, D, dtype)
     return out
 
 
@@ -798,6 +816,8 @@ def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interlea
         _need(k_weight, "k_weight", torch.float32, (d,), dev)
     rot = 0
     if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor):
+            raise TypeError("inv_freq must be a torch.Tensor")
         rot = 2 * inv_freq.numel()
         _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
     pos_sb = 0
@@ -805,11 +825,12 @@ def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interlea
         one = isinstance(positions, torch.Tensor) and positions.dim() == 1
         _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
         pos_sb = 0 if one else T
+    _ints(B, T, Hq, kn[2], d, rot)
     # a dimension of one entry is never stepped over, whatever its stride says
     structs = _qk_structs(qs[0] if B != 1 else 0, qs[1] if T != 1 else 0, qs[2] if Hq != 1 else 0,
                           ks[0] if B != 1 else 0, ks[1] if T != 1 else 0,
                           ks[2] if kn[2] != 1 else 0, pos_sb, dtype, _NORMS[norm],
-                          bool(interleaved), eps)
+                          bool(interleaved), float(eps))
     return ((q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
              _ptr(inv_freq)), (B, T, Hq, kn[2], d, rot, *structs))
 
@@ -897,7 +918,7 @@ class _GlaQkNormRope(torch.autograd.Function):
         pointers, sizes = _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
                                     interleaved)
         ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
-        ctx.sizes = sizes
+        ctx.options = norm, eps, interleaved
         return _qk_fwd(q, pointers, sizes)
 
     @staticmethod
@@ -905,9 +926,11 @@ class _GlaQkNormRope(torch.autograd.Function):
     def backward(ctx, d_q, d_k):
         saved = ctx.saved_tensors
         q, wq, wk = saved[0], saved[2], saved[3]
+        # checked again: what was saved may come back with other strides (hooks on saved tensors)
+        pointers, sizes = _qk_sizes(*saved, *ctx.options)
         need = ctx.needs_input_grad
-        grads = _qk_grads(q, _like(d_q, q.dtype), _like(d_k, q.dtype), wq, wk,
-                          [_ptr(t) for t in saved], ctx.sizes, need[2] or need[3])
+        grads = _qk_grads(q, _like(d_q, q.dtype), _like(d_k, q.dtype), wq, wk, pointers, sizes,
+                          need[2] or need[3])
         return (*grads, None, None, None, None, None)
 
 

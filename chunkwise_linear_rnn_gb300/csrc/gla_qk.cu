@@ -565,7 +565,8 @@ int check(const QkArgs &a, const gla_qk_options &op) {
     if (!aligned(a.pos, 8) || !aligned(a.inv_freq, 8)) return GLA_ERR_ARG;
     if (a.B <= 0 || a.T <= 0 || a.H[0] <= 0 || a.H[1] <= 0 || a.d <= 0 || a.rot < 0)
         return GLA_ERR_ARG;
-    if (static_cast<long long>(a.H[0]) + a.H[1] > 0x7fffffffLL) return GLA_ERR_ARG;
+    // heads are counted on past the last in whole rounds of whole chunks
+    if (static_cast<long long>(a.H[0]) + a.H[1] > 1LL << 30) return GLA_ERR_ARG;
     if (op.dtype != GLA_BF16 && op.dtype != GLA_F32) return GLA_ERR_ARG;
     if (op.norm != GLA_NORM_RMS && op.norm != GLA_NORM_L2) return GLA_ERR_ARG;
     if (op.interleaved != 0 && op.interleaved != 1) return GLA_ERR_ARG;

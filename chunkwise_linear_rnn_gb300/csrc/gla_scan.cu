@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
+#include <new>
 #include <type_traits>
 #include <vector>
 
@@ -904,7 +905,7 @@ int check_common(const ScanArgs &a, long long states, int D, int dtype) {
     if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
     if (!elements_aligned(a, dtype)) return GLA_ERR_ARG;
     // thread blocks of the narrowest tiles in the longest clusters
-    if (states * ((D + 31LL) / 32) > 0x7fffffffLL / kMaxCluster) return GLA_ERR_ARG;
+    if (states > 0x7fffffffLL / kMaxCluster / ((D + 31LL) / 32)) return GLA_ERR_ARG;
     return GLA_OK;
 }
 
@@ -1020,7 +1021,12 @@ int run(ScanArgs &a, bool backward, const int *cu_seqlens, int N, int H, int T_t
     int st = check_common(a, static_cast<long long>(N) * H, D, dtype);
     if (st != GLA_OK) return st;
     if (cu_seqlens[0] != 0 || cu_seqlens[N] != T_total) return GLA_ERR_ARG;
-    std::vector<ScanSeq> seqs(N);
+    std::vector<ScanSeq> seqs;
+    try {
+        seqs.resize(N);
+    } catch (const std::bad_alloc &) {   // no exception crosses the C interface
+        return GLA_ERR_ALLOC;
+    }
     long long blocks = 0;
     for (int n = 0; n < N; ++n) {
         const long long len = static_cast<long long>(cu_seqlens[n + 1]) - cu_seqlens[n];

@@ -473,7 +473,7 @@ enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
  * with D a multiple of 4; other calls take one channel at a time and need up to
  * twice the time.  Returns GLA_ERR_ARG for null required pointers, non-positive
  * sizes, an unknown dtype, misaligned pointers or more than 2^31 thread blocks
- * of work.
+ * of work; GLA_ERR_ALLOC when the host has no memory for a packed batch's table.
  */
 #define GLA_SCAN_BLOCK 64
 int gla_scan_fwd(const void *x, const float *log_alpha, const float *h0, void *h, float *hT,
@@ -547,6 +547,7 @@ int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, in
  * to 256, rot a multiple of 8 up to d (GLA_ERR_SHAPE otherwise).  GLA_ERR_ARG for
  * null required pointers, non-positive sizes, eps not in (0, 1], unknown dtype,
  * norm or interleaved, strides that are negative or not multiples of 8 elements,
+ * more than 2^30 heads,
  * inputs or outputs that are not 16-byte aligned (positions and inv_freq: 8).
  * No output may overlap an input.
  */

@@ -4,6 +4,8 @@ a recurrent layer run one after another."""
 
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import pytest
 import torch
@@ -387,3 +389,40 @@ def test_a_layer_trains_and_decodes():
     # the chunked form and the step round o to bf16 from sums that differ by the forward's bar
     assert_close(stepped.float().cpu().numpy(), h.detach().double().cpu().numpy(), "decoded",
                  bf16_output=True)
+
+
+@pytest.mark.parametrize("fused", [False, True])
+def test_saved_tensors_that_were_moved_and_gradients_off_16_bytes(fused):
+    q, k, wq, wk, dq, dk = make(2, 33, 4, 2, 64, fused=fused)
+    f = gla.gla_rope_frequencies(32, device=DEV)
+
+    def grads(moved, shift):
+        a, b = q.detach().requires_grad_(), k.detach().requires_grad_()
+        ws = [w.clone().requires_grad_() for w in (wq, wk)]
+        with torch.autograd.graph.save_on_cpu() if moved else contextlib.nullcontext():
+            outs = gla.gla_qk_norm_rope(a, b, *ws, None, f)
+        pad = torch.zeros(shift, dtype=q.dtype, device=DEV)
+        return torch.autograd.grad([torch.cat([pad, o.flatten()]) for o in outs], [a, b, *ws],
+                                   [torch.cat([pad, d.flatten()]) for d in (dq, dk)])
+
+    want = grads(False, 0)
+    for got in (grads(True, 0), grads(False, 3)):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_options_are_taken_by_value():
+    q, k = make(1, 5, 2, 2, 64)[:2]
+    eps = torch.tensor(1e-6)
+    gla.gla_qk_norm_rope_fwd(q, k, eps=eps)
+    eps.fill_(0.5)
+    got, want = gla.gla_qk_norm_rope_fwd(q, k, eps=eps), gla.gla_qk_norm_rope_fwd(q, k, eps=0.5)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    one = torch.zeros(1, 1, 1, 8, device=DEV)
+    k = one.expand(1, 2 ** 31, 1, 8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gla.gla_qk_norm_rope_fwd(k, k)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gla.gla_qk_norm_rope_fwd(one, one.expand(1, 1, 2 ** 31, 8))

@@ -6,6 +6,8 @@ roundings; nothing here is compared by a fitted tolerance.
 
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import pytest
 import torch
@@ -555,3 +557,47 @@ def test_packed_refusals(cu):
     x, la, _, _, _ = make((), 40, 16)
     with pytest.raises(ValueError):
         gla.gla_scan_fwd_varlen(x, la, cu)
+
+
+@pytest.mark.parametrize("kind", ["out", "gates", "state", "checkpoints", "shifted"])
+def test_outputs_that_share_memory_with_inputs_are_refused(kind):
+    x, la, h0, _, _ = make((2,), 64, 32, F32)
+    both = torch.zeros(3 * 64 * 32, device=DEV)
+    kw = {"out": lambda: {"out": x}, "gates": lambda: {"out": la},
+          "state": lambda: {"final_state": x.view(-1)[:64].view(2, 32)},
+          "checkpoints": lambda: {"checkpoints": h0.view(2, 1, 32)},
+          "shifted": lambda: {"out": both[32:32 + x.numel()].view_as(x)}}[kind]()
+    src = both[:x.numel()].view_as(x) if kind == "shifted" else x
+    with pytest.raises(ValueError, match="share memory"):
+        gla.gla_scan_fwd(src, la, h0, **kw)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    one = torch.zeros(1, 1, 1, device=DEV)
+    for shape in ((1, 2 ** 31, 1), (2 ** 31, 1, 1), (1, 1, 2 ** 31)):
+        big = one.expand(shape)
+        with pytest.raises(ValueError, match="2\\^31"):
+            gla.gla_scan_fwd(big, big)
+    with pytest.raises(ValueError, match="2\\^31"):
+        gla.gla_scan_fwd_varlen(one[0].expand(2 ** 31, 1), one, [0, 2 ** 31])
+
+
+@pytest.mark.parametrize("cu", [None, [0, 3, 40]])
+def test_saved_tensors_that_were_moved_and_gradients_off_16_bytes(cu):
+    x, la, h0, d, dT = (t[0] for t in make((1,), 40, 64))
+    h0, dT = (torch.stack([t] * (len(cu) - 1)) if cu else t[None] for t in (h0, dT))
+    if not cu:
+        x, la, d = x[None], la[None], d[None]
+
+    def grads(moved, shift):
+        leaves = [t.clone().requires_grad_() for t in (x, la, h0)]
+        with torch.autograd.graph.save_on_cpu() if moved else contextlib.nullcontext():
+            h, hT = gla.gla_scan(*leaves) if cu is None else gla.gla_scan_varlen(
+                leaves[0], leaves[1], cu, leaves[2])
+        flat = torch.cat([torch.zeros(shift, dtype=h.dtype, device=DEV), h.flatten()])
+        w = torch.cat([torch.zeros(shift, dtype=h.dtype, device=DEV), d.flatten()])
+        return torch.autograd.grad([flat, hT], leaves, [w, dT])
+
+    want = grads(False, 0)
+    for got in (grads(True, 0), grads(False, 3)):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

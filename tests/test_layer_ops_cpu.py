@@ -5,6 +5,8 @@ from __future__ import annotations
 
 import ctypes
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -147,6 +149,34 @@ def test_valid_arguments_reach_the_device_check(lib):
                  lib.gla_scan_fwd_varlen(None, None, P, None, P, None, _cu(0, 0), 1, 1, 0, 8, 0,
                                          None)):
         assert call == _lib.GLA_ERR_DEVICE
+
+
+def test_sizes_whose_products_pass_64_bits_are_refused(lib):
+    most = 2 ** 31 - 1
+    assert lib.gla_scan_fwd_varlen(P, P, P, P, P, None, _cu(*[0] * 201), 200, most, 0, most, 0,
+                                   None) == _lib.GLA_ERR_ARG
+    assert _qk(lib, Hq=2 ** 30, Hk=1) == _lib.GLA_ERR_ARG
+    assert _qk_bwd(lib, Hq=1, Hk=2 ** 30) == _lib.GLA_ERR_ARG
+    with pytest.raises(ValueError):
+        gla._ints(4, 2 ** 31)
+
+
+NO_MEMORY = """
+import ctypes, resource, sys
+lib = ctypes.CDLL(sys.argv[1])
+n = 1 << 25
+cu = (ctypes.c_int * (n + 1))()
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (size + (64 << 20),) * 2)
+p = ctypes.c_void_p(1 << 20)
+print(lib.gla_scan_fwd_varlen(p, p, p, p, p, None, cu, n, 1, 0, 8, 0, None))
+"""
+
+
+def test_no_exception_leaves_the_library_without_memory(lib):
+    out = subprocess.run([sys.executable, "-c", NO_MEMORY, lib._name], capture_output=True,
+                         text=True, timeout=120)
+    assert (out.returncode, out.stdout.strip()) == (0, "6"), out.stderr   # GLA_ERR_ALLOC
 
 
 def test_structs_and_constants_match_the_header():
