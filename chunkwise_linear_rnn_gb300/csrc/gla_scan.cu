@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <new>
 #include <type_traits>
@@ -64,7 +65,10 @@ struct ScanArgs {
 // takes LPR * VEC neighbouring channels of TPW consecutive tokens, and the
 // block's runs follow one another in time, so that its tile is
 // (kThreads / LPR) * TPW tokens of LPR * VEC channels.
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
+
+// Blocks of a cluster of blocks of so many channels, at most.
+constexpr int cluster_of(int channels) { return channels == 32 ? kMaxCluster : channels == 64 ? 4 : 1; }
 
 template <int VEC, int LPR, int TPW, int THREADS>
 struct Tile {
@@ -293,7 +297,7 @@ constexpr int kBuffers = 2;
 
 template <int CH>
 struct Exchange {
-    float2 pair[kBuffers][kMaxCluster][CH];
+    float2 pair[kBuffers][cluster_of(CH)][CH];
     uint64_t bar[kBuffers];
 };
 
@@ -914,18 +918,18 @@ template <typename G, auto Kernel>
 int launch(const ScanArgs &a, size_t dynamic, cudaStream_t stream) {
     const long long units =
         static_cast<long long>(a.nseq) * a.H * ((a.D + G::kChannels - 1) / G::kChannels);
-    if (dynamic > 0) {
-        // once for each device
-        static std::atomic<unsigned long long> allowed{0};
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return static_cast<int>(cudaGetLastError());
-        const unsigned long long bit = 1ull << (dev & 63);
-        if (!(allowed.load(std::memory_order_acquire) & bit)) {
-            const cudaError_t e = cudaFuncSetAttribute(
-                Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(dynamic));
-            if (e != cudaSuccess) return static_cast<int>(e);
-            allowed.fetch_or(bit, std::memory_order_release);
-        }
+    // once for each device
+    static std::atomic<unsigned long long> allowed{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return static_cast<int>(cudaGetLastError());
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(allowed.load(std::memory_order_acquire) & bit)) {
+        cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(dynamic));
+        if (e == cudaSuccess)   // clusters of more than 8
+            e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return static_cast<int>(e);
+        allowed.fetch_or(bit, std::memory_order_release);
     }
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -954,43 +958,77 @@ int launch_bwd(const ScanArgs &a, cudaStream_t stream) {
         a, STAGES * sizeof(BwdStage<E, G::kChannels, G::kTokens>), stream);
 }
 
-// Channels of a thread block and blocks of a cluster for one launch: the first of the
-// list that gives the device enough blocks, counting ragged sequences by the longest.
-//
-// Enough is 1.6 blocks an SM; one of the forward's 64 wide blocks, whose rows are whole
-// 128-byte lines of 16-bit x; 1.3 with one channel a thread.  Narrower blocks come before
-// clusters, whose exchange costs more than shorter rows.  Forward, bf16, us, as channels x
-// cluster: B8 T2048 D2048 128x1 57, 64x1 46, 32x1 55, 64x2 53; B16 T2048 D4096 128x1
-// 165, 64x1 173; B1 T65536 D4864 64x2 472, 32x2 376, 32x8 450; B1 T262144 D1024 32x4
-// 485, 32x8 342; 24 ragged sequences of 65536 tokens, D1000, 64x2 110, 64x4 95, 32x2 103.
-// The backward, whose blocks keep twice as much in registers, has narrow ones only (B16
-// T2048 D4096: 32 wide 290, 64 wide with half the tokens a thread 315).
-struct Choice {
-    int width, cluster;
-};
-constexpr Choice kEven[] = {{128, 1}, {64, 1}, {32, 1}, {32, 2}, {32, 4}, {32, 8}};
-constexpr Choice kRagged[] = {{128, 1}, {64, 1}, {64, 2}, {64, 4}, {32, 4}, {32, 8}};
-constexpr Choice kNarrow[] = {{32, 1}, {32, 2}, {32, 4}, {32, 8}};
-
 // The tiles' ways to the registers: by TMA, where rows are whole 16-byte pieces; four
 // neighbouring channels a thread without it; one.  (B2 T16384, bf16 forward: D2048 by TMA
 // 89 us, D2052 by fours 110, D2050 by ones 163.)
 enum class Way { kTma, kFour, kOne };
 
-void plan(ScanArgs &a, bool backward, Way way, long long longest, long long total, int sms) {
-    const Choice *list = kNarrow;
-    int count = 4;
-    if (!backward && way == Way::kTma) list = a.nseq == 1 ? kEven : kRagged, count = 6;
-    // as many sequences as the longest would make of all tokens
-    const double units = a.H * (longest > 0 ? static_cast<double>(total) / longest : 1.0);
+// Channels of a thread block and blocks of a cluster.
+struct Choice {
+    int width, cluster;
+};
+constexpr Choice kChoices[] = {{32, 1}, {32, 2}, {32, 4}, {32, 8}, {32, 16},
+                               {64, 1}, {64, 2}, {64, 4}, {128, 1}};   // the forward's by TMA
+
+// A launch's work: tokens of the longest sequence and of all, sequences, heads, channels.
+struct Work {
+    double longest, total, nseq, heads;
+    int D, size;             // size: bytes of a value of x
+    bool backward;
+    Way way;
+};
+
+// The time of a launch in us, as far as it takes to choose: how long a block takes for a tile
+// (`alone` on its SM, or one of two there; or HBM's rate shared by all that run), times the
+// tiles, times the waves.  The figures are fits to 55 shapes, forward and backward, with
+// every choice measured; over 70 others the choices made were 1.5% slower than the best on
+// average, 24% at most.  (Forward, bf16, us, as channels x cluster: B8 T2048 D2048 128x1 54,
+// 64x1 44, 32x1 46, 32x2 55; B1 T262144 D1024 32x4 466, 32x8 333, 32x16 444; B2 T143060 D176
+// 32x8 131, 32x16 95; fp32 B7 T458 D1360 64x1 18, 32x1 9; fp32 16 ragged sequences of 20000
+// tokens, D1024, 32x4 59, 32x1 47.)
+double estimate(const Work &k, Choice c, int sms) {
+    const int run = k.way == Way::kTma ? 4096 / c.width : k.way == Way::kFour ? 128 : 64;
+    const double tokens = run * c.cluster;
+    const double blocks = k.nseq * k.heads * ((k.D + c.width - 1) / c.width) * c.cluster;
+    // blocks that run alone on an SM, and at once: large clusters do not fill every part of the chip
+    const double one = sms * (c.cluster < 8 ? 1.0 : 0.72);
+    const bool single = k.backward && (k.way == Way::kFour || (k.way == Way::kTma && k.size == 4));
+    const double most = single ? one : sms * (c.cluster < 8 ? 2.0 : c.cluster == 8 ? 1.9 : 1.35);
+    double alone, two;
+    if (k.way == Way::kTma) {
+        alone = k.backward ? 1.4 : 1.0;
+        two = k.backward ? 2.2 : 0.4 * (k.size + 2);
+    } else if (k.way == Way::kFour) {
+        alone = k.backward ? 1.5 : 1.1;
+        two = 1.6;   // the backward's blocks are always alone
+    } else {
+        alone = k.backward ? 1.5 : 0.9;
+        two = k.backward ? 2.4 : 1.4;
+    }
+    if (c.cluster > 1) alone *= 1.4;
+    const double bytes = run * c.width * (k.backward ? 8 + 3 * k.size : 4 + 2 * k.size) / 6.5e6;
+    const auto tile = [&](double n) { return std::max(n <= one ? alone : two, n * bytes); };
+    const double begin = 1.5 + (c.cluster > 1 ? 0.18 * c.cluster : 0.0);
+    const double tiles = std::ceil(k.longest / tokens);
+    if (k.nseq == 1) {
+        const double waves = std::floor(blocks / most), rest = blocks - waves * most;
+        return waves * (tiles * tile(most) + begin) + (rest > 0 ? tiles * tile(rest) + begin : 0.0);
+    }
+    // the longest sequence, or all of them shared by the blocks that run at once
+    const double n = std::min(blocks, most), first = tiles * alone + begin;
+    const double all = blocks / n * ((k.total / k.nseq / tokens + 0.5) * tile(n) + begin);
+    return std::max(first, all) + 0.25 * std::min(first, all);
+}
+
+void plan(ScanArgs &a, const Work &k, int sms) {
+    const int count = k.way == Way::kTma && !k.backward ? 9 : 5;
+    double least = 0.0;
     for (int i = 0; i < count; ++i) {
-        const Choice c = list[i];
-        const int tokens = way == Way::kTma ? 4096 / c.width : way == Way::kFour ? 128 : 64;
-        if (c.cluster > 1 && longest <= static_cast<long long>(c.cluster / 2) * tokens) break;
-        a.width = c.width;
-        a.cluster = c.cluster;
-        const double enough = way == Way::kOne ? 1.3 : c.width == 64 && c.cluster == 1 ? 1.0 : 1.6;
-        if (units * ((a.D + c.width - 1) / c.width) * c.cluster >= enough * sms) break;
+        const double t = estimate(k, kChoices[i], sms);
+        if (i > 0 && t >= least) continue;
+        least = t;
+        a.width = kChoices[i].width;
+        a.cluster = kChoices[i].cluster;
     }
 }
 
@@ -1054,7 +1092,10 @@ int run(ScanArgs &a, bool backward, const int *cu_seqlens, int N, int H, int T_t
         std::copy(seqs.begin() + n, seqs.begin() + n + a.nseq, a.seqs);
         long long total = 0;
         for (int i = 0; i < a.nseq; ++i) total += a.seqs[i].len;
-        plan(a, backward, way, seqs[n].len, total, sms);
+        const Work work = {static_cast<double>(seqs[n].len), static_cast<double>(total),
+                           static_cast<double>(a.nseq), static_cast<double>(H), D,
+                           dtype == GLA_BF16 ? 2 : 4, backward, way};
+        plan(a, work, sms);
         const int e = dtype == GLA_BF16 ? launch_for<__nv_bfloat16>(a, backward, way, stream)
                                         : launch_for<float>(a, backward, way, stream);
         if (e != 0) return GLA_ERR_LAUNCH;
