@@ -10,6 +10,8 @@
 // others of its own cluster only (and never longer than the library's limit), nothing is
 // added in an order that the scheduler chooses, and no memory but the arguments is used.
 //
+// Short sequences in numbers take neither tiles nor exchange: a thread walks its own.
+//
 // Both directions are bound by HBM: 8 bytes an element forward (bf16 x, fp32 gates, bf16
 // h), 14 backward, against about 20 instructions.  Measured on one GB300: forward B8 T2048
 // D2048 43 us (6.2 TB/s of a copy's 6.67), B1 T262144 D1024 335 us (6.4 TB/s); backward B8
@@ -227,6 +229,16 @@ __device__ __forceinline__ Vec<4> fma(Vec<4> a, Vec<4> b, Vec<4> c) {
 __device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {__fmul_rn(a.v, b.v)}; }
 __device__ __forceinline__ Vec<4> mul(Vec<4> a, Vec<4> b) {
     return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)};
+}
+// A product that no compiler joins with the sum that follows (it does join pairs').
+__device__ __forceinline__ Vec<1> mul_alone(Vec<1> a, Vec<1> b) { return mul(a, b); }
+__device__ __forceinline__ Vec<4> mul_alone(Vec<4> a, Vec<4> b) {
+    float x[4], y[4];
+    a.to(x);
+    b.to(y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __fmul_rn(x[i], y[i]);
+    return Vec<4>::of(x);
 }
 __device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {__fadd_rn(a.v, b.v)}; }
 __device__ __forceinline__ Vec<4> add(Vec<4> a, Vec<4> b) {
@@ -877,6 +889,137 @@ __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
     exchange_end(o.cl);
 }
 
+// Short sequences: a thread walks one by itself, VEC channels of it, kChunk tokens on their
+// way at a time.  No tile to fill, no exchange.
+constexpr int kChunk = 8;
+constexpr int kShortThreads = 64;
+
+struct ShortPlace {
+    int len;
+    size_t row, state, ck;   // elements: first row, state and checkpoint of its channels
+};
+
+template <int VEC>
+__device__ __forceinline__ bool short_place(const ScanArgs &p, ShortPlace &o) {
+    const unsigned i = blockIdx.x * kShortThreads + threadIdx.x;
+    const unsigned pieces = p.D / VEC, unit = i / pieces, c = (i % pieces) * VEC;
+    if (unit >= static_cast<unsigned>(p.nseq) * p.H) return false;
+    const unsigned head = unit % p.H;
+    const ScanSeq s = p.seqs[unit / p.H];
+    o.len = s.len;
+    o.row = (static_cast<size_t>(head) * p.rows + s.first) * p.D + c;
+    o.state = (static_cast<size_t>(s.n) * p.H + head) * p.D + c;
+    o.ck = (static_cast<size_t>(head) * p.blocks + s.block) * p.D + c;
+    return true;
+}
+
+template <typename E, int VEC>
+struct ShortChunk {
+    Raw<float, VEC> l[kChunk];
+    Raw<E, VEC> x[kChunk];
+    __device__ __forceinline__ void read(const ScanArgs &p, const ShortPlace &o, int t0) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            l[i] = Raw<float, VEC>{};
+            x[i] = Raw<E, VEC>{};
+            if (t0 + i >= o.len) continue;
+            const size_t at = o.row + static_cast<size_t>(t0 + i) * p.D;
+            l[i] = load<float, VEC>(p.log_alpha, at);
+            x[i] = load<E, VEC>(p.x, at);
+        }
+    }
+};
+
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kShortThreads)
+    scan_short_fwd_kernel(const __grid_constant__ ScanArgs p) {
+    using V = Vec<VEC>;
+    ShortPlace o;
+    if (!short_place<VEC>(p, o)) return;
+    ShortChunk<E, VEC> c;
+    c.read(p, o, 0);
+    V h = p.h0 ? fetch_vec<VEC>(p.h0 + o.state) : V::all(0.f);
+    for (int t0 = 0; t0 < o.len; t0 += kChunk) {
+        if (p.ckpt_out && t0 % kBlock == 0)
+            store_vec<VEC>(p.ckpt_out + o.ck + static_cast<size_t>(t0 / kBlock) * p.D, h);
+        V a[kChunk], x[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) a[i] = gate<VEC>(c.l[i]), x[i] = widen(c.x[i]);
+        c.read(p, o, t0 + kChunk);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            h = fma(a[i], h, x[i]);
+            if (p.h && t0 + i < o.len)
+                store_vec<VEC>(static_cast<E *>(p.h) + (o.row + static_cast<size_t>(t0 + i) * p.D), h);
+        }
+    }
+    if (p.hT) store_vec<VEC>(p.hT + o.state, h);
+}
+
+// Backward, a block of the checkpoints after another from the end: the states that enter its
+// chunks first, then the chunks from the last.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(kShortThreads)
+    scan_short_bwd_kernel(const __grid_constant__ ScanArgs p) {
+    using V = Vec<VEC>;
+    ShortPlace o;
+    if (!short_place<VEC>(p, o)) return;
+    V u = p.dhT ? fetch_vec<VEC>(p.dhT + o.state) : V::all(0.f);
+    for (int base = (o.len - 1) / kBlock * kBlock; base >= 0 && o.len > 0; base -= kBlock) {
+        const int chunks = (min(o.len - base, kBlock) + kChunk - 1) / kChunk;
+        ShortChunk<E, VEC> c;
+        Raw<E, VEC> d[kChunk];
+        const auto read_d = [&](int t0) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                d[i] = Raw<E, VEC>{};
+                if (p.d_h && t0 + i < o.len)
+                    d[i] = load<E, VEC>(p.d_h, o.row + static_cast<size_t>(t0 + i) * p.D);
+            }
+        };
+        c.read(p, o, base);
+        V state[kBlock / kChunk];
+        state[0] = fetch_vec<VEC>(p.ckpt_in + o.ck + static_cast<size_t>(base / kBlock) * p.D);
+        for (int k = 0; k + 1 < chunks; ++k) {
+            V a[kChunk], x[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) a[i] = gate<VEC>(c.l[i]), x[i] = widen(c.x[i]);
+            c.read(p, o, base + (k + 1) * kChunk);
+            V h = state[k];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) h = fma(a[i], h, x[i]);
+            state[k + 1] = h;
+        }
+        read_d(base + (chunks - 1) * kChunk);
+        for (int k = chunks - 1; k >= 0; --k) {
+            const int t0 = base + k * kChunk;
+            V a[kChunk], before[kChunk], dd[kChunk];
+            V h = state[k];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                a[i] = gate<VEC>(c.l[i]);
+                before[i] = h;
+                h = fma(a[i], h, widen(c.x[i]));
+                dd[i] = widen(d[i]);
+            }
+            if (k > 0) {
+                c.read(p, o, t0 - kChunk);
+                read_d(t0 - kChunk);
+            }
+#pragma unroll
+            for (int i = kChunk - 1; i >= 0; --i) {
+                const V g = add(u, dd[i]);
+                u = mul_alone(a[i], g);
+                if (t0 + i >= o.len) continue;
+                const size_t at = o.row + static_cast<size_t>(t0 + i) * p.D;
+                if (p.h) store_vec<VEC>(static_cast<E *>(p.h) + at, g);
+                if (p.ga) store_vec<VEC>(p.ga + at, mul(u, before[i]));
+            }
+        }
+    }
+    if (p.hT) store_vec<VEC>(p.hT + o.state, u);
+}
+
 // The decode step: VEC values a thread, one pass over the state.
 template <typename E, int VEC>
 __global__ void __launch_bounds__(256)
@@ -1020,7 +1163,7 @@ double estimate(const Work &k, Choice c, int sms) {
     return std::max(first, all) + 0.25 * std::min(first, all);
 }
 
-void plan(ScanArgs &a, const Work &k, int sms) {
+double plan(ScanArgs &a, const Work &k, int sms) {
     const int count = k.way == Way::kTma && !k.backward ? 9 : 5;
     double least = 0.0;
     for (int i = 0; i < count; ++i) {
@@ -1030,6 +1173,17 @@ void plan(ScanArgs &a, const Work &k, int sms) {
         a.width = kChoices[i].width;
         a.cluster = kChoices[i].cluster;
     }
+    return least;
+}
+
+// The same for threads that walk a sequence each: a chunk after another, and HBM's rate.
+// (us, bf16, walks / tiles: forward B256 T1 D4096 10 / 59, B64 T64 D4096 28 / 32, B64 T256 D4096
+// 104 / 84, B1 T64 D2048 7.1 / 3.4; backward B256 T16 D4096 53 / 306, B64 T100 D4096 87 / 102,
+// B64 T400 D4096 329 / 272.  Over 190 shapes the faster of both but for 0.6% on average, 30% at most.)
+double walk_time(const Work &k) {
+    const double chunks = std::ceil(k.longest / kChunk);
+    const double bytes = k.heads * k.total * k.D * (k.backward ? 8 + 3 * k.size : 4 + 2 * k.size);
+    return 1.0 + chunks * (k.backward ? 1.35 : 0.55) + bytes * (k.backward ? 1.2 : 1.0) / 6.5e6;
 }
 
 template <typename E>
@@ -1049,6 +1203,18 @@ int launch_for(ScanArgs &a, bool backward, Way way, cudaStream_t stream) {
     if (a.width == 128) return launch_fwd<E, 4, 32, 4, 256, 3>(a, stream);
     if (a.width == 64) return launch_fwd<E, 4, 16, 4, 256, 3>(a, stream);
     return launch_fwd<E, 4, 8, 8, 128, 2>(a, stream);
+}
+
+template <typename E>
+int launch_short(const ScanArgs &a, bool backward, bool vec4, cudaStream_t stream) {
+    const long long threads = static_cast<long long>(a.nseq) * a.H * (vec4 ? a.D / 4 : a.D);
+    const unsigned grid = static_cast<unsigned>((threads + kShortThreads - 1) / kShortThreads);
+    const auto go = [&](auto kernel) {
+        kernel<<<grid, kShortThreads, 0, stream>>>(a);
+        return static_cast<int>(cudaGetLastError());
+    };
+    if (backward) return vec4 ? go(scan_short_bwd_kernel<E, 4>) : go(scan_short_bwd_kernel<E, 1>);
+    return vec4 ? go(scan_short_fwd_kernel<E, 4>) : go(scan_short_fwd_kernel<E, 1>);
 }
 
 // Forward or backward over N sequences of H heads (a fixed-length batch is one
@@ -1095,7 +1261,14 @@ int run(ScanArgs &a, bool backward, const int *cu_seqlens, int N, int H, int T_t
         const Work work = {static_cast<double>(seqs[n].len), static_cast<double>(total),
                            static_cast<double>(a.nseq), static_cast<double>(H), D,
                            dtype == GLA_BF16 ? 2 : 4, backward, way};
-        plan(a, work, sms);
+        const long long threads = static_cast<long long>(a.nseq) * H * (vec4 ? D / 4 : D);
+        if (plan(a, work, sms) >= walk_time(work) && threads < 0x7fffff00LL) {
+            const int e = dtype == GLA_BF16
+                              ? launch_short<__nv_bfloat16>(a, backward, vec4, stream)
+                              : launch_short<float>(a, backward, vec4, stream);
+            if (e != 0) return GLA_ERR_LAUNCH;
+            continue;
+        }
         const int e = dtype == GLA_BF16 ? launch_for<__nv_bfloat16>(a, backward, way, stream)
                                         : launch_for<float>(a, backward, way, stream);
         if (e != 0) return GLA_ERR_LAUNCH;

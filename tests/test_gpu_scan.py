@@ -96,6 +96,22 @@ def test_shapes_of_few_and_many_sequences(B, T, D, dtype):
                    f"{B}x{T}x{D}")
 
 
+@pytest.mark.parametrize("B,T,D", [(3000, 9, 33), (2000, 70, 36), (600, 130, 264), (5000, 1, 40)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_many_short_sequences(B, T, D, dtype):
+    x, la, h0, d, dT = make((B,), T, D, dtype, seed=B)
+    ck = gla.gla_scan_checkpoints(x)
+    h, hT = gla.gla_scan_fwd(x, la, h0, checkpoints=ck)
+    check_forward(x, la, h0, h, hT, f"{B}x{T}x{D}")
+    check_backward(x, la, h0, d, dT, gla.gla_scan_bwd(x, la, d, h0, dT, checkpoints=ck),
+                   f"{B}x{T}x{D}")
+    for need in ("need_dx", "need_dh0"):
+        got = gla.gla_scan_bwd(x, la, d, h0, dT, checkpoints=ck, **{
+            n: n == need for n in ("need_dx", "need_dlog_alpha", "need_dh0")})
+        i = ("need_dx", "", "need_dh0").index(need)
+        assert torch.equal(got[i], gla.gla_scan_bwd(x, la, d, h0, dT)[i])
+
+
 def test_without_states():
     x, la, h0, d, dT = make((2,), 100, 64)
     h, hT = gla.gla_scan_fwd(x, la, output_final_state=False)
