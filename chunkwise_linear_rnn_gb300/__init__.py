@@ -82,6 +82,36 @@ def _like(grad, dtype):
     return grad.clone() if grad.data_ptr() % 16 else grad
 
 
+def _meta(t):
+    """What the checks of a tensor argument look at."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _fits(meta, name: str, dtype: torch.dtype, shape: tuple, device) -> None:
+    """`_need` for a tensor's `_meta`; None fits."""
+    if meta is None:
+        return
+    has, strides, kind, dev = meta
+    if dev != device:
+        raise ValueError(f"{name} must be on the CUDA device {device}")
+    if kind != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {kind}")
+    if tuple(has) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(has)}")
+    step = 1
+    for size, stride in zip(reversed(has), reversed(strides)):
+        if size != 1 and stride != step and 0 not in has:
+            raise ValueError(f"{name} must be contiguous")
+        step *= size
+
+
+def _all_tensors(**tensors) -> None:
+    """Refuses an argument that is no tensor."""
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+
 def _apart(out, name: str, *inputs) -> None:
     """Refuses an output that the caller gave and that shares memory with an input."""
     first, last = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
@@ -572,20 +602,37 @@ def _bounds(cu_seqlens) -> list:
     return [int(c) for c in (cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else cu_seqlens)]
 
 
+@functools.lru_cache(maxsize=256)
+def _scan_fixed(x, log_alpha, h0):
+    """`_scan_sizes` for a batch of one length, with the inputs' checks: functions of their
+    `_meta`s alone."""
+    shape, _, kind, dev = x
+    if dev.type != "cuda":
+        raise ValueError("x must be on a CUDA device")
+    if kind not in _DTYPES:
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    if len(shape) not in (3, 4):
+        raise ValueError("x must be [B, T, D] or [B, H, T, D]")
+    lead, T, D = tuple(shape[:-2]), shape[-2], shape[-1]
+    H = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    _ints(H, T, D)
+    state = (*lead, D)
+    if log_alpha is not None:
+        _fits(x, "x", kind, shape, dev)
+        _fits(log_alpha, "log_alpha", torch.float32, shape, dev)
+        _fits(h0, "h0", torch.float32, state, dev)
+    return state, (*lead, -(-T // _lib.SCAN_BLOCK), D), (H, T, D, _DTYPES[kind])
+
+
 def _scan_sizes(x: torch.Tensor, cu):
     """(shape of a state, shape of the checkpoints, the C call's sizes) of a scan over `x`."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
+    if cu is None:
+        return _scan_fixed(_meta(x), None, None)
     if not x.is_cuda:
         raise ValueError("x must be on a CUDA device")
     shape, dtype = x.shape, _dtype(x, "x")
-    if cu is None:
-        if len(shape) not in (3, 4):
-            raise ValueError("x must be [B, T, D] or [B, H, T, D]")
-        lead, T, D = shape[:-2], shape[-2], shape[-1]
-        H = shape[0] if len(shape) == 3 else shape[0] * shape[1]
-        _ints(H, T, D)
-        return (*lead, D), (*lead, -(-T // _lib.SCAN_BLOCK), D), (H, T, D, dtype)
     if len(shape) not in (2, 3):
         raise ValueError("x must be [T_total, D] or [H, T_total, D]")
     T, D, N = shape[-2], shape[-1], len(cu) - 1
@@ -600,14 +647,29 @@ def _scan_sizes(x: torch.Tensor, cu):
     return (N, *lead, D), (*lead, blocks, D), sizes
 
 
-def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkpoints,
-              write_h=True, with_checkpoints=False):
-    state, ckpt, sizes = _scan_sizes(x, cu)
+def _scan_inputs(x, log_alpha, cu, h0):
+    """`_scan_sizes`, and the checks of these inputs."""
+    if x is None or log_alpha is None:
+        raise TypeError("x and log_alpha must be torch.Tensors")
+    if cu is None:
+        try:
+            return _scan_fixed(_meta(x), _meta(log_alpha), _meta(h0))
+        except AttributeError:
+            _all_tensors(x=x, log_alpha=log_alpha, h0=h0)
+            raise
+    sizes = _scan_sizes(x, cu)
     dev = x.device
     _need(x, "x", x.dtype, x.shape, dev)
     _need(log_alpha, "log_alpha", torch.float32, x.shape, dev)
     if h0 is not None:
-        _need(h0, "h0", torch.float32, state, dev)
+        _need(h0, "h0", torch.float32, sizes[0], dev)
+    return sizes
+
+
+def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkpoints,
+              write_h=True, with_checkpoints=False):
+    state, ckpt, sizes = _scan_inputs(x, log_alpha, cu, h0)
+    dev = x.device
     if out is not None:
         _need(out, "out", x.dtype, x.shape, dev)
         _apart(out, "out", x, log_alpha, h0)
@@ -631,10 +693,8 @@ def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkp
 
 
 def _scan_bwd(x, log_alpha, d_h, cu, h0, dhT, checkpoints, need_dx, need_dlog_alpha, need_dh0):
-    state, ckpt, sizes = _scan_sizes(x, cu)
+    state, ckpt, sizes = _scan_inputs(x, log_alpha, cu, None)
     dev = x.device
-    _need(x, "x", x.dtype, x.shape, dev)
-    _need(log_alpha, "log_alpha", torch.float32, x.shape, dev)
     if d_h is not None:
         _need(d_h, "d_h", x.dtype, x.shape, dev)
     if dhT is not None:
@@ -752,29 +812,43 @@ def gla_scan_varlen(x: torch.Tensor, log_alpha: torch.Tensor, cu_seqlens,
     return _GlaScan.apply(x, log_alpha, h0, _bounds(cu_seqlens))
 
 
+@functools.lru_cache(maxsize=256)
+def _step_checked(x, log_alpha, h):
+    """The checks of a step's arguments and the C call's sizes, of the tensors' `_meta`s alone."""
+    shape, _, kind, dev = x
+    if len(shape) not in (2, 3):
+        raise ValueError("x must be [B, D] or [B, H, D]")
+    if dev.type != "cuda":
+        raise ValueError("x must be on a CUDA device")
+    if kind not in _DTYPES:
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    _fits(x, "x", kind, shape, dev)
+    _fits(log_alpha, "log_alpha", torch.float32, shape, dev)
+    _fits(h, "h", torch.float32, shape, dev)
+    B, D = shape[:-1].numel(), shape[-1]
+    _ints(B, D)
+    return B, D, _DTYPES[kind]
+
+
 def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """One decode token of ``gla_scan_fwd``: ``h`` is updated in place, returns it in ``x``'s type.
 
     x ``[B, D]`` or ``[B, H, D]`` bf16 or fp32; log_alpha and h the same shape in fp32.
     """
-    if not isinstance(h, torch.Tensor) or h.dim() not in (2, 3):
-        raise ValueError("h must be [B, D] or [B, H, D]")
-    if not h.is_cuda:
-        raise ValueError("h must be on a CUDA device")
-    dev, shape, dtype = h.device, h.shape, _dtype(x, "x")
-    _need(h, "h", torch.float32, shape, dev)
-    _need(x, "x", x.dtype, shape, dev)
-    _need(log_alpha, "log_alpha", torch.float32, shape, dev)
+    if x is None or log_alpha is None or h is None:
+        raise TypeError("x, log_alpha and h must be torch.Tensors")
+    try:
+        sizes = _step_checked(_meta(x), _meta(log_alpha), _meta(h))
+    except AttributeError:
+        _all_tensors(x=x, log_alpha=log_alpha, h=h)
+        raise
     if out is None:
         out = torch.empty_like(x)
     else:
-        _need(out, "out", x.dtype, shape, dev)
-    D = shape[-1]
-    B = h.numel() // max(D, 1)
-    _ints(B, D)
-    _call("gla_scan_step", dev, x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(), out.data_ptr(),
-          B, D, dtype)
+        _need(out, "out", x.dtype, x.shape, x.device)
+    _call("gla_scan_step", x.device, x.data_ptr(), log_alpha.data_ptr(), h.data_ptr(),
+          out.data_ptr(), *sizes)
     return out
 
 
@@ -782,57 +856,62 @@ _NORMS = {"rms": _lib.GLA_NORM_RMS, "l2": _lib.GLA_NORM_L2}
 
 
 @functools.lru_cache(maxsize=256)
-def _qk_structs(*args):
-    """The C call's layout and options for these strides and options."""
-    return (ctypes.byref(_lib.GlaQkLayout(*args[:7])),
-            ctypes.byref(_lib.GlaQkOptions(dtype=args[7], norm=args[8], interleaved=int(args[9]),
-                                           eps=args[10])))
-
-
-def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
-    """Checks the arguments of a gla_qk_norm_rope call: (the inputs' pointers, the C call's
-    sizes)."""
-    for t, name in ((q, "q"), (k, "k")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-    dev, dtype = q.device, _dtype(q, "q")
-    qn, kn, qs, ks = q.shape, k.shape, q.stride(), k.stride()
-    if not q.is_cuda or k.device != dev:
+def _qk_checked(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+    """The checks of a gla_qk_norm_rope call's arguments and the C call's sizes, layout and
+    options: functions of the tensors' `_meta`s and of the options alone."""
+    if q is None or k is None:
+        raise TypeError("q and k must be torch.Tensors")
+    (qn, qs, kind, dev), (kn, ks, k_kind, k_dev) = q, k
+    if kind not in _DTYPES:
+        raise TypeError("q must be a torch.bfloat16 or torch.float32 tensor")
+    if dev.type != "cuda" or k_dev != dev:
         raise ValueError("q and k must be on the same CUDA device")
     if len(qn) != 4 or len(kn) != 4:
         raise ValueError("q and k must be [B, T, H, d]")
     if qs[3] != 1 or ks[3] != 1:
         raise ValueError("the last dimension of q and k must be contiguous")
     B, T, Hq, d = qn
-    if k.dtype is not q.dtype:
-        raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+    Hk = kn[2]
+    if k_kind is not kind:
+        raise TypeError(f"k must be {kind}, got {k_kind}")
     if kn[0] != B or kn[1] != T or kn[3] != d:
-        raise ValueError(f"k must have shape {(B, T, kn[2], d)}, got {tuple(kn)}")
+        raise ValueError(f"k must have shape {(B, T, Hk, d)}, got {tuple(kn)}")
     if norm not in _NORMS:
         raise ValueError("norm must be 'rms' or 'l2'")
-    if q_weight is not None:
-        _need(q_weight, "q_weight", torch.float32, (d,), dev)
-    if k_weight is not None:
-        _need(k_weight, "k_weight", torch.float32, (d,), dev)
+    _fits(q_weight, "q_weight", torch.float32, (d,), dev)
+    _fits(k_weight, "k_weight", torch.float32, (d,), dev)
     rot = 0
     if inv_freq is not None:
-        if not isinstance(inv_freq, torch.Tensor):
-            raise TypeError("inv_freq must be a torch.Tensor")
-        rot = 2 * inv_freq.numel()
-        _need(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+        rot = 2 * inv_freq[0].numel()
+        _fits(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
     pos_sb = 0
     if positions is not None:
-        one = isinstance(positions, torch.Tensor) and positions.dim() == 1
-        _need(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
+        one = len(positions[0]) == 1
+        _fits(positions, "positions", torch.int64, (T,) if one else (B, T), dev)
         pos_sb = 0 if one else T
-    _ints(B, T, Hq, kn[2], d, rot)
+    _ints(B, T, Hq, Hk, d, rot)
     # a dimension of one entry is never stepped over, whatever its stride says
-    structs = _qk_structs(qs[0] if B != 1 else 0, qs[1] if T != 1 else 0, qs[2] if Hq != 1 else 0,
-                          ks[0] if B != 1 else 0, ks[1] if T != 1 else 0,
-                          ks[2] if kn[2] != 1 else 0, pos_sb, dtype, _NORMS[norm],
-                          bool(interleaved), float(eps))
-    return ((q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-             _ptr(inv_freq)), (B, T, Hq, kn[2], d, rot, *structs))
+    layout = _lib.GlaQkLayout(qs[0] if B != 1 else 0, qs[1] if T != 1 else 0,
+                              qs[2] if Hq != 1 else 0, ks[0] if B != 1 else 0,
+                              ks[1] if T != 1 else 0, ks[2] if Hk != 1 else 0, pos_sb)
+    options = _lib.GlaQkOptions(dtype=_DTYPES[kind], norm=_NORMS[norm],
+                                interleaved=int(interleaved), eps=eps)
+    return B, T, Hq, Hk, d, rot, ctypes.byref(layout), ctypes.byref(options)
+
+
+def _qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps, interleaved):
+    """Checks the arguments of a gla_qk_norm_rope call: (the inputs' pointers, the C call's
+    sizes)."""
+    try:
+        sizes = _qk_checked(_meta(q), _meta(k), _meta(q_weight), _meta(k_weight),
+                            _meta(positions), _meta(inv_freq), norm, float(eps),
+                            bool(interleaved))
+    except AttributeError:
+        _all_tensors(q=q, k=k, q_weight=q_weight, k_weight=k_weight, positions=positions,
+                     inv_freq=inv_freq)
+        raise
+    return (q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+            _ptr(inv_freq)), sizes
 
 
 def _qk_fwd(q, pointers, sizes):

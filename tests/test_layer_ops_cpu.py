@@ -206,6 +206,49 @@ def test_python_calls_refuse_cpu_tensors():
         gla.gla_rope_frequencies(12)
 
 
+def _meta(shape, dtype=torch.float32, stride=None, device="cuda:0"):
+    t = torch.empty(shape, dtype=dtype, device="meta")
+    return t.shape, stride or t.stride(), dtype, torch.device(device)
+
+
+def test_checks_of_the_arguments_alone():
+    x = _meta((2, 5, 8), torch.bfloat16)
+    la, h0 = _meta((2, 5, 8)), _meta((2, 8))
+    assert gla._scan_fixed(x, la, h0) == ((2, 8), (2, 1, 8), (2, 5, 8, _lib.GLA_BF16))
+    # a dimension of one entry may have any stride
+    assert gla._scan_fixed(_meta((1, 5, 8), stride=(7, 8, 1)), _meta((1, 5, 8)), None)[2][0] == 1
+    for bad in ((x, _meta((2, 5, 9)), h0), (x, _meta((2, 5, 8), torch.float64), h0),
+                (x, la, _meta((2, 9))), (_meta((2, 5, 8), torch.float16), la, h0),
+                (_meta((2, 5, 8), stride=(80, 16, 1)), la, h0), (_meta((5, 8)), la, h0),
+                (_meta((2, 5, 8), device="cpu"), la, h0), (x, _meta((2, 5, 8), device="cuda:1"), h0)):
+        with pytest.raises((TypeError, ValueError)):
+            gla._scan_fixed(*bad)
+    q, k = _meta((2, 5, 4, 64)), _meta((2, 5, 2, 64))
+    rest = (None, None, None, None, "rms", 1e-6, False)
+    assert gla._qk_checked(q, k, *rest)[:6] == (2, 5, 4, 2, 64, 0)
+    w, f = _meta((64,)), _meta((16,), torch.float64)
+    assert gla._qk_checked(q, k, w, w, _meta((5,), torch.int64), f, "l2", 1e-6, True)[5] == 32
+    for bad in ((q, _meta((2, 5, 2, 32)), *rest), (q, _meta((2, 5, 2, 64), torch.bfloat16), *rest),
+                (q, _meta((2, 5, 2, 64), device="cuda:1"), *rest),
+                (_meta((2, 5, 4, 64), stride=(1280, 256, 1, 4)), k, *rest),
+                (q, k, _meta((32,)), *rest[1:]), (q, k, None, _meta((64,), torch.bfloat16), *rest[2:]),
+                (q, k, None, None, _meta((2, 4), torch.int64), *rest[3:]),
+                (q, k, None, None, None, _meta((16,)), *rest[4:]),
+                (q, k, *rest[:4], "max", 1e-6, False)):
+        with pytest.raises((TypeError, ValueError)):
+            gla._qk_checked(*bad)
+    s = _meta((3, 8))
+    assert gla._step_checked(_meta((3, 8), torch.bfloat16), s, s) == (3, 8, _lib.GLA_BF16)
+    for bad in ((s, s, _meta((3, 9))), (s, _meta((3, 8), stride=(16, 1)), s), (_meta((3,)), s, s)):
+        with pytest.raises((TypeError, ValueError)):
+            gla._step_checked(*bad)
+    for call in (lambda: gla.gla_scan_fwd([1.0], None), lambda: gla.gla_scan_step(1.0, 2.0, 3.0),
+                 lambda: gla.gla_qk_norm_rope_fwd(None, None),
+                 lambda: gla.gla_qk_norm_rope_fwd([1.0], [1.0])):
+        with pytest.raises(TypeError):
+            call()
+
+
 def test_frequencies():
     f = gla.gla_rope_frequencies(16, 100.0)
     want = [100.0 ** (-i / 8) for i in range(8)]
