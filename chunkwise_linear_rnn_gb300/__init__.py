@@ -835,6 +835,8 @@ def gla_scan_step(x: torch.Tensor, log_alpha: torch.Tensor, h: torch.Tensor, *,
     """One decode token of ``gla_scan_fwd``: ``h`` is updated in place, returns it in ``x``'s type.
 
     x ``[B, D]`` or ``[B, H, D]`` bf16 or fp32; log_alpha and h the same shape in fp32.
+    ``out`` (or ``h``) may be another argument of the same element size itself, such as
+    ``out=x``; tensors that share memory in any other way are refused.
     """
     if x is None or log_alpha is None or h is None:
         raise TypeError("x, log_alpha and h must be torch.Tensors")

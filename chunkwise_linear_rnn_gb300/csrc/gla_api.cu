@@ -510,7 +510,8 @@ int gla_version(void) { return 200; }
 const char *gla_status_string(int status) {
     switch (status) {
         case GLA_OK: return "ok";
-        case GLA_ERR_ARG: return "invalid argument (null pointer, non-positive size or misaligned pointer)";
+        case GLA_ERR_ARG: return "invalid argument (null pointer, non-positive size, misaligned pointer "
+                                  "or overlapping tensors)";
         case GLA_ERR_SHAPE: return "unsupported head dimensions (dk in {64,128}, dv in {64,128,256}; "
                                     "gla_qk_norm_rope: d and rot multiples of 8, rot <= d <= 256)";
         case GLA_ERR_DEVICE: return "no usable CUDA device (this library needs an sm_103 GB300)";

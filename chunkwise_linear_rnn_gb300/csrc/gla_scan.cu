@@ -1047,6 +1047,14 @@ bool elements_aligned(const ScanArgs &a, int dtype) {
            aligned(4, a.log_alpha, a.h0, a.dhT, a.ckpt_in, a.hT, a.ga, a.ckpt_out);
 }
 
+// Whether two tensors of n elements each share memory without being the same elements: a
+// thread that reads and writes its own element of both would then meet another thread's.
+bool mixed(const void *a, int size_a, const void *b, int size_b, long long n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(n) * size_b && y < x + static_cast<uintptr_t>(n) * size_a &&
+           (x != y || size_a != size_b);
+}
+
 // Checks shared by the scans; cu_seqlens [N + 1] is checked by the caller's loop.
 int check_common(const ScanArgs &a, long long states, int D, int dtype) {
     if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
@@ -1339,6 +1347,10 @@ int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, in
     if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_ARG;
     if (!aligned(dtype == GLA_BF16 ? 2 : 4, x, out) || !aligned(4, log_alpha, h)) return GLA_ERR_ARG;
     const long long n = static_cast<long long>(B) * D;
+    const int size = dtype == GLA_BF16 ? 2 : 4;
+    if (mixed(h, 4, x, size, n) || mixed(h, 4, log_alpha, 4, n) || mixed(out, size, x, size, n) ||
+        mixed(out, size, log_alpha, 4, n) || mixed(out, size, h, 4, n))
+        return GLA_ERR_ARG;
     const bool vec4 = n % 4 == 0 && aligned(16, x, log_alpha, h, out);
     const long long blocks = (n + (vec4 ? 1023 : 255)) / (vec4 ? 1024 : 256);
     if (blocks > 0x7fffffffLL) return GLA_ERR_ARG;

@@ -56,7 +56,7 @@ typedef struct CUstream_st *cudaStream_t;
 
 enum gla_status {
     GLA_OK = 0,
-    GLA_ERR_ARG = 1,         /* null pointer, non-positive size, misaligned pointer   */
+    GLA_ERR_ARG = 1,         /* null pointer, non-positive size, misaligned or overlap */
     GLA_ERR_SHAPE = 2,       /* dk / dv outside the supported set                      */
     GLA_ERR_DEVICE = 3,      /* no CUDA device, or the device is not sm_103            */
     GLA_ERR_LAUNCH = 4,      /* a CUDA call failed while enqueuing the work            */
@@ -514,7 +514,10 @@ int gla_scan_bwd_varlen(const void *x, const float *log_alpha, const float *chec
 /*
  * gla_scan_step — one decode token of gla_scan_fwd for B streams: h (fp32
  * [B, D]) becomes exp(log_alpha) h + x in place, and out ([B, D] dtype)
- * receives it rounded.  x [B, D] dtype, log_alpha [B, D] fp32.
+ * receives it rounded.  x [B, D] dtype, log_alpha [B, D] fp32.  h and out may each
+ * be the same tensor as another argument of the same element size (out = x, say),
+ * element for element; any other overlap of h or out with an argument is refused
+ * (GLA_ERR_ARG), since threads would read what others write.
  */
 int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, int B, int D,
                   int dtype, cudaStream_t stream);
