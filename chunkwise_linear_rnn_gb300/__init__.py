@@ -112,13 +112,13 @@ def _all_tensors(**tensors) -> None:
             raise TypeError(f"{name} must be a torch.Tensor")
 
 
-def _apart(out, name: str, *inputs) -> None:
-    """Refuses an output that the caller gave and that shares memory with an input."""
+def _apart(out, name: str, *others, also: str = "an input") -> None:
+    """Refuses an output that shares memory with an input, or with what `also` names."""
     first, last = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
-    for t in inputs:
+    for t in others:
         if t is not None and first < t.data_ptr() + t.numel() * t.element_size() and \
                 t.data_ptr() < last:
-            raise ValueError(f"{name} must not share memory with an input")
+            raise ValueError(f"{name} must not share memory with {also}")
 
 
 def _ints(*sizes) -> None:
@@ -680,6 +680,7 @@ def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkp
         _need(hT, "final_state", torch.float32, state, dev)
         _apart(hT, "final_state", x, log_alpha, None if h0 is None or
                h0.data_ptr() == hT.data_ptr() else h0)
+        _apart(hT, "final_state", out, also="another output")
     elif output_final_state:
         hT = torch.empty(state, dtype=torch.float32, device=dev)
     if with_checkpoints:
@@ -687,6 +688,7 @@ def _scan_fwd(x, log_alpha, cu, h0, output_final_state, out, final_state, checkp
     elif checkpoints is not None:
         _need(checkpoints, "checkpoints", torch.float32, ckpt, dev)
         _apart(checkpoints, "checkpoints", x, log_alpha, h0)
+        _apart(checkpoints, "checkpoints", out, hT, also="another output")
     _call("gla_scan_fwd" if cu is None else "gla_scan_fwd_varlen", dev, x.data_ptr(),
           log_alpha.data_ptr(), _ptr(h0), _ptr(out), _ptr(hT), _ptr(checkpoints), *sizes)
     return (out, hT, checkpoints) if with_checkpoints else (out, hT)
@@ -735,7 +737,7 @@ def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | No
     fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
     fp32 on the way, and the last one in fp32 (None when ``output_final_state`` is
     False).  ``final_state`` may be ``h0`` itself; no other output may share memory
-    with an input.  ``checkpoints`` (from
+    with an input, and no output with another.  ``checkpoints`` (from
     ``gla_scan_checkpoints``) is filled for ``gla_scan_bwd``.
     """
     return _scan_fwd(x, log_alpha, None, h0, output_final_state, out, final_state, checkpoints)

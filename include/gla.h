@@ -463,8 +463,9 @@ enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
  * once to dtype as it is stored.  The results do not depend on the order in
  * which the GPU runs the work: equal calls give equal bits.  The calls use no
  * scratch.  h may be NULL when checkpoints or hT is asked for.  No other output
- * may overlap an input.  A bounded device wait that expires leaves the outputs
- * unspecified and is reported by gla_last_device_status (GLA_ERR_TIMEOUT).
+ * may overlap an input, and no output another.  A bounded device wait that
+ * expires leaves the outputs unspecified and is reported by
+ * gla_last_device_status (GLA_ERR_TIMEOUT).
  * Accuracy: with M the recurrence on |x|, |h0| and N the recurrence on M,
  * |h - exact| <= 2^-24 (4 N + 8 M) before the rounding to dtype.
  *

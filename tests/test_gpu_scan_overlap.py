@@ -53,3 +53,17 @@ def test_a_step_over_its_own_arguments(dtype, D):
         args = [x.clone(), la.clone(), h.clone()]
         assert torch.equal(gla.gla_scan_step(*args, out=args[i]), want)
         assert torch.equal(args[2], want if i == 2 else state)
+
+
+def test_a_forward_refuses_outputs_over_each_other():
+    x, la, h0, _, _ = make((2,), 70, 8, F32)
+    flat = torch.zeros(4096, device=DEV)
+    out, ck = flat[:x.numel()].view_as(x), flat[4:36].view(2, 2, 8)
+    for kw in (dict(out=out, final_state=flat[8:24].view(2, 8)), dict(out=out, checkpoints=ck),
+               dict(final_state=flat[8:24].view(2, 8), checkpoints=ck)):
+        with pytest.raises(ValueError, match="another output"):
+            gla.gla_scan_fwd(x, la, h0, **kw)
+    last, ck = flat[1120:1136].view(2, 8), flat[1136:1168].view(2, 2, 8)
+    want = gla.gla_scan_fwd(x, la, h0)
+    got = gla.gla_scan_fwd(x, la, h0, out=out, final_state=last, checkpoints=ck)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -1,10 +1,12 @@
-"""gla_scan_step refuses tensors that share memory without being the same elements."""
+"""Tensors that share memory are refused: arguments of gla_scan_step that are not the same
+elements, and outputs of gla_scan_fwd over each other."""
 
 from __future__ import annotations
 
 import pytest
 import torch
 
+import chunkwise_linear_rnn_gb300 as gla
 from chunkwise_linear_rnn_gb300 import _lib
 from chunkwise_linear_rnn_gb300.build import build
 from test_library_cpu import P
@@ -52,3 +54,60 @@ def test_the_same_elements_and_neighbours_are_taken(lib, dtype):
     if dtype == F32:
         assert taken(out=APART["h"]) and taken(out=APART["la"]) and taken(h=APART["x"])
         assert taken(h=APART["x"], out=APART["x"], la=APART["x"])
+
+
+# ---------------------------------------------------------------- outputs of gla_scan_fwd
+
+SHAPE, STATE, BLOCKS = (2, 70, 8), (2, 8), (2, 2, 8)
+
+
+@pytest.fixture
+def forward(monkeypatch):
+    """gla_scan_fwd up to its C call, on CPU tensors: what the call was given."""
+    calls = []
+    monkeypatch.setattr(gla, "_scan_fixed", lambda *metas: (STATE, BLOCKS, (*SHAPE, F32)))
+    monkeypatch.setattr(gla, "_call", lambda name, device, *args: calls.append(args))
+
+    def run(h0=None, **outputs):
+        del calls[:]
+        x, la = torch.zeros(2, *SHAPE)
+        gla.gla_scan_fwd(x, la, h0, **outputs)
+        return calls[0]
+
+    return run
+
+
+def _views(*wanted):
+    """Tensors of these (offset, shape) in one buffer."""
+    flat = torch.zeros(4096)
+    return [flat[at:at + torch.Size(s).numel()].view(s) for at, s in wanted]
+
+
+@pytest.mark.parametrize("shift", [0, 1, -1, 1119, -15])
+def test_final_state_over_out_is_refused(forward, shift):
+    out, last = _views((1000, SHAPE), (1000 + shift, STATE))
+    with pytest.raises(ValueError, match="final_state must not share memory with another output"):
+        forward(out=out, final_state=last)
+    with pytest.raises(ValueError, match="share memory"):
+        forward(h0=last, out=out, final_state=last)
+
+
+@pytest.mark.parametrize("shift", [0, 1, -1, 1119, -31])
+def test_checkpoints_over_out_are_refused(forward, shift):
+    out, ck = _views((1000, SHAPE), (1000 + shift, BLOCKS))
+    with pytest.raises(ValueError, match="checkpoints must not share memory with another output"):
+        forward(out=out, checkpoints=ck)
+
+
+@pytest.mark.parametrize("shift", [0, 1, -1, 15, -31])
+def test_checkpoints_over_the_final_state_are_refused(forward, shift):
+    last, ck = _views((1000, STATE), (1000 + shift, BLOCKS))
+    with pytest.raises(ValueError, match="checkpoints must not share memory with another output"):
+        forward(final_state=last, checkpoints=ck)
+
+
+def test_outputs_beside_each_other_are_taken(forward):
+    out, last, ck = _views((1000, SHAPE), (1000 + 1120, STATE), (1000 - 32, BLOCKS))
+    args = forward(out=out, final_state=last, checkpoints=ck)
+    assert args[3:6] == (out.data_ptr(), last.data_ptr(), ck.data_ptr())
+    assert forward(h0=last, out=out, final_state=last)[2:5:2] == (last.data_ptr(),) * 2
