@@ -71,28 +71,44 @@ int current_device(DeviceInfo **out) {
     return GLA_OK;
 }
 
-// The tensor-map encoder.  It is a driver call: it wants the device's context bound
-// to this thread, which a thread that has made no other call (autograd's own threads)
-// does not have yet.
+using CtxGetCurrentFn = CUresult (*)(CUcontext *);
+CtxGetCurrentFn g_ctx_get_current = nullptr;
+
+// A driver entry point of this CUDA version.
+template <typename Fn>
+bool driver_fn(Fn *fn, const char *name, unsigned int version) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !p) {
+        cudaGetLastError();
+        return false;
+    }
+    *fn = reinterpret_cast<Fn>(p);
+    return true;
+}
+
+// The tensor-map encoder.  It is a driver call: it wants a context bound to this thread,
+// which a thread that has made no other call (autograd's own threads) does not have yet.
+// Such a thread gets the device's primary context; one that the caller has made current
+// (a green context, say) stays, since the launch and what follows belong there.
 int encode_fn(EncodeTiledFn *fn) {
+    CtxGetCurrentFn current = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if ((!g_ctx_get_current && !driver_fn(&g_ctx_get_current, "cuCtxGetCurrent", 4000)) ||
+            (!g_encode && !driver_fn(&g_encode, "cuTensorMapEncodeTiled", 12000)))
+            return GLA_ERR_DEVICE;
+        current = g_ctx_get_current;
+        *fn = g_encode;
+    }
+    CUcontext ctx = nullptr;
+    if (current(&ctx) == CUDA_SUCCESS && ctx) return GLA_OK;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
         cudaGetLastError();
         return GLA_ERR_DEVICE;
     }
-    std::lock_guard<std::mutex> lock(g_mutex);
-    if (!g_encode) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || !p) {
-            cudaGetLastError();
-            return GLA_ERR_DEVICE;
-        }
-        g_encode = reinterpret_cast<EncodeTiledFn>(p);
-    }
-    *fn = g_encode;
     return GLA_OK;
 }
 
