@@ -41,7 +41,14 @@ struct QkArgs {
     gla_qk_layout lay;
     int B, T, H[2], d, rot, interleaved;
     int chunk;               // heads (q's, then k's) of a block
+    long long first, end;    // backward: the launch's tokens
     float inv_n, eps;
+};
+
+// Where the backward's weight gradients go, and their sums over several launches.
+struct WeightGrads {
+    float *q, *k;
+    double *so_far;          // [2][d]
 };
 
 constexpr int kWarps = 8;
@@ -405,11 +412,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     static_assert(sizeof(s_queue) >= sizeof(float) * kWarps * ROWS * 8 * LANES, "the sums' space");
     const int lane = threadIdx.x & 31, row = lane / LANES;
     const Lane<LANES, HALVES> l(p, lane);
-    const long long tokens = static_cast<long long>(p.B) * p.T;
+    const long long tokens = p.end;
+    const long long start =
+        p.first + blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5);
     auto *queue = s_queue[threadIdx.x >> 5];
 
     Rounds<E, ROWS> ask;
-    ask.begin(p, blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5), tokens, row);
+    ask.begin(p, start, tokens, row);
     const auto request = [&](int slot) {
         if (ask.n < tokens) {
             if (ask.h + row < ask.to) {   // the others' values go nowhere
@@ -430,8 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 #pragma unroll
     for (int k = 0; k < 4; ++k) dw[0][k] = dw[1][k] = pair_of(0.f, 0.f);
     int slot = 0;
-    for (long long n = blockIdx.x * static_cast<long long>(kWarps) + (threadIdx.x >> 5); n < tokens;
-         n += static_cast<long long>(gridDim.x) * kWarps) {
+    for (long long n = start; n < tokens; n += static_cast<long long>(gridDim.x) * kWarps) {
         Angles<LANES, HALVES> turn;
         if (p.rot) {
             const int b = batch_of(p, n, tokens);
@@ -497,9 +505,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     }
 }
 
-// The blocks' partial weight gradients, added in order in fp64.
-__global__ void __launch_bounds__(1024) qk_weight_grad_kernel(const float *partial, int blocks,
-                                                              int d, float *gq, float *gk) {
+// The blocks' partial weight gradients, added in order in fp64.  Of several launches (`so_far`
+// given) each adds its own to the sums of those before it; the last one writes the gradients.
+__global__ void __launch_bounds__(1024)
+    qk_weight_grad_kernel(const float *partial, int blocks, int d, float *gq, float *gk,
+                          double *so_far, bool first, bool last) {
     __shared__ double s_sum[32][17];
     const int c = threadIdx.x & 15, part = threadIdx.x >> 4;   // 16 columns, 64 parts
     const int i = blockIdx.x * 16 + c;
@@ -513,6 +523,11 @@ __global__ void __launch_bounds__(1024) qk_weight_grad_kernel(const float *parti
     if (part != 0) return;
     v = 0.0;
     for (int k = 0; k < 32; ++k) v += s_sum[k][c];
+    if (so_far) {
+        if (!first) v += so_far[i];
+        so_far[i] = v;
+    }
+    if (!last) return;
     float *g = i < d ? gq : gk;
     if (g) g[i < d ? i : i - d] = static_cast<float>(v);
 }
@@ -531,28 +546,58 @@ dim3 grid_of(QkArgs &a, int rows, long long most, int sms) {
     return dim3(static_cast<unsigned>(std::max<long long>(1, std::min(groups, most / y))), y);
 }
 
+// Rows that a lane adds one after another in 32 bits for the weight gradients, at most (but a
+// token's own heads, of which a block takes more than so many rounds from 300,000 heads on): a
+// longer batch takes several launches, whose sums are added in 64 bits.  (As a test in the
+// kernel, once a token, it took 5% of the time: 54 us -> 56.5 for B4 T4096, 32+8 heads of 64.)
+constexpr int kSumRows = 1024;
+
+template <typename E, int LANES, bool HALVES, bool PART>
+int launch_bwd(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
+    constexpr int ROWS = 32 / LANES;
+    const dim3 grid = grid_of(a, ROWS, kPartials, sms);
+    const long long tokens = static_cast<long long>(a.B) * a.T;
+    // q's and k's heads of a block may each end in a short round
+    const long long each = std::max(1, kSumRows / (a.chunk / ROWS + 1));
+    const long long step = a.partial ? each * grid.x * kWarps : tokens;
+    for (a.first = 0; a.first < tokens; a.first = a.end) {
+        a.end = std::min(a.first + step, tokens);
+        qk_bwd_kernel<E, LANES, HALVES, PART><<<grid, 32 * kWarps, 0, stream>>>(a);
+        if (a.partial)
+            qk_weight_grad_kernel<<<2 * a.d / 16, 1024, 0, stream>>>(
+                a.partial, grid.x * grid.y, a.d, to.q, to.k, step < tokens ? to.so_far : nullptr,
+                a.first == 0, a.end == tokens);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return static_cast<int>(e);
+    }
+    return 0;
+}
+
 template <typename E, int LANES, bool HALVES, bool PART, bool BACKWARD>
-int launch_one(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
-    *grid = grid_of(a, 32 / LANES, most, sms);
-    if constexpr (BACKWARD) qk_bwd_kernel<E, LANES, HALVES, PART><<<*grid, 32 * kWarps, 0, stream>>>(a);
-    else qk_fwd_kernel<E, LANES, HALVES, PART><<<*grid, 32 * kWarps, 0, stream>>>(a);
-    return static_cast<int>(cudaGetLastError());
+int launch_one(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
+    if constexpr (BACKWARD) {
+        return launch_bwd<E, LANES, HALVES, PART>(a, to, sms, stream);
+    } else {
+        const dim3 grid = grid_of(a, 32 / LANES, kFwdBlocks * sms, sms);
+        qk_fwd_kernel<E, LANES, HALVES, PART><<<grid, 32 * kWarps, 0, stream>>>(a);
+        return static_cast<int>(cudaGetLastError());
+    }
 }
 
 template <typename E, int LANES, bool BACKWARD>
-int launch_lanes(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
+int launch_lanes(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
     const bool halves = !a.interleaved, part = a.rot > 0 && a.rot < a.d;
-    if (halves) return part ? launch_one<E, LANES, true, true, BACKWARD>(a, most, sms, grid, stream)
-                            : launch_one<E, LANES, true, false, BACKWARD>(a, most, sms, grid, stream);
-    return part ? launch_one<E, LANES, false, true, BACKWARD>(a, most, sms, grid, stream)
-                : launch_one<E, LANES, false, false, BACKWARD>(a, most, sms, grid, stream);
+    if (halves) return part ? launch_one<E, LANES, true, true, BACKWARD>(a, to, sms, stream)
+                            : launch_one<E, LANES, true, false, BACKWARD>(a, to, sms, stream);
+    return part ? launch_one<E, LANES, false, true, BACKWARD>(a, to, sms, stream)
+                : launch_one<E, LANES, false, false, BACKWARD>(a, to, sms, stream);
 }
 
 template <typename E, bool BACKWARD>
-int launch(QkArgs &a, long long most, int sms, dim3 *grid, cudaStream_t stream) {
-    if (a.d <= 64) return launch_lanes<E, 8, BACKWARD>(a, most, sms, grid, stream);
-    if (a.d <= 128) return launch_lanes<E, 16, BACKWARD>(a, most, sms, grid, stream);
-    return launch_lanes<E, 32, BACKWARD>(a, most, sms, grid, stream);
+int launch(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
+    if (a.d <= 64) return launch_lanes<E, 8, BACKWARD>(a, to, sms, stream);
+    if (a.d <= 128) return launch_lanes<E, 16, BACKWARD>(a, to, sms, stream);
+    return launch_lanes<E, 32, BACKWARD>(a, to, sms, stream);
 }
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -622,15 +667,13 @@ int gla_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
-    dim3 grid;
-    const int e = options->dtype == GLA_BF16
-                      ? launch<__nv_bfloat16, false>(a, kFwdBlocks * sms, sms, &grid, stream)
-                      : launch<float, false>(a, kFwdBlocks * sms, sms, &grid, stream);
+    const int e = options->dtype == GLA_BF16 ? launch<__nv_bfloat16, false>(a, {}, sms, stream)
+                                             : launch<float, false>(a, {}, sms, stream);
     return e == 0 ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 unsigned long gla_qk_norm_rope_bwd_scratch(int d) {
-    return d > 0 ? static_cast<unsigned long>(gla::kPartials) * 2 * d * sizeof(float) : 0;
+    return d > 0 ? 2ul * d * (gla::kPartials * sizeof(float) + sizeof(double)) : 0;
 }
 
 int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk,
@@ -649,25 +692,20 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
     a.dy[1] = d_k;
     int st = check(a, *options);
     if (st != GLA_OK) return st;
-    const bool weights = grad_wq || grad_wk;
-    if (weights) {
+    WeightGrads to = {};
+    if (grad_wq || grad_wk) {
         if (!scratch || !aligned(scratch, 16)) return GLA_ERR_ARG;
         if (scratch_bytes < gla_qk_norm_rope_bwd_scratch(d)) return GLA_ERR_SCRATCH;
         if (!aligned(grad_wq, 4) || !aligned(grad_wk, 4)) return GLA_ERR_ARG;
         a.partial = static_cast<float *>(scratch);
+        to = {grad_wq, grad_wk, reinterpret_cast<double *>(a.partial + size_t{kPartials} * 2 * d)};
     }
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
-    dim3 grid;
-    const int e = options->dtype == GLA_BF16
-                      ? launch<__nv_bfloat16, true>(a, kPartials, sms, &grid, stream)
-                      : launch<float, true>(a, kPartials, sms, &grid, stream);
-    if (e != 0) return GLA_ERR_LAUNCH;
-    if (weights)
-        qk_weight_grad_kernel<<<2 * d / 16, 1024, 0, stream>>>(a.partial, grid.x * grid.y, d, grad_wq,
-                                                               grad_wk);
-    return cudaGetLastError() == cudaSuccess ? GLA_OK : GLA_ERR_LAUNCH;
+    const int e = options->dtype == GLA_BF16 ? launch<__nv_bfloat16, true>(a, to, sms, stream)
+                                             : launch<float, true>(a, to, sms, stream);
+    return e == 0 ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 }  // extern "C"
