@@ -230,7 +230,8 @@ __device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {__fmul_rn(a.
 __device__ __forceinline__ Vec<4> mul(Vec<4> a, Vec<4> b) {
     return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)};
 }
-// A product that no compiler joins with the sum that follows (it does join pairs').
+// A product that the compiler does not join with the sum that follows, as it may with a
+// pair's: it does so in scan_short_bwd_kernel.
 __device__ __forceinline__ Vec<1> mul_alone(Vec<1> a, Vec<1> b) { return mul(a, b); }
 __device__ __forceinline__ Vec<4> mul_alone(Vec<4> a, Vec<4> b) {
     float x[4], y[4];
@@ -630,8 +631,9 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Forward in time, the states h_{t-1} are walked again from the checkpoint of each
 // block of kBlock tokens; backward in time, u_t = alpha_t g_t is the recurrence's
 // own scan from the end: a run maps the u that enters it on the right to the one that
-// leaves it on the left, u -> P u + U, with the same P.  Products and sums are rounded
-// one by one, so that a call with fewer outputs gives the same bits.
+// leaves it on the left, u -> P u + U, with the same P.  The walk's products (mul_alone) and
+// sums are rounded one by one in both of its loops, so that a call with fewer outputs gives
+// the same bits.
 template <typename E, int VEC, int LPR, int TPW, int THREADS, int STAGES>
 __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
     scan_bwd_kernel(const __grid_constant__ ScanArgs p) {
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
 #pragma unroll
             for (int i = TPW - 1; i >= 0; --i) {
                 const V g = add(u, widen(c.d[i]));
-                u = mul(c.a[i], g);
+                u = mul_alone(c.a[i], g);
                 store_vec<VEC>(dx, g);
                 store_vec<VEC>(da, mul(u, before[i]));
                 dx -= pitch;
@@ -850,7 +852,7 @@ __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
 #pragma unroll
             for (int i = TPW - 1; i >= 0; --i) {
                 const V g = add(u, widen(c.d[i]));
-                u = mul(c.a[i], g);
+                u = mul_alone(c.a[i], g);
                 if (p.h && t0 + i < o.len) store_vec<VEC>(dx, g);
                 if (p.ga && t0 + i < o.len) store_vec<VEC>(da, mul(u, before[i]));
                 dx -= pitch;
