@@ -22,7 +22,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 #include <cstdint>
 #include <new>
 #include <type_traits>
@@ -31,6 +30,7 @@
 #include "gla.h"
 #include "gla_internal.h"
 #include "gla_ptx.cuh"
+#include "gla_scan_plan.h"
 
 namespace gla {
 namespace {
@@ -67,11 +67,6 @@ struct ScanArgs {
 // takes LPR * VEC neighbouring channels of TPW consecutive tokens, and the
 // block's runs follow one another in time, so that its tile is
 // (kThreads / LPR) * TPW tokens of LPR * VEC channels.
-constexpr int kMaxCluster = 16;
-
-// Blocks of a cluster of blocks of so many channels, at most.
-constexpr int cluster_of(int channels) { return channels == 32 ? kMaxCluster : channels == 64 ? 4 : 1; }
-
 template <int VEC, int LPR, int TPW, int THREADS>
 struct Tile {
     static constexpr int kThreads = THREADS;
@@ -153,10 +148,10 @@ struct Place {
 template <typename G, int VEC, int LPR>
 __device__ __forceinline__ Place place(const ScanArgs &p) {
     Place o;
-    o.cl = p.cluster;
-    o.rank = blockIdx.x % p.cluster;
+    o.cl = cluster_of(G::kChannels) > 1 ? p.cluster : 1;
+    o.rank = blockIdx.x % o.cl;
     const unsigned groups = (p.D + G::kChannels - 1) / G::kChannels;
-    const unsigned work = blockIdx.x / p.cluster;
+    const unsigned work = blockIdx.x / o.cl;
     const unsigned unit = work / groups;
     o.first = (work % groups) * G::kChannels;
     const int c = o.first + (threadIdx.x % LPR) * VEC;
@@ -893,7 +888,6 @@ __global__ void __launch_bounds__(THREADS, STAGES == 0 && VEC == 4 ? 1 : 2)
 
 // Short sequences: a thread walks one by itself, VEC channels of it, kChunk tokens on their
 // way at a time.  No tile to fill, no exchange.
-constexpr int kChunk = 8;
 constexpr int kShortThreads = 64;
 
 struct ShortPlace {
@@ -1111,97 +1105,13 @@ int launch_bwd(const ScanArgs &a, cudaStream_t stream) {
         a, STAGES * sizeof(BwdStage<E, G::kChannels, G::kTokens>), stream);
 }
 
-// The tiles' ways to the registers: by TMA, where rows are whole 16-byte pieces; four
-// neighbouring channels a thread without it; one.  (B2 T16384, bf16 forward: D2048 by TMA
-// 89 us, D2052 by fours 110, D2050 by ones 163.)
-enum class Way { kTma, kFour, kOne };
-
-// Channels of a thread block and blocks of a cluster.
-struct Choice {
-    int width, cluster;
-};
-constexpr Choice kChoices[] = {{32, 1}, {32, 2}, {32, 4}, {32, 8}, {32, 16},
-                               {64, 1}, {64, 2}, {64, 4}, {128, 1}};   // the forward's by TMA
-
-// A launch's work: tokens of the longest sequence and of all, sequences, heads, channels.
-struct Work {
-    double longest, total, nseq, heads;
-    int D, size;             // size: bytes of a value of x
-    bool backward;
-    Way way;
-};
-
-// The time of a launch in us, as far as it takes to choose: how long a block takes for a tile
-// (`alone` on its SM, or one of two there; or HBM's rate shared by all that run), times the
-// tiles, times the waves.  The figures are fits to 55 shapes, forward and backward, with
-// every choice measured; over 70 others the choices made were 1.5% slower than the best on
-// average, 24% at most.  (Forward, bf16, us, as channels x cluster: B8 T2048 D2048 128x1 54,
-// 64x1 44, 32x1 46, 32x2 55; B1 T262144 D1024 32x4 466, 32x8 333, 32x16 444; B2 T143060 D176
-// 32x8 131, 32x16 95; fp32 B7 T458 D1360 64x1 18, 32x1 9; fp32 16 ragged sequences of 20000
-// tokens, D1024, 32x4 59, 32x1 47.)
-double estimate(const Work &k, Choice c, int sms) {
-    const int run = k.way == Way::kTma ? 4096 / c.width : k.way == Way::kFour ? 128 : 64;
-    const double tokens = run * c.cluster;
-    const double blocks = k.nseq * k.heads * ((k.D + c.width - 1) / c.width) * c.cluster;
-    // blocks that run alone on an SM, and at once: large clusters do not fill every part of the chip
-    const double one = sms * (c.cluster < 8 ? 1.0 : 0.72);
-    const bool single = k.backward && (k.way == Way::kFour || (k.way == Way::kTma && k.size == 4));
-    const double most = single ? one : sms * (c.cluster < 8 ? 2.0 : c.cluster == 8 ? 1.9 : 1.35);
-    double alone, two;
-    if (k.way == Way::kTma) {
-        alone = k.backward ? 1.4 : 1.0;
-        two = k.backward ? 2.2 : 0.4 * (k.size + 2);
-    } else if (k.way == Way::kFour) {
-        alone = k.backward ? 1.5 : 1.1;
-        two = 1.6;   // the backward's blocks are always alone
-    } else {
-        alone = k.backward ? 1.5 : 0.9;
-        two = k.backward ? 2.4 : 1.4;
-    }
-    if (c.cluster > 1) alone *= 1.4;
-    const double bytes = run * c.width * (k.backward ? 8 + 3 * k.size : 4 + 2 * k.size) / 6.5e6;
-    const auto tile = [&](double n) { return std::max(n <= one ? alone : two, n * bytes); };
-    const double begin = 1.5 + (c.cluster > 1 ? 0.18 * c.cluster : 0.0);
-    const double tiles = std::ceil(k.longest / tokens);
-    if (k.nseq == 1) {
-        const double waves = std::floor(blocks / most), rest = blocks - waves * most;
-        return waves * (tiles * tile(most) + begin) + (rest > 0 ? tiles * tile(rest) + begin : 0.0);
-    }
-    // the longest sequence, or all of them shared by the blocks that run at once
-    const double n = std::min(blocks, most), first = tiles * alone + begin;
-    const double all = blocks / n * ((k.total / k.nseq / tokens + 0.5) * tile(n) + begin);
-    return std::max(first, all) + 0.25 * std::min(first, all);
-}
-
-double plan(ScanArgs &a, const Work &k, int sms) {
-    const int count = k.way == Way::kTma && !k.backward ? 9 : 5;
-    double least = 0.0;
-    for (int i = 0; i < count; ++i) {
-        const double t = estimate(k, kChoices[i], sms);
-        if (i > 0 && t >= least) continue;
-        least = t;
-        a.width = kChoices[i].width;
-        a.cluster = kChoices[i].cluster;
-    }
-    return least;
-}
-
-// The same for threads that walk a sequence each: a chunk after another, and HBM's rate.
-// (us, bf16, walks / tiles: forward B256 T1 D4096 10 / 59, B64 T64 D4096 28 / 32, B64 T256 D4096
-// 104 / 84, B1 T64 D2048 7.1 / 3.4; backward B256 T16 D4096 53 / 306, B64 T100 D4096 87 / 102,
-// B64 T400 D4096 329 / 272.  Over 190 shapes the faster of both but for 0.6% on average, 30% at most.)
-double walk_time(const Work &k) {
-    const double chunks = std::ceil(k.longest / kChunk);
-    const double bytes = k.heads * k.total * k.D * (k.backward ? 8 + 3 * k.size : 4 + 2 * k.size);
-    return 1.0 + chunks * (k.backward ? 1.35 : 0.55) + bytes * (k.backward ? 1.2 : 1.0) / 6.5e6;
-}
-
 template <typename E>
 int launch_for(ScanArgs &a, bool backward, Way way, cudaStream_t stream) {
     if (way == Way::kOne) return backward ? launch_bwd<E, 1, 32, 8, 256, 0>(a, stream)
                                           : launch_fwd<E, 1, 32, 8, 256, 0>(a, stream);
-    if (way == Way::kFour) return backward ? launch_bwd<E, 4, 8, 4, 256, 0>(a, stream)
-                                           : launch_fwd<E, 4, 8, 4, 256, 0>(a, stream);
+    if constexpr (sizeof(E) == 2)   // four fp32 values are a piece that TMA takes
+        if (way == Way::kFour) return backward ? launch_bwd<E, 4, 8, 4, 256, 0>(a, stream)
+                                               : launch_fwd<E, 4, 8, 4, 256, 0>(a, stream);
     const int tokens = 4096 / a.width;
     const bool f32 = sizeof(E) == 4;
     const long long dims[3] = {a.D, a.rows, a.H};
@@ -1258,8 +1168,7 @@ int run(ScanArgs &a, bool backward, const int *cu_seqlens, int N, int H, int T_t
     const bool vec4 = D % 4 == 0 && aligned(16, a.x, a.log_alpha, a.h0, a.dhT, a.ckpt_in, a.d_h, a.h,
                                             a.hT, a.ga, a.ckpt_out);
     // TMA wants rows of whole 16-byte pieces
-    const Way way = !vec4 ? Way::kOne
-                    : T_total > 0 && (dtype == GLA_F32 || D % 8 == 0) ? Way::kTma : Way::kFour;
+    const Way way = !vec4 ? Way::kOne : dtype == GLA_F32 || D % 8 == 0 ? Way::kTma : Way::kFour;
     // longest first, so that the last thread blocks to start are short ones
     std::stable_sort(seqs.begin(), seqs.end(),
                      [](const ScanSeq &x, const ScanSeq &y) { return x.len > y.len; });
@@ -1271,8 +1180,10 @@ int run(ScanArgs &a, bool backward, const int *cu_seqlens, int N, int H, int T_t
         const Work work = {static_cast<double>(seqs[n].len), static_cast<double>(total),
                            static_cast<double>(a.nseq), static_cast<double>(H), D,
                            dtype == GLA_BF16 ? 2 : 4, backward, way};
-        const long long threads = static_cast<long long>(a.nseq) * H * (vec4 ? D / 4 : D);
-        if (plan(a, work, sms) >= walk_time(work) && threads < 0x7fffff00LL) {
+        const Layout plan = layout(work, sms);
+        a.width = plan.tiles.width;
+        a.cluster = plan.tiles.cluster;
+        if (plan.walk) {
             const int e = dtype == GLA_BF16
                               ? launch_short<__nv_bfloat16>(a, backward, vec4, stream)
                               : launch_short<float>(a, backward, vec4, stream);
