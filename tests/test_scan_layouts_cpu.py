@@ -5,6 +5,8 @@ from __future__ import annotations
 import random
 
 import scan_layouts as plan
+import test_gpu_scan
+import test_gpu_scan_layouts as gpu
 
 
 def calls(n, seed=0):
@@ -27,3 +29,37 @@ def test_every_layout_is_the_best_of_some_call():
         want = narrow if backward or way != plan.TMA else set(plan.choices())
         assert got == want | {"walk"}, (way, backward, got ^ (want | {"walk"}))
     assert len(seen) == 6
+
+
+def test_wide_cases_are_laid_out_as_they_say():
+    for (B, T, D, size), want in gpu.WIDE.items():
+        assert plan.way_of(D, size) == plan.TMA
+        assert plan.layout([T], B, D, size, False) == want, (B, T, D, size)
+    for (lens, H, D), want in gpu.WIDE_PACKED.items():
+        for size in (2, 4):
+            assert plan.way_of(D, size) == plan.TMA
+            assert plan.layout(lens, H or 1, D, size, False) == want, (lens, D, size)
+    # more tiles than are on their way at once (3): stages are used again
+    for (_, T, _, _), (width, _) in gpu.WIDE.items():
+        assert T > 4 * 4096 // width
+
+
+def test_the_gpu_tests_reach_every_layout():
+    def marked(test):   # the shapes of a parametrised test
+        return next(m.args[1] for m in test.pytestmark if m.args[0] in ("B,T,D", "T,D"))
+
+    shapes = [(2, T, 36) for T in test_gpu_scan.LENGTHS] + gpu.NARROW
+    shapes += [(3, 150, D) for D in test_gpu_scan.WIDTHS]
+    shapes += marked(test_gpu_scan.test_shapes_of_few_and_many_sequences)
+    shapes += marked(test_gpu_scan.test_many_short_sequences)
+    seen = {(plan.way_of(D, size), size, False, want) for (_, _, D, size), want in gpu.WIDE.items()}
+    for B, T, D in shapes:
+        for size in (2, 4):
+            for backward in (False, True):
+                seen.add((plan.way_of(D, size), size, backward,
+                          plan.layout([T], B, D, size, backward)))
+    for way, size in ((plan.TMA, 2), (plan.TMA, 4), (plan.FOUR, 2), (plan.ONE, 2), (plan.ONE, 4)):
+        for backward in (False, True):
+            for choice in ["walk"] + plan.choices():
+                if choice == "walk" or choice[0] == 32 or (way == plan.TMA and not backward):
+                    assert (way, size, backward, choice) in seen
