@@ -6,7 +6,9 @@
 // registers, its threads a few tokens each; each maps the state before its tokens to
 // the state after them, and these maps are joined over the block and, where few
 // sequences leave the device idle, over a cluster of blocks that stand side by side
-// in time.  The blocks walk the sequence together, tile after tile.  A block waits for
+// in time.  The blocks walk the sequence together, tile after tile.  (A state that crosses
+// tokens as P s loses what is left of it once P falls below fp32's range, 2^-126 of its size;
+// a thread's own tokens and the decode step multiply gate by gate.)  A block waits for
 // others of its own cluster only (and never longer than the library's limit), nothing is
 // added in an order that the scheduler chooses, and no memory but the arguments is used.
 //

@@ -466,8 +466,13 @@ enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
  * may overlap an input, and no output another.  A bounded device wait that
  * expires leaves the outputs unspecified and is reported by
  * gla_last_device_status (GLA_ERR_TIMEOUT).
- * Accuracy: with M the recurrence on |x|, |h0| and N the recurrence on M,
- * |h - exact| <= 2^-24 (4 N + 8 M) before the rounding to dtype.
+ * Accuracy: with M the recurrence on |x|, |h0|, N the recurrence on M, and G the
+ * largest M of the tokens before (|h0| among them), |h - exact| <=
+ * 2^-24 (4 N + 8 M) + 2^-125 G + 2^-119 before the rounding to dtype.  The last
+ * two: a gate below fp32's range counts as 0, and so does the product of the
+ * gates of tokens that are taken together.  Gradients g are alike, from the end.
+ * An infinite or NaN state makes every later one of its channel infinite or NaN,
+ * past a gate of 0 too.
  *
  * Any D >= 1 and T >= 1, pointers aligned to their elements.  Fastest with every
  * pointer at a multiple of 16 bytes and D a multiple of 8 (4 for GLA_F32), next
