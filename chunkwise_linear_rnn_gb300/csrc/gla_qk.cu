@@ -173,7 +173,9 @@ __device__ __forceinline__ unsigned long long turn_of(double inv_freq) {
 // cos and sin of a phase in 2^32nds of a turn (a third of the instructions of sincospif,
 // which does not know that its argument is reduced): the nearest quarter by integers, then
 // Chebyshev fits in the square of what is left, |x| <= 1/2 quarters (sin = x S(x^2), cos =
-// 1 + x^2 C(x^2); each within a rounding of 2^-24).
+// 1 + x^2 C(x^2)).  The fits are within a rounding of 2^-24; with those of x, its square and
+// the products the values are off by 1.72 * 2^-24 at most and 0.35 * 2^-24 in the root mean
+// square (33 million phases; a rounded 64-bit value: 0.5 and 0.24).
 __device__ __forceinline__ float2 cos_sin(unsigned phase) {
     const unsigned quarter = (phase + 0x20000000u) >> 30;
     const float x = static_cast<float>(static_cast<int>(phase - (quarter << 30))) * 9.313225746154785e-10f;
