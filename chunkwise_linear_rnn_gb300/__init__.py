@@ -732,9 +732,9 @@ def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | No
                  checkpoints: torch.Tensor | None = None):
     """The gated linear recurrence ``h_t = exp(log_alpha_t) h_{t-1} + x_t``, elementwise.
 
-    ``x`` ``[B, T, D]`` or ``[B, H, T, D]``, bf16 or fp32; ``log_alpha`` the same
-    shape in fp32, <= 0 (-inf is a gate of zero); ``h0`` ``[B, D]`` / ``[B, H, D]``
-    fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
+    ``x`` ``[B, T, D]`` or ``[B, H, T, D]``, bf16 or fp32, contiguous as all tensors
+    here; ``log_alpha`` the same shape in fp32, <= 0 (-inf is a gate of zero); ``h0``
+    ``[B, D]`` / ``[B, H, D]`` fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
     fp32 on the way, and the last one in fp32 (None when ``output_final_state`` is
     False).  ``final_state`` may be ``h0`` itself; no other output may share memory
     with an input, and no output with another.  ``checkpoints`` (from
@@ -951,7 +951,7 @@ def gla_qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tenso
     fp32 or None) and, with ``inv_freq`` (fp64 ``[rot/2]``, see
     ``gla_rope_frequencies``), the pairs of its first ``rot`` values are turned by
     ``position * inv_freq``: pairs ``(i, i + rot/2)``, or ``(2i, 2i + 1)`` when
-    ``interleaved``.  ``positions`` is int64 ``[B, T]`` or ``[T]`` (None: 0 .. T-1).
+    ``interleaved``.  ``positions`` is int64 ``[B, T]`` or ``[T]``, contiguous (None: 0 .. T-1).
     d and rot are multiples of 8, up to 256.
     """
     return _qk_fwd(q, *_qk_sizes(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,

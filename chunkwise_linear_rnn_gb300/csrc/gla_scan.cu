@@ -16,7 +16,7 @@
 //
 // Both directions are bound by HBM: 8 bytes an element forward (bf16 x, fp32 gates, bf16
 // h), 14 backward, against about 20 instructions.  Measured on one GB300: forward B8 T2048
-// D2048 43 us (6.2 TB/s of a copy's 6.67), B1 T262144 D1024 335 us (6.4 TB/s); backward B8
+// D2048 42 us (6.3 TB/s of a copy's 6.67), B1 T262144 D1024 335 us (6.4 TB/s); backward B8
 // T2048 D2048 80 us (5.9 TB/s).  With few sequences the blocks of one SM, not HBM, set the
 // pace: two of them on some SMs and one on others.
 #include <cuda_bf16.h>

@@ -43,9 +43,9 @@ struct Work {
 // (`alone` on its SM, or one of two there; or HBM's rate shared by all that run), times the
 // tiles, times the waves.  The figures are fits to 55 shapes, forward and backward, with
 // every choice measured; over 70 others the choices made were 1.5% slower than the best on
-// average, 24% at most.  (Forward, bf16, us, as channels x cluster: B8 T2048 D2048 128x1 54,
-// 64x1 44, 32x1 46, 32x2 55; B1 T262144 D1024 32x4 466, 32x8 333, 32x16 444; B2 T143060 D176
-// 32x8 131, 32x16 95; fp32 B7 T458 D1360 64x1 18, 32x1 9; fp32 16 ragged sequences of 20000
+// average, 24% at most.  (Forward, bf16, us, as channels x cluster: B8 T2048 D2048 128x1 47,
+// 64x1 42, 32x1 46, 32x2 55; B16 T512 D2048 128x1 24, 64x1 27; B1 T262144 D1024 32x4 466, 32x8 333, 32x16 444; B2 T143060 D176
+// 32x8 131, 32x16 95; fp32 B7 T458 D1360 64x1 14, 32x1 12; fp32 16 ragged sequences of 20000
 // tokens, D1024, 32x4 59, 32x1 47.)
 inline double estimate(const Work &k, Choice c, int sms) {
     const int run = k.way == Way::kTma ? 4096 / c.width : k.way == Way::kFour ? 128 : 64;
