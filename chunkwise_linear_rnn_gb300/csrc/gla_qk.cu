@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "gla.h"
@@ -536,20 +537,22 @@ __global__ void __launch_bounds__(1024)
 
 // The work of a call as a grid: eight tokens to a block, and the heads in as many chunks
 // (of whole rounds of the warps' rows) as fill the device with small batches.  `most`:
-// blocks at most, the rest of the tokens taken by the same blocks.
-dim3 grid_of(QkArgs &a, int rows, long long most, int sms) {
+// blocks at most, the rest of the tokens taken by the same blocks.  `rounds_each`: rounds of a
+// token that a block takes at most, as long as `most` blocks are enough for that.
+dim3 grid_of(QkArgs &a, int rows, long long most, int rounds_each, int sms) {
     const long long tokens = static_cast<long long>(a.B) * a.T;
     const long long groups = (tokens + kWarps - 1) / kWarps;
     const int heads = a.H[0] + a.H[1], rounds = (heads + rows - 1) / rows;
-    const long long want = std::max<long long>(1, (4LL * sms + groups - 1) / groups);
+    const long long want = std::max<long long>((4LL * sms + groups - 1) / groups,
+                                               (rounds - 1) / rounds_each + 1);
     const int chunks = static_cast<int>(std::min<long long>({want, rounds, 65535, most}));
     a.chunk = (rounds + chunks - 1) / chunks * rows;
     const int y = (heads + a.chunk - 1) / a.chunk;
     return dim3(static_cast<unsigned>(std::max<long long>(1, std::min(groups, most / y))), y);
 }
 
-// Rows that a lane adds one after another in 32 bits for the weight gradients, at most (but a
-// token's own heads, of which a block takes more than so many rounds from 300,000 heads on): a
+// Rows that a lane adds one after another in 32 bits for the weight gradients, at most: a
+// token's many heads go to several blocks (enough for 300,000 heads; more add more), and a
 // longer batch takes several launches, whose sums are added in 64 bits.  (As a test in the
 // kernel, once a token, it took 5% of the time: 54 us -> 56.5 for B4 T4096, 32+8 heads of 64.)
 constexpr int kSumRows = 1024;
@@ -557,9 +560,9 @@ constexpr int kSumRows = 1024;
 template <typename E, int LANES, bool HALVES, bool PART>
 int launch_bwd(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
     constexpr int ROWS = 32 / LANES;
-    const dim3 grid = grid_of(a, ROWS, kPartials, sms);
-    const long long tokens = static_cast<long long>(a.B) * a.T;
     // q's and k's heads of a block may each end in a short round
+    const dim3 grid = grid_of(a, ROWS, kPartials, a.partial ? kSumRows - 1 : INT_MAX, sms);
+    const long long tokens = static_cast<long long>(a.B) * a.T;
     const long long each = std::max(1, kSumRows / (a.chunk / ROWS + 1));
     const long long step = a.partial ? each * grid.x * kWarps : tokens;
     for (a.first = 0; a.first < tokens; a.first = a.end) {
@@ -580,7 +583,7 @@ int launch_one(QkArgs &a, const WeightGrads &to, int sms, cudaStream_t stream) {
     if constexpr (BACKWARD) {
         return launch_bwd<E, LANES, HALVES, PART>(a, to, sms, stream);
     } else {
-        const dim3 grid = grid_of(a, 32 / LANES, kFwdBlocks * sms, sms);
+        const dim3 grid = grid_of(a, 32 / LANES, kFwdBlocks * sms, INT_MAX, sms);
         qk_fwd_kernel<E, LANES, HALVES, PART><<<grid, 32 * kWarps, 0, stream>>>(a);
         return static_cast<int>(cudaGetLastError());
     }

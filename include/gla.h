@@ -589,8 +589,8 @@ int gla_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const fl
  * 16-byte aligned, for the weight gradients' partial sums (GLA_ERR_SCRATCH
  * when scratch_bytes is smaller): each thread block sums its rows in a fixed
  * order, and a second kernel adds the blocks', so equal calls give equal bits.
- * No more than 2^10 rows are added one after another in 32 bits (2^10 heads of a
- * token in 300,000 or more); the rest of a longer batch is added in 64.
+ * A thread adds no more than 2^10 rows one after another in 32 bits (up to
+ * 300,000 heads); the rest of a longer batch is added in 64.
  * Two calls that may run at the same time need scratch of their own.
  */
 unsigned long gla_qk_norm_rope_bwd_scratch(int d);

@@ -19,7 +19,8 @@ def _built():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
-@pytest.mark.parametrize("T,Hq,Hk", [(19456, 8192, 4), (19450, 4, 4099), (80000000, 1, 1)])
+@pytest.mark.parametrize("T,Hq,Hk", [(19456, 8192, 4), (19450, 4, 4099), (80000000, 1, 1),
+                                     (4864, 100003, 4), (9728, 3, 60001)])
 def test_equal_rows(T, Hq, Hk, dtype):
     """Every row is the same, so that a weight's gradient is the number of rows times one
     product, and every addition to a running sum is rounded in the same direction.
