@@ -734,11 +734,11 @@ def gla_scan_fwd(x: torch.Tensor, log_alpha: torch.Tensor, h0: torch.Tensor | No
 
     ``x`` ``[B, T, D]`` or ``[B, H, T, D]``, bf16 or fp32, contiguous as all tensors
     here; ``log_alpha`` the same shape in fp32, <= 0 (-inf is a gate of zero); ``h0``
-    ``[B, D]`` / ``[B, H, D]`` fp32 or None (zero).  Returns ``(h, hT)``: every state in ``x``'s type, kept in
-    fp32 on the way, and the last one in fp32 (None when ``output_final_state`` is
-    False).  ``final_state`` may be ``h0`` itself; no other output may share memory
-    with an input, and no output with another.  ``checkpoints`` (from
-    ``gla_scan_checkpoints``) is filled for ``gla_scan_bwd``.
+    ``[B, D]`` / ``[B, H, D]`` fp32 or None (zero).  Returns ``(h, hT)``: every state
+    in ``x``'s type, kept in fp32 on the way, and the last one in fp32 (None when
+    ``output_final_state`` is False).  ``final_state`` may be ``h0`` itself; no other
+    output may share memory with an input, and no output with another.
+    ``checkpoints`` (from ``gla_scan_checkpoints``) is filled for ``gla_scan_bwd``.
     """
     return _scan_fwd(x, log_alpha, None, h0, output_final_state, out, final_state, checkpoints)
 

@@ -28,7 +28,9 @@
 namespace gla {
 namespace {
 
-constexpr int kPartials = 304;   // thread blocks of the backward, at most (2 for each of 152 SMs)
+// Thread blocks of the backward, at most: 2 for each of 152 SMs.  A constant, since the scratch
+// that they leave their sums in is sized by d alone.
+constexpr int kPartials = 304;
 constexpr long long kFwdBlocks = 8;   // thread blocks of the forward for each SM, at most
 
 struct QkArgs {

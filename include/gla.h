@@ -479,8 +479,9 @@ enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
  * with D a multiple of 4; other calls take one channel at a time and need up to
  * twice the time.  Returns GLA_ERR_ARG for null required pointers, non-positive
  * sizes, an unknown dtype, misaligned pointers or more than 2^31 thread blocks
- * of work; GLA_ERR_LAUNCH also where a part of a device cannot place a cluster of 16
- * thread blocks, which few channels over a long sequence take; GLA_ERR_ALLOC when the host has no memory for a packed batch's table.
+ * of work; GLA_ERR_LAUNCH also where a part of a device cannot place a cluster
+ * of 16 thread blocks, which few channels over a long sequence take;
+ * GLA_ERR_ALLOC when the host has no memory for a packed batch's table.
  */
 #define GLA_SCAN_BLOCK 64
 int gla_scan_fwd(const void *x, const float *log_alpha, const float *h0, void *h, float *hT,
@@ -553,9 +554,9 @@ int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, in
  *   inv_freq   : fp64 [rot / 2], device, finite, nullable when rot = 0
  *   q_out,k_out: [B, Hq, T, d] and [B, Hk, T, d] dtype, contiguous
  *
- * Sums and rotations are fp32; each value is rounded once.  A row whose squares add
- * up past fp32's range (values near 10^19) comes out as zeros.  d a multiple of 8 up
- * to 256, rot a multiple of 8 up to d (GLA_ERR_SHAPE otherwise).  GLA_ERR_ARG for
+ * Sums and rotations are fp32; each value is rounded once.  A row whose squares
+ * add up past fp32's range (values near 10^19) comes out as zeros.  d a multiple of 8
+ * up to 256, rot a multiple of 8 up to d (GLA_ERR_SHAPE otherwise).  GLA_ERR_ARG for
  * null required pointers, non-positive sizes, eps not in (0, 1], unknown dtype,
  * norm or interleaved, strides that are negative or not multiples of 8 elements,
  * more than 2^30 heads,
