@@ -30,7 +30,8 @@ __all__ = ["gla_chunk_fwd", "gla_chunk_fwd_varlen", "gla_chunk_fwd_varlen_plan",
            "gla_scan_fwd", "gla_scan_bwd", "gla_scan", "gla_scan_step", "gla_scan_fwd_varlen",
            "gla_scan_bwd_varlen", "gla_scan_varlen", "gla_scan_checkpoints",
            "gla_qk_norm_rope_fwd", "gla_qk_norm_rope_bwd", "gla_qk_norm_rope",
-           "gla_rope_frequencies",
+           "gla_rope_frequencies", "gla_headgate_fwd_varlen", "gla_headgate_step",
+           "gla_group_norm_act_fwd", "gla_group_norm_act_bwd", "gla_group_norm_act",
            "gla_recurrent_step", "gla_last_device_status", "GlaError", "status_string",
            "library_path"]
 
@@ -1024,6 +1025,314 @@ def gla_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | 
     """Differentiable ``gla_qk_norm_rope_fwd``: gradients of q, k and the weights."""
     return _GlaQkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, norm, eps,
                                 interleaved)
+
+
+def _steps(name: str, meta, *dims) -> list:
+    """The strides of a tensor over `dims`, 0 for one that is never stepped over; its last
+    dimension has to be contiguous."""
+    shape, strides = meta[:2]
+    if strides[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return [strides[i] if shape[i] > 1 else 0 for i in dims]
+
+
+def _span(t) -> tuple:
+    """The first address of a tensor's elements, and the one behind the last."""
+    first = t.data_ptr()
+    if t.numel() == 0:
+        return first, first
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return first, first + (last + 1) * t.element_size()
+
+
+def _clear_of(out, name: str, *others) -> None:
+    """`_apart` for inputs that may be strided."""
+    first, last = _span(out)
+    for t in others:
+        if t is not None:
+            begin, end = _span(t)
+            if first < end and begin < last:
+                raise ValueError(f"{name} must not share memory with an input")
+
+
+@functools.lru_cache(maxsize=256)
+def _headgate_checked(q, k, v, log_alpha, kinds):
+    """The checks of a gla_headgate call's q, k, v and gates: (rows, Hk, H, dk, dv) and the C
+    call's layout, of the tensors' `_meta`s alone."""
+    (qn, _, kind, dev) = q
+    if dev.type != "cuda":
+        raise ValueError("q must be on a CUDA device")
+    if kind not in kinds:
+        raise TypeError("q must be a " + " or ".join(map(str, kinds)) + " tensor")
+    if len(qn) != 3 or len(v[0]) != 3:
+        raise ValueError("q, k and v must be [rows, heads, d]")
+    rows, Hk, dk = qn
+    H, dv = v[0][1:]
+    for name, meta, shape in (("k", k, (rows, Hk, dk)), ("v", v, (rows, H, dv))):
+        if meta[3] != dev:
+            raise ValueError(f"{name} must be on the CUDA device {dev}")
+        if meta[2] is not kind:
+            raise TypeError(f"{name} must be {kind}, got {meta[2]}")
+        if tuple(meta[0]) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(meta[0])}")
+    if Hk < 1 or H % Hk:
+        raise ValueError("v must have a multiple of the heads of q and k")
+    an, steps, a_kind, a_dev = log_alpha
+    if a_dev != dev:
+        raise ValueError(f"log_alpha must be on the CUDA device {dev}")
+    if a_kind is not torch.float32:
+        raise TypeError(f"log_alpha must be torch.float32, got {a_kind}")
+    if tuple(an) not in ((rows, H), (H,)):
+        raise ValueError(f"log_alpha must have shape {(rows, H)} or {(H,)}, got {tuple(an)}")
+    _ints(rows, Hk, H, dk, dv)
+    layout = _lib.GlaHeadgateLayout(
+        *_steps("q", q, 0, 1), *_steps("k", k, 0, 1), *_steps("v", v, 0, 1),
+        steps[0] if len(an) == 2 and rows > 1 else 0, steps[-1] if H > 1 else 0)
+    return (rows, Hk, H, dk, dv), ctypes.byref(layout), _DTYPES[kind]
+
+
+def _headgate(q, k, v, log_alpha, *kinds):
+    if q is None or k is None or v is None or log_alpha is None:
+        raise TypeError("q, k, v and log_alpha must be torch.Tensors")
+    try:
+        return _headgate_checked(_meta(q), _meta(k), _meta(v), _meta(log_alpha), kinds)
+    except AttributeError:
+        _all_tensors(q=q, k=k, v=v, log_alpha=log_alpha)
+        raise
+
+
+@functools.lru_cache(maxsize=256)
+def _headgate_lengths(cu: tuple, T: int, H: int, dk: int, dv: int):
+    """The bounds of a packed batch as the C call takes them, and the bytes of its scratch."""
+    if len(cu) < 2:
+        raise ValueError("cu_seqlens needs at least two entries")
+    if cu[0] != 0 or cu[-1] != T or any(b < a for a, b in zip(cu, cu[1:])):
+        raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
+    c = (ctypes.c_int * len(cu))(*cu)
+    return c, _entry("gla_headgate_fwd_varlen_scratch")(c, len(cu) - 1, H, dk, dv)
+
+
+def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            log_alpha: torch.Tensor, cu_seqlens, scale: float | None = None,
+                            h0: torch.Tensor | None = None, output_final_state: bool = True, *,
+                            final_state: torch.Tensor | None = None):
+    """Packed prompts through attention with one gate per token and head (chunkwise).
+
+    ``S_t = exp(log_alpha_t) S_{t-1} + k_t^T v_t``, ``o_t = scale q_t S_t`` with a gate that
+    all channels of a head share.  q, k ``[T_total, Hk, dk]`` and v ``[T_total, H, dv]`` bf16,
+    token-major as a projection leaves them: strided views with a contiguous last dimension
+    are read in place (strides in multiples of 8 elements, 16-byte aligned).  H is a multiple
+    of Hk: each key head serves H / Hk neighbouring value heads.  ``log_alpha`` is
+    ``[T_total, H]`` fp32 with any strides, or ``[H]``: a fixed decay for each head (<= 0;
+    -inf is a gate of zero).  dk is a multiple of 8 up to 128, dv up to 256.
+
+    Sequence ``n`` holds rows ``cu_seqlens[n] : cu_seqlens[n+1]``; ``cu_seqlens`` is a host
+    sequence of ``N + 1`` ints.  ``h0`` is ``[N, H, dk, dv]`` fp32 or None (zero).  Returns
+    ``(o, hT)``: ``[T_total, H, dv]`` bf16 and the last states in fp32 (an empty sequence
+    keeps its own; None when ``output_final_state`` is False).  ``final_state`` may be ``h0``
+    itself.  For gradients see ``gla_chunk``, which takes ``[B, H, T]`` gates head-first.
+    """
+    (T, Hk, H, dk, dv), layout, _ = _headgate(q, k, v, log_alpha, torch.bfloat16)
+    dev = q.device
+    cu = tuple(_bounds(cu_seqlens))
+    bounds, size = _headgate_lengths(cu, T, H, dk, dv)
+    N = len(cu) - 1
+    state = (N, H, dk, dv)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, state, dev)
+    hT = None
+    if output_final_state:
+        hT = final_state
+        if hT is None:
+            hT = torch.empty(state, dtype=torch.float32, device=dev)
+        else:
+            _need(hT, "final_state", torch.float32, state, dev)
+            _clear_of(hT, "final_state", q, k, v, log_alpha,
+                      None if h0 is None or h0.data_ptr() == hT.data_ptr() else h0)
+    o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+    scratch = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _call("gla_headgate_fwd_varlen", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), dk ** -0.5 if scale is None else float(scale), _ptr(h0),
+          o.data_ptr(), _ptr(hT), bounds, N, T, Hk, H, dk, dv, layout, _ptr(scratch), size)
+    return o, hT
+
+
+def gla_headgate_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alpha: torch.Tensor,
+                      h: torch.Tensor, scale: float | None = None, *,
+                      slots: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """One decode token of ``gla_headgate_fwd_varlen`` for each of B rows; returns o.
+
+    q, k ``[B, Hk, dk]``, v ``[B, H, dv]``, bf16 or fp32, strided as there; log_alpha
+    ``[B, H]`` or ``[H]`` fp32.  ``h`` ``[S, H, dk, dv]`` fp32 is a pool of states, updated in
+    place: row ``b`` has entry ``slots[b]`` (int64 on the device, read as the kernel runs, so
+    that a captured step takes new ones), or entry ``b`` without ``slots``.  A negative slot is a
+    row of padding: its output is zero.  So is that of a row whose slot is S or more or has
+    come before, and ``gla_last_device_status`` then reports GLA_ERR_ARG.
+    """
+    (B, Hk, H, dk, dv), layout, dtype = _headgate(q, k, v, log_alpha, torch.bfloat16,
+                                                  torch.float32)
+    dev = q.device
+    if not isinstance(h, torch.Tensor) or h.dim() != 4:
+        raise ValueError("h must be [S, H, dk, dv]")
+    S = h.shape[0]
+    _need(h, "h", torch.float32, (S, H, dk, dv), dev)
+    if slots is not None:
+        _need(slots, "slots", torch.int64, (B,), dev)
+    elif S < B:
+        raise ValueError("h must have a state for each row, or slots be given")
+    _clear_of(h, "h", q, k, v, log_alpha, slots)
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", q.dtype, (B, H, dv), dev)
+        _clear_of(out, "out", q, k, v, log_alpha, slots, h)
+    _call("gla_headgate_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          log_alpha.data_ptr(), dk ** -0.5 if scale is None else float(scale), h.data_ptr(),
+          _ptr(slots), out.data_ptr(), B, S, Hk, H, dk, dv, layout, dtype)
+    return out
+
+
+_NORM_ACT_NORMS = {"rms": _lib.GLA_NORM_RMS, "layer": _lib.GLA_NORM_LAYER}
+_ACTIVATIONS = {"silu": _lib.GLA_ACT_SILU, "sigmoid": _lib.GLA_ACT_SIGMOID}
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_act_checked(x, gate, weight, bias, dx, norm, activation, eps):
+    """The checks of a gla_group_norm_act call's arguments and the C call's sizes, layout and
+    options: functions of the tensors' `_meta`s and of the options alone.  dx: None forward."""
+    shape, _, kind, dev = x
+    if kind not in _DTYPES:
+        raise TypeError("x must be a torch.bfloat16 or torch.float32 tensor")
+    if dev.type != "cuda":
+        raise ValueError("x must be on a CUDA device")
+    if len(shape) not in (3, 4):
+        raise ValueError("x must be [T, H, d] or [B, T, H, d]")
+    B, T, H, d = (1, *shape) if len(shape) == 3 else shape
+    if min(B, T, H, d) < 1:
+        raise ValueError("x must have elements")
+    dims = (0, 1) if len(shape) == 3 else (0, 1, 2)
+    lead = [0] if len(shape) == 3 else []
+    steps = lead + _steps("x", x, *dims)
+    if gate is not None:
+        if gate[3] != dev:
+            raise ValueError(f"gate must be on the CUDA device {dev}")
+        if gate[2] is not kind:
+            raise TypeError(f"gate must be {kind}, got {gate[2]}")
+        if gate[0] != shape:
+            raise ValueError(f"gate must have shape {tuple(shape)}, got {tuple(gate[0])}")
+        steps += lead + _steps("gate", gate, *dims)
+    else:
+        steps += [0, 0, 0]
+    steps += [0, 0, 0] if dx is None else lead + _steps("dx", dx, *dims)
+    if norm not in _NORM_ACT_NORMS:
+        raise ValueError("norm must be 'rms' or 'layer'")
+    if activation not in _ACTIVATIONS:
+        raise ValueError("activation must be 'silu' or 'sigmoid'")
+    per_channel = any(t is not None and len(t[0]) == 2 for t in (weight, bias))
+    _fits(weight, "weight", torch.float32, (H, d) if per_channel else (d,), dev)
+    _fits(bias, "bias", torch.float32, (H, d) if per_channel else (d,), dev)
+    _ints(B, T, H, d)
+    layout = _lib.GlaNormActLayout(*steps)
+    options = _lib.GlaNormActOptions(dtype=_DTYPES[kind], norm=_NORM_ACT_NORMS[norm],
+                                     activation=_ACTIVATIONS[activation],
+                                     per_channel=int(per_channel), eps=eps)
+    return B, T, H, d, ctypes.byref(layout), ctypes.byref(options)
+
+
+def _norm_act_sizes(x, gate, weight, bias, dx, norm, activation, eps):
+    if x is None:
+        raise TypeError("x must be a torch.Tensor")
+    try:
+        return _norm_act_checked(_meta(x), _meta(gate), _meta(weight), _meta(bias), _meta(dx),
+                                 norm, activation, float(eps))
+    except AttributeError:
+        _all_tensors(x=x, gate=gate, weight=weight, bias=bias)
+        raise
+
+
+def gla_group_norm_act_fwd(x: torch.Tensor, gate: torch.Tensor | None = None,
+                           weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                           *, norm: str = "rms", activation: str = "silu",
+                           eps: float = 1e-5) -> torch.Tensor:
+    """The norm of each head's channels and the activation behind it, in one pass.
+
+    ``n = (x - mean) / sqrt(mean((x - mean)^2) + eps) * weight + bias`` over the last dimension
+    of x (``norm="layer"``: a group norm of the token's channels with one group a head;
+    ``"rms"``: without the mean), then ``n * f(gate)``, or ``f(n)`` without a gate, with f
+    ``silu`` or ``sigmoid``.
+
+    x and gate are ``[B, T, H, d]`` or ``[T, H, d]``, bf16 or fp32; strided views with a
+    contiguous last dimension are read in place (strides in multiples of 8 elements, 16-byte
+    aligned): ``o.transpose(1, 2)`` of a head-first output, a slice of a fused projection.
+    weight and bias are fp32, ``[d]`` or, both, ``[H, d]``.  Returns a contiguous tensor of x's
+    shape and type.  d is a multiple of 8 up to 512.
+    """
+    sizes = _norm_act_sizes(x, gate, weight, bias, None, norm, activation, eps)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _call("gla_group_norm_act_fwd", x.device, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
+          y.data_ptr(), *sizes)
+    return y
+
+
+def _norm_act_bwd(dy, x, gate, weight, bias, options, need_dweight, need_dbias):
+    # the gradient of x lies as x does where x has no gaps and no overlaps
+    dx = torch.empty_like(x)
+    if dx.stride(-1) != 1:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    sizes = _norm_act_sizes(x, gate, weight, bias, dx, *options)
+    dev = x.device
+    dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dw = torch.empty_like(weight) if weight is not None and need_dweight else None
+    db = torch.empty_like(bias) if bias is not None and need_dbias else None
+    scratch, size = None, 0
+    if dw is not None or db is not None:
+        size = _entry("gla_group_norm_act_bwd_scratch")(*sizes[:4])
+        scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+    _call("gla_group_norm_act_bwd", dev, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
+          dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), *sizes, _ptr(scratch),
+          size)
+    return dx, dgate, dw, db
+
+
+def gla_group_norm_act_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor | None = None,
+                           weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                           *, norm: str = "rms", activation: str = "silu", eps: float = 1e-5,
+                           need_dweight: bool = True, need_dbias: bool = True):
+    """Gradients of ``<dy, y>`` through ``gla_group_norm_act_fwd``; dy is contiguous like y.
+
+    Returns ``(dx, dgate, dweight, dbias)``: dx with x's strides (contiguous where x has
+    gaps), dgate contiguous, both in x's type; fp32 sums over every token like weight and
+    bias (None without them, or when not needed).
+    """
+    _norm_act_sizes(x, gate, weight, bias, None, norm, activation, eps)
+    _need(dy, "dy", x.dtype, x.shape, x.device)
+    return _norm_act_bwd(dy, x, gate, weight, bias, (norm, activation, eps), need_dweight,
+                         need_dbias)
+
+
+class _GlaGroupNormAct(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, weight, bias, norm, activation, eps):
+        ctx.save_for_backward(x, gate, weight, bias)
+        ctx.options = norm, activation, eps
+        return gla_group_norm_act_fwd(x, gate, weight, bias, norm=norm, activation=activation,
+                                      eps=eps)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy):
+        x, gate, weight, bias = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        return (*_norm_act_bwd(_like(dy, x.dtype), x, gate, weight, bias, ctx.options, need[2],
+                               need[3]), None, None, None)
+
+
+def gla_group_norm_act(x: torch.Tensor, gate: torch.Tensor | None = None,
+                       weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+                       norm: str = "rms", activation: str = "silu", eps: float = 1e-5):
+    """Differentiable ``gla_group_norm_act_fwd``: gradients of x, gate, weight and bias."""
+    return _GlaGroupNormAct.apply(x, gate, weight, bias, norm, activation, eps)
 
 
 def gla_last_device_status(device: torch.device | int | None = None) -> int:

@@ -31,7 +31,9 @@ EXPORTED = ("gla_chunk_fwd", "gla_chunk_fwd_ex", "gla_chunk_fwd_plan", "gla_chun
             "gla_gdn_fwd", "gla_gdn_chunk_fwd", "gla_recurrent_step",
             "gla_scan_fwd", "gla_scan_bwd", "gla_scan_fwd_varlen", "gla_scan_bwd_varlen",
             "gla_scan_step", "gla_qk_norm_rope_fwd", "gla_qk_norm_rope_bwd",
-            "gla_qk_norm_rope_bwd_scratch", "gla_status_string",
+            "gla_qk_norm_rope_bwd_scratch", "gla_headgate_fwd_varlen",
+            "gla_headgate_fwd_varlen_scratch", "gla_headgate_step", "gla_group_norm_act_fwd",
+            "gla_group_norm_act_bwd", "gla_group_norm_act_bwd_scratch", "gla_status_string",
             "gla_last_device_status", "gla_version")
 
 
@@ -40,6 +42,10 @@ GLA_BF16 = 0
 GLA_F32 = 1
 GLA_NORM_RMS = 0
 GLA_NORM_L2 = 1
+GLA_NORM_LAYER = 2
+# Activations (enum gla_activation).
+GLA_ACT_SILU = 0
+GLA_ACT_SIGMOID = 1
 # Tokens of one block of a scan's checkpoints (GLA_SCAN_BLOCK).
 SCAN_BLOCK = 64
 
@@ -66,6 +72,24 @@ class GlaQkOptions(ctypes.Structure):
     """gla_qk_options (include/gla.h)."""
     _fields_ = [("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("interleaved", ctypes.c_int),
                 ("eps", ctypes.c_float)]
+
+
+class GlaHeadgateLayout(ctypes.Structure):
+    """gla_headgate_layout (include/gla.h): strides of q, k, v and log_alpha, in elements."""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("q_st", "q_sh", "k_st", "k_sh", "v_st", "v_sh",
+                                                 "a_st", "a_sh")]
+
+
+class GlaNormActLayout(ctypes.Structure):
+    """gla_norm_act_layout (include/gla.h): strides of x, gate and grad_x, in elements."""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("x_sb", "x_st", "x_sh", "g_sb", "g_st", "g_sh",
+                                                 "dx_sb", "dx_st", "dx_sh")]
+
+
+class GlaNormActOptions(ctypes.Structure):
+    """gla_norm_act_options (include/gla.h)."""
+    _fields_ = [("dtype", ctypes.c_int), ("norm", ctypes.c_int), ("activation", ctypes.c_int),
+                ("per_channel", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
 class GlaError(RuntimeError):
@@ -142,6 +166,21 @@ def _bind(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gla_qk_norm_rope_bwd.restype = i
     lib.gla_qk_norm_rope_bwd_scratch.argtypes = [i]
     lib.gla_qk_norm_rope_bwd_scratch.restype = ctypes.c_ulong
+    ul, lay = ctypes.c_ulong, ctypes.POINTER(GlaHeadgateLayout)
+    lib.gla_headgate_fwd_varlen_scratch.argtypes = [ip, i, i, i, i]
+    lib.gla_headgate_fwd_varlen_scratch.restype = ul
+    lib.gla_headgate_fwd_varlen.argtypes = [vp, vp, vp, fp, f, fp, vp, fp, ip, i, i, i, i, i, i,
+                                            lay, vp, ul, vp]
+    lib.gla_headgate_fwd_varlen.restype = i
+    lib.gla_headgate_step.argtypes = [vp, vp, vp, fp, f, fp, vp, vp, i, i, i, i, i, i, lay, i, vp]
+    lib.gla_headgate_step.restype = i
+    norm = [i, i, i, i, ctypes.POINTER(GlaNormActLayout), ctypes.POINTER(GlaNormActOptions)]
+    lib.gla_group_norm_act_fwd.argtypes = [vp, vp, fp, fp, vp] + norm + [vp]
+    lib.gla_group_norm_act_fwd.restype = i
+    lib.gla_group_norm_act_bwd_scratch.argtypes = [i, i, i, i]
+    lib.gla_group_norm_act_bwd_scratch.restype = ul
+    lib.gla_group_norm_act_bwd.argtypes = [vp, vp, fp, fp, vp, vp, vp, fp, fp] + norm + [vp, ul, vp]
+    lib.gla_group_norm_act_bwd.restype = i
     lib.gla_status_string.argtypes = [i]
     lib.gla_status_string.restype = ctypes.c_char_p
     lib.gla_last_device_status.argtypes = [vp]

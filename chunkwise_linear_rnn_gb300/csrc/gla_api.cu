@@ -13,6 +13,7 @@
 
 #include "gla.h"
 #include "gla_internal.h"
+#include "gla_ptx.cuh"
 
 namespace gla {
 
@@ -232,6 +233,22 @@ bool tile_map(CUtensorMap *map, const void *ptr, bool f32, const long long (&dim
     return make_map(enc, map, ptr, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                     f32 ? 4 : 2, static_cast<int>(dims[0]), static_cast<int>(dims[1]),
                     static_cast<int>(dims[2]), box_c, box_r, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+bool head_map(CUtensorMap *map, const void *ptr, int d, int heads, int tokens, long long head_step,
+              long long token_step, int box_t) {
+    EncodeTiledFn enc = nullptr;
+    if (encode_fn(&enc) != GLA_OK) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? 2 * head_step : 16),
+                                   static_cast<cuuint64_t>(tokens > 1 ? 2 * token_step : 16)};
+    const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(box_t)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int usable_device(int *sm_count, unsigned int **status) {
@@ -529,7 +546,9 @@ const char *gla_status_string(int status) {
         case GLA_ERR_ARG: return "invalid argument (null pointer, non-positive size, misaligned pointer "
                                   "or overlapping tensors)";
         case GLA_ERR_SHAPE: return "unsupported head dimensions (dk in {64,128}, dv in {64,128,256}; "
-                                    "gla_qk_norm_rope: d and rot multiples of 8, rot <= d <= 256)";
+                                    "gla_qk_norm_rope: d and rot multiples of 8, rot <= d <= 256; "
+                                    "gla_headgate: dk and dv multiples of 8, dk <= 128, dv <= 256; "
+                                    "gla_group_norm_act: d a multiple of 8, d <= 512)";
         case GLA_ERR_DEVICE: return "no usable CUDA device (this library needs an sm_103 GB300)";
         case GLA_ERR_LAUNCH: return "a CUDA call failed while enqueuing work";
         case GLA_ERR_TIMEOUT: return "a bounded device-side wait expired";
@@ -1014,7 +1033,7 @@ int gla_last_device_status(cudaStream_t stream) {
     if (word != 0) {
         const unsigned int zero = 0;
         cudaMemcpy(dev->status, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-        return GLA_ERR_TIMEOUT;
+        return word & kStatusTimeout ? GLA_ERR_TIMEOUT : GLA_ERR_ARG;
     }
     return GLA_OK;
 }

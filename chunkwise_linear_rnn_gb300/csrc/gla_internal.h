@@ -175,8 +175,19 @@ int launch_gdn_chunk(const GdnChunkLaunch &p, cudaStream_t stream);
 bool tile_map(CUtensorMap *map, const void *ptr, bool f32, const long long (&dims)[3], int box_c,
               int box_r);
 
+// A tensor map of a bf16 tensor of [tokens][heads][d] with these strides over heads and tokens (in
+// elements, multiples of 8), for boxes of box_t tokens of 64 channels of one head, laid down with
+// the 128-byte swizzle, zeros outside.  A stride that is never stepped over may be 0.
+bool head_map(CUtensorMap *map, const void *ptr, int d, int heads, int tokens, long long head_step,
+              long long token_step, int box_t);
+
 // The current device's SM count and (when asked for) the address of its status
 // word, when it is an sm_103; returns a GLA status.
 int usable_device(int *sm_count, unsigned int **status = nullptr);
+
+// What every gla_headgate_* call asks of its pointers, sizes and strides; a GLA status.
+int headgate_check(const void *q, const void *k, const void *v, const float *log_alpha,
+                   const float *h, const void *o, int Hk, int H, int dk, int dv,
+                   const gla_headgate_layout &lay);
 
 }  // namespace gla

@@ -12,6 +12,7 @@ namespace gla {
 
 // Device status word bits (the word lives in gla_api.cu; kernels get its address).
 constexpr unsigned int kStatusTimeout = 1u;
+constexpr unsigned int kStatusSlot = 2u;   // a decode step met a slot that it refuses
 
 // A bounded wait gives up after this many nanoseconds of wall time.  Every
 // legitimate wait in these kernels completes within microseconds.

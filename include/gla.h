@@ -439,7 +439,8 @@ int gla_gdn_chunk_fwd(const void *q, const void *k, const void *v, const float *
                       const float *beta, float scale, const float *h0, void *o, float *hT, int B,
                       int H, int T, int dk, int dv, cudaStream_t stream);
 
-/* Element types of the calls that take more than one (gla_scan_*, gla_qk_norm_rope_*). */
+/* Element types of the calls that take more than one (gla_scan_*, gla_qk_norm_rope_*,
+ * gla_headgate_step, gla_group_norm_act_*). */
 enum gla_dtype { GLA_BF16 = 0, GLA_F32 = 1 };
 
 /*
@@ -563,7 +564,11 @@ int gla_scan_step(const void *x, const float *log_alpha, float *h, void *out, in
  * inputs or outputs that are not 16-byte aligned (positions and inv_freq: 8).
  * No output may overlap an input, and no output another.
  */
-enum gla_norm { GLA_NORM_RMS = 0, GLA_NORM_L2 = 1 };
+enum gla_norm {
+    GLA_NORM_RMS = 0,
+    GLA_NORM_L2 = 1,      /* gla_qk_norm_rope_* alone   */
+    GLA_NORM_LAYER = 2    /* gla_group_norm_act_* alone */
+};
 typedef struct gla_qk_layout {
     long long q_sb, q_st, q_sh;   /* strides of q over batch, token, head */
     long long k_sb, k_st, k_sh;   /* strides of k                         */
@@ -602,14 +607,140 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
                          const gla_qk_layout *layout, const gla_qk_options *options,
                          void *scratch, unsigned long scratch_bytes, cudaStream_t stream);
 
+/*
+ * gla_headgate_* — the recurrence at the top of this file with one gate for every
+ * key channel of a token and head, as it is served:
+ *     S_t = exp(log_alpha_t) S_{t-1} + k_t^T v_t,      o_t = scale * q_t S_t
+ * (the GLA page's "The Retention and Recall Degradation Problem": RetNet's fixed
+ * decay; "Structural Comparison Across Sub-Quadratic Architectures": Mamba-2's gate
+ * of every token).  Tensors are token-major, as projections leave them, and a key
+ * head may serve several value heads: value head h reads q and k of head
+ * h / (H / Hk).
+ *
+ *   q, k       : [T, Hk, dk], v : [T, H, dv], read through the strides of `layout`
+ *                (in elements; the last dimension is contiguous)
+ *   log_alpha  : [T, H] fp32, <= 0, through strides of its own; a token stride of 0
+ *                is a fixed decay for each head.  -infinity is a gate of 0 and cuts
+ *                the sequence
+ *   o          : [T, H, dv] contiguous, rounded once
+ *   states     : fp32 [., H, dk, dv], row index = key channel
+ * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256 (GLA_ERR_SHAPE
+ * otherwise); H a multiple of Hk, up to 65535.  q, k, v, o and the states 16-byte
+ * aligned, strides of q, k and v non-negative multiples of 8 elements (over the tokens
+ * of a prompt positive ones), those of log_alpha non-negative (GLA_ERR_ARG otherwise).  No output may overlap an input
+ * but hT, which may be h0 itself.
+ *
+ * gla_headgate_fwd_varlen — prompts: a packed batch of N sequences, sequence n in
+ * rows cu_seqlens[n] : cu_seqlens[n+1] (a HOST array of N + 1 ints from 0 to
+ * T_total, nondecreasing, read during the call only: a captured call keeps its
+ * lengths).  All of q, k, v and o are bf16.  h0 and hT are [N, H, dk, dv], each
+ * nullable (zero; not written); an empty sequence has hT = h0.  `scratch` holds
+ * gla_headgate_fwd_varlen_scratch(...) bytes of device memory, 16-byte aligned (NULL
+ * when that is 0), for the states at the cuts of sequences that are divided among
+ * SMs; GLA_ERR_SCRATCH when scratch_bytes is smaller.  Two calls that may run at the
+ * same time need scratch of their own.  Equal calls give equal bits.
+ * Accuracy: the states are held and summed in fp32.  With M the recurrence on |k|, |v|
+ * and |h0|, hT is within 2^-24 (264 + T / 32) M and the gates' own roundings of the exact
+ * state, o before its rounding within 2^-8 scale |q| M and as many more of 2^-24.  A sequence does not see its neighbours' values,
+ * infinite or NaN ones included; an infinite or NaN value of a token may show in the
+ * outputs of the up to 127 tokens before it, and does in the later ones.  A bounded
+ * device wait that expires leaves the outputs unspecified and is reported by
+ * gla_last_device_status (GLA_ERR_TIMEOUT).
+ */
+typedef struct gla_headgate_layout {
+    long long q_st, q_sh;   /* strides of q over token (row of a step) and head */
+    long long k_st, k_sh;
+    long long v_st, v_sh;
+    long long a_st, a_sh;   /* strides of log_alpha                             */
+} gla_headgate_layout;
+unsigned long gla_headgate_fwd_varlen_scratch(const int *cu_seqlens, int N, int H, int dk, int dv);
+int gla_headgate_fwd_varlen(const void *q, const void *k, const void *v, const float *log_alpha,
+                            float scale, const float *h0, void *o, float *hT,
+                            const int *cu_seqlens, int N, int T_total, int Hk, int H, int dk,
+                            int dv, const gla_headgate_layout *layout, void *scratch,
+                            unsigned long scratch_bytes, cudaStream_t stream);
+
+/*
+ * gla_headgate_step — one token for each of B rows, in place on states that lie in a
+ * pool: h is [S, H, dk, dv] fp32, and row b reads and overwrites entry slots[b]
+ * (int64, device; NULL: entry b, with B <= S).  q, k [B, Hk, dk], v, o [B, H, dv] in
+ * `dtype` (GLA_BF16 or GLA_F32), log_alpha [B, H] fp32, all but o through `layout`.
+ * A negative slot is a row of padding: its o is zero and no state is touched.  A slot
+ * of S or more, or one that an earlier row of the call has, is refused on the device:
+ * that row is treated as padding, and gla_last_device_status reports GLA_ERR_ARG.
+ */
+int gla_headgate_step(const void *q, const void *k, const void *v, const float *log_alpha,
+                      float scale, float *h, const long long *slots, void *o, int B, int S, int Hk,
+                      int H, int dk, int dv, const gla_headgate_layout *layout, int dtype,
+                      cudaStream_t stream);
+
+/*
+ * gla_group_norm_act_* — what follows the attention in such a layer: the norm of each
+ * head's channels (a group norm over the channels of a token, one group a head), with
+ * an activation of a gate that multiplies it, or of the norm itself:
+ *     n = (x - mean) r w + b,     y = n * f(gate)   or, without a gate,   y = f(n),
+ *     r = 1 / sqrt(mean((x - mean)^2) + eps),       f(z) = z s(z) or s(z),
+ * with s(z) = 1 / (1 + exp(-z)).  GLA_NORM_LAYER takes the mean from x,
+ * GLA_NORM_RMS leaves it (mean = 0).
+ *
+ *   x, gate      : [B, T, H, d] dtype, through the strides of `layout` (the last
+ *                  dimension is contiguous): token-major, head-first or part of a
+ *                  wider tensor; gate is nullable
+ *   weight, bias : fp32 [d], or [H, d] with options->per_channel; each nullable
+ *   y            : [B, T, H, d] dtype, contiguous: token-major, as the projection
+ *                  that follows reads it
+ *
+ * Sums are fp32, y is rounded once.  d a multiple of 8 up to 512 (GLA_ERR_SHAPE
+ * otherwise).  GLA_ERR_ARG for null required pointers, non-positive sizes, eps not in
+ * (0, 1], unknown dtype, norm, activation or per_channel, strides that are negative or
+ * not multiples of 8 elements, tensors that are not 16-byte aligned, or more than
+ * 2^31 - 1 thread blocks of work.  No output may overlap an input, and no output
+ * another.
+ */
+enum gla_activation { GLA_ACT_SILU = 0, GLA_ACT_SIGMOID = 1 };
+typedef struct gla_norm_act_layout {
+    long long x_sb, x_st, x_sh;      /* strides of x over batch, token, head */
+    long long g_sb, g_st, g_sh;      /* strides of gate                      */
+    long long dx_sb, dx_st, dx_sh;   /* strides of grad_x (backward alone)   */
+} gla_norm_act_layout;
+typedef struct gla_norm_act_options {
+    int dtype;         /* GLA_BF16 or GLA_F32               */
+    int norm;          /* GLA_NORM_RMS or GLA_NORM_LAYER    */
+    int activation;    /* GLA_ACT_SILU or GLA_ACT_SIGMOID   */
+    int per_channel;   /* weight and bias are [H, d]        */
+    float eps;
+} gla_norm_act_options;
+int gla_group_norm_act_fwd(const void *x, const void *gate, const float *weight,
+                           const float *bias, void *y, int B, int T, int H, int d,
+                           const gla_norm_act_layout *layout, const gla_norm_act_options *options,
+                           cudaStream_t stream);
+
+/*
+ * gla_group_norm_act_bwd — gradients of L = <dy, y>, the norms recomputed from x.  dy is
+ * contiguous like y; grad_x is written through its own strides of `layout` (so that it can
+ * lie as x does), grad_gate [B, T, H, d] contiguous (NULL with gate NULL); both in
+ * dtype.  grad_weight and grad_bias are fp32 like weight and bias, each nullable (not
+ * wanted).  With either, `scratch` holds gla_group_norm_act_bwd_scratch(...) bytes of
+ * device memory, 16-byte aligned, for their partial sums (GLA_ERR_SCRATCH when
+ * scratch_bytes is smaller): a thread adds at most 2^10 rows in 32 bits, everything
+ * after that is added in 64, in a fixed order, so equal calls give equal bits.  Two
+ * calls that may run at the same time need scratch of their own.
+ */
+unsigned long gla_group_norm_act_bwd_scratch(int B, int T, int H, int d);
+int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
+                           const float *bias, const void *dy, void *grad_x, void *grad_gate,
+                           float *grad_weight, float *grad_bias, int B, int T, int H, int d,
+                           const gla_norm_act_layout *layout, const gla_norm_act_options *options,
+                           void *scratch, unsigned long scratch_bytes, cudaStream_t stream);
+
 /* Static text for a status code (never NULL). */
 const char *gla_status_string(int status);
 
 /*
  * Synchronises `stream`, then reads and clears the library's device status
  * word on the current device.  Returns GLA_ERR_TIMEOUT if any kernel since
- * the last call gave up a bounded wait, GLA_ERR_LAUNCH if the stream reports
- * a CUDA error, else GLA_OK.
+ * the last call gave up a bounded wait, GLA_ERR_ARG if gla_headgate_step met a slot that
+ * it refuses, GLA_ERR_LAUNCH if the stream reports a CUDA error, else GLA_OK.
  */
 int gla_last_device_status(cudaStream_t stream);
 
