@@ -2,14 +2,48 @@
 //     S_t = a_t S_{t-1} + k_t^T v_t,     o_t = scale q_t S_t,    a_t = exp(log_alpha_t),
 // over a packed batch, token-major, with fewer key heads than value heads.
 //
-// Token by token: a thread holds one column of the state, a block 64 columns of one head of
-// one sequence; the tokens' keys and queries come through shared memory.
+// By chunks of 128 tokens on the tensor cores.  With G_t = log2(a_1 ... a_t) inside a chunk that
+// the state S enters, and n its last token,
+//     o_t = scale 2^G_t (q_t S + sum_{i <= t} (q_t . k_i) 2^-G_i v_i),
+//     S'  = 2^G_n S + sum_i k_i^T (2^(G_n - G_i) v_i).
+// One gate a token leaves q, k and v the bf16 numbers that they are: the decays go on the
+// scores, on the rows of the output and on v's rows.  A chunk whose gates fall below 2^-60 in
+// all takes its rows relative to R_t = max(G_t, -60) instead of G_t, with 2^(G_t - R_t - G_i) on
+// the scores, so that nothing overflows; the state's part of rows below is then 2^-60 of its
+// size or less where it should be less still.
+//
+// What is rounded to bf16: the scores and the copy of the state that q multiplies, once for
+// each output, as the output itself is.  The state does not lose anything by it: 2^(G_n - G_i) v_i
+// enters as the sum of three bf16 numbers, which hold all 24 bits of it, and S' is summed in
+// fp32 registers.
+//
+// One block takes 64 columns of v of one head of a sequence (or of a segment of it) and walks
+// its chunks:
+//   warps 0-3   state: thread i holds row i of S; adds the chunk's sum, writes the bf16 copy
+//   warps 4-7   scores: thread t reads row t of Q K^T, decays and masks it, leaves it in TMEM
+//   warps 8-11  values: thread t writes row t of the decayed V in three parts; then the
+//               outputs of row t
+//   warp 12     loads: lane 0 queues the next chunk's tiles by TMA; the warp sums its gates
+//   warp 13     issues every product
+// Products of chunk u, in this order, and when they may start:
+//   K^T [V'1 | V'2 | V'3]   the parts are written, the last chunk's sum is read
+//   Q S                     the copy of S is written, the last chunk's outputs are read
+//   Q K^T of chunk u + 1    its tiles are there, chunk u - 1 is done
+//   P V, onto Q S           the scores are written
+// so that every warp has the time of the other products for its part.
+//
+// Long sequences in small numbers are cut into segments: a first launch walks all but the last
+// one from a state of zero (k and v alone), and each segment then starts from the states before
+// it, S = 2^G S + S_segment.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
+#include <new>
+#include <vector>
 
 #include "gla.h"
 #include "gla_exp.cuh"
@@ -36,54 +70,571 @@ int headgate_check(const void *q, const void *k, const void *v, const float *log
 
 namespace {
 
-constexpr int kBounds = 256;     // sequences of one launch
+constexpr int C = 128;                   // tokens of a chunk
+constexpr int kCols = 64;                // columns of v of a block
+constexpr int kThreads = 448;
+constexpr int kItems = 200;              // segments of one launch: their table is a parameter
+constexpr float kFloor = -60.f;          // of R_t
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kBlk = C * 128;       // a tile of 128 rows of 64 bf16
 
-struct TokenArgs {
-    const __nv_bfloat16 *q, *k, *v;
-    const float *log_alpha, *h0;
-    __nv_bfloat16 *o;
-    float *hT;
-    gla_headgate_layout lay;
-    float scale;
-    int H, share, dk, dv, first;
-    int bounds[kBounds + 1];
+struct Smem {
+    // the loaded tiles of a chunk, twice: Q and K by blocks of 64 channels, V
+    static constexpr uint32_t kQ = 0, kK = 2 * kBlk, kV = 4 * kBlk, kStage = 5 * kBlk;
+    static constexpr uint32_t kW = 2 * kStage;            // the three parts of the decayed V
+    static constexpr uint32_t kS = kW + 3 * kBlk;         // bf16 copy of the state
+    static constexpr uint32_t kGates = kS + kBlk;         // twice
+    static constexpr uint32_t kBar = kGates + 2 * 1040;
+    static constexpr uint32_t kSlot = kBar + 256;
+    static constexpr uint32_t kBytes = kSlot + 16;
+};
+static_assert(Smem::kBytes <= 227 * 1024, "shared memory of one block");
+
+// What the gates of a chunk come to: for the scores, by token, 2^-G_i, or -G_i in a chunk that
+// falls below the floor (`deep`); the decay from each token to the chunk's end; over all of it,
+// and its logarithm.
+struct Gates {
+    float e[C], w[C];
+    float all, total;
+    int deep, pad;
+};
+static_assert(sizeof(Gates) == 1040, "room in Smem");
+
+// Barriers; those of two are taken in turn, chunk u the (u & 1)th.
+constexpr int kFull = 0;       // [2] tiles loaded
+constexpr int kDone = 2;       // [2] every product of the chunk done: tiles free, outputs there
+constexpr int kGFull = 4;      // [2] gates written
+constexpr int kGFree = 6;      // [2] gates read by all
+constexpr int kScore = 8;      // [2] Q K^T done
+constexpr int kP = 10;         // [2] scores written
+constexpr int kParts = 12;     // parts of the decayed V written
+constexpr int kSum = 13;       // the chunk's sum done, the parts free
+constexpr int kSumFree = 14;   // the sum read
+constexpr int kCopy = 15;      // copy of the state written
+constexpr int kQS = 16;        // Q S done, the copy free
+constexpr int kOFree = 17;     // outputs read
+constexpr int kDrain = 18;
+constexpr int kBars = 19;
+static_assert(kBars * 8 <= 256, "room in Smem");
+
+// A segment of a sequence.
+struct Item {
+    int row, rows;             // first token, tokens
+    int n;                     // sequence
+    int slot, seg, parts;      // scratch: the sequence's first slot; number of segment, of how many
 };
 
-constexpr int kMaxDk = 128, kCols = 64;
+struct Args {
+    CUtensorMap tq, tk, tv;
+    const float *la, *h0;
+    __nv_bfloat16 *o;
+    float *hT;
+    float *seg_state;          // [slots][H][dk][dv]
+    float *seg_log;            // [slots][H]
+    long long a_st, a_sh;
+    float scale;
+    int H, share, dk, dv, tiles;
+    int q_step, k_step, v_step;   // from head to head of the tensor maps: 1, or 0 for a shared one
+    int wide_store;            // rows of o lie at multiples of 32 bytes
+    unsigned int *status;
+    Item items[kItems];
+};
 
-__global__ void __launch_bounds__(kCols) headgate_token_kernel(const __grid_constant__ TokenArgs p) {
-    __shared__ float s_q[kMaxDk], s_k[kMaxDk];
-    const int head = blockIdx.x, n = blockIdx.z, c = blockIdx.y * kCols + threadIdx.x;
-    const int hk = head / p.share;
-    const bool mine = c < p.dv;
-    const long long state = ((static_cast<long long>(p.first + n) * p.H + head) * p.dk) * p.dv + c;
-    float S[kMaxDk];
+// TMEM columns: two buffers of scores (Q K^T in fp32, the decayed scores over it), the chunk's
+// sum in its three parts, the outputs.
+constexpr uint32_t kTScore = 0, kTSum = 256, kTOut = 448;
+
+// Four consecutive tokens' gates of a chunk of n tokens, by lane.
+__device__ __forceinline__ void load_gates(const Args &p, long long row, int n, int h, float (&g)[4]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kMaxDk; ++i)
-        S[i] = p.h0 && mine && i < p.dk ? p.h0[state + static_cast<long long>(i) * p.dv] : 0.f;
-    for (int i = threadIdx.x; i < kMaxDk; i += kCols) s_q[i] = s_k[i] = 0.f;
-    for (int t = p.bounds[n]; t < p.bounds[n + 1]; ++t) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < p.dk; i += kCols) {
-            s_q[i] = __bfloat162float(p.q[t * p.lay.q_st + hk * p.lay.q_sh + i]);
-            s_k[i] = __bfloat162float(p.k[t * p.lay.k_st + hk * p.lay.k_sh + i]);
-        }
-        const float a = exp_centred(p.log_alpha[t * p.lay.a_st + head * p.lay.a_sh]);
-        const float v = mine ? __bfloat162float(p.v[t * p.lay.v_st + head * p.lay.v_sh + c]) : 0.f;
-        __syncthreads();
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMaxDk; ++i) {
-            S[i] = fmaf(a, S[i], s_k[i] * v);
-            sum = fmaf(s_q[i], S[i], sum);
-        }
-        if (mine)
-            p.o[(static_cast<long long>(t) * p.H + head) * p.dv + c] = __float2bfloat16_rn(p.scale * sum);
+    for (int j = 0; j < 4; ++j) {
+        const int i = 4 * lane + j;
+        g[j] = i < n ? __ldg(p.la + (row + i) * p.a_st + h * p.a_sh) : 0.f;
+        // exp(-111) is 0 in 32 bits: a gate of 0 takes part in the sums as this
+        if (g[j] < -111.f) g[j] = -111.f;
     }
-    if (p.hT && mine)
+}
+
+template <bool STATE>
+__device__ __forceinline__ void write_gates(const float (&g)[4], Gates &out) {
+    const int lane = threadIdx.x & 31;
+    const float p[4] = {g[0], g[0] + g[1], g[0] + g[1] + g[2], (g[0] + g[1]) + (g[2] + g[3])};
+    // sums of the lanes before and behind, each by additions alone: small sums stay exact
+    float before = p[3], behind = p[3];
 #pragma unroll
-        for (int i = 0; i < kMaxDk; ++i)
-            if (i < p.dk) p.hT[state + static_cast<long long>(i) * p.dv] = S[i];
+    for (int o = 1; o < 32; o <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, before, o);
+        const float b = __shfl_down_sync(0xffffffffu, behind, o);
+        if (lane >= o) before += a;
+        if (lane + o < 32) behind += b;
+    }
+    const float total = __shfl_sync(0xffffffffu, before, 31);
+    before = __shfl_up_sync(0xffffffffu, before, 1);
+    behind = __shfl_down_sync(0xffffffffu, behind, 1);
+    if (lane == 0) before = 0.f;
+    if (lane == 31) behind = 0.f;
+    const bool deep = total * kLog2e < kFloor;
+    if (!STATE) {
+        float e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            e[j] = -kLog2e * (before + p[j]);
+            if (!deep) e[j] = ex2f(e[j]);
+        }
+        *reinterpret_cast<float4 *>(out.e + 4 * lane) = make_float4(e[0], e[1], e[2], e[3]);
+    }
+    *reinterpret_cast<float4 *>(out.w + 4 * lane) =
+        make_float4(exp_centred(behind + (g[1] + (g[2] + g[3]))), exp_centred(behind + (g[2] + g[3])),
+                    exp_centred(behind + g[3]), exp_centred(behind));
+    if (lane == 0) {
+        out.all = exp_centred(total);
+        out.total = total;
+        out.deep = deep;
+    }
+}
+
+// A pair of values as three pairs of bf16 numbers that add up to it.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&part)[3]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        part[i] = pack_bf16x2(x, y);
+        x -= __uint_as_float(part[i] << 16);
+        y -= __uint_as_float(part[i] & 0xffff0000u);
+    }
+}
+
+// Where 16 bytes of row `row` of a tile lie: column group c8 of 8.
+__device__ __forceinline__ uint32_t at_tile(int row, int c8) {
+    return static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(c8 ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// STATE: the first launch of divided sequences, whose segments' sums alone are wanted.
+template <bool STATE>
+__global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __grid_constant__ Args p) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Smem::kBar);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + Smem::kSlot);
+    Gates *gates = reinterpret_cast<Gates *>(sm + Smem::kGates);
+    const int tile = blockIdx.x % p.tiles, h = blockIdx.x / p.tiles % p.H;
+    const Item &it = p.items[blockIdx.x / p.tiles / p.H];
+    const int hk = h / p.share, c0 = tile * kCols, dk = p.dk;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nch = (it.rows + C - 1) / C;
+    const int kblocks = dk > 64 ? 2 : 1, ksteps = (dk + 15) / 16;
+    const uint32_t a0 = smem_u32(sm);
+    unsigned int *status = p.status;
+
+    if (warp == 0) tmem_alloc(slot, 512);
+    if (tid == 32) {
+        for (int i = 0; i < kBars; ++i) {
+            const bool by_warps = i == kP || i == kP + 1 || i == kParts || i == kSumFree ||
+                                  i == kCopy || i == kOFree;
+            const bool by_all = i == kGFree || i == kGFree + 1;
+            mbar_init(&bar[i], by_all ? (STATE ? 8 : 12) : by_warps ? 4 : 1);
+        }
+        fence_mbar_init();
+    }
+    // channels past the first block: rows of the state that stay 0
+    if (kblocks == 1)
+        for (uint32_t i = tid * 16; i < kBlk; i += kThreads * 16)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                *reinterpret_cast<uint4 *>(sm + s * Smem::kStage + Smem::kK + kBlk + i) =
+                    make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;   // the warp's lanes
+    // a warp's wait for the barrier's phase of chunk u (of two in turn, or one)
+    auto wait2 = [&](int b, int u) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(&bar[b + (u & 1)],
+                                                         static_cast<uint32_t>(u >> 1) & 1u, status));
+    };
+    auto wait1 = [&](int b, int u) {
+        return __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar[b], static_cast<uint32_t>(u) & 1u, status));
+    };
+    auto arrive = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[b]);
+    };
+
+    if (warp < 4) {
+        // ================================================================ state
+        const int i = tid;
+        float S[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) S[c] = 0.f;
+        auto state_row = [&](long long entry) {   // of [.][H][dk][dv]
+            return ((entry * p.H + h) * dk + i) * p.dv + c0;
+        };
+        auto add_row = [&](const float *from, float a) {
+            if (i >= dk) return;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 4)
+                if (c0 + c < p.dv) {
+                    const float4 x = *reinterpret_cast<const float4 *>(from + c);
+                    S[c] = fmaf(a, S[c], x.x);
+                    S[c + 1] = fmaf(a, S[c + 1], x.y);
+                    S[c + 2] = fmaf(a, S[c + 2], x.z);
+                    S[c + 3] = fmaf(a, S[c + 3], x.w);
+                }
+        };
+        auto put_row = [&](float *to) {
+            if (i >= dk) return;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 4)
+                if (c0 + c < p.dv)
+                    *reinterpret_cast<float4 *>(to + c) =
+                        make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+        };
+        auto put_copy = [&]() {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8)
+                *reinterpret_cast<uint4 *>(sm + Smem::kS + at_tile(i, c / 8)) = make_uint4(
+                    pack_bf16x2(S[c], S[c + 1]), pack_bf16x2(S[c + 2], S[c + 3]),
+                    pack_bf16x2(S[c + 4], S[c + 5]), pack_bf16x2(S[c + 6], S[c + 7]));
+            fence_proxy_async_smem();
+            arrive(kCopy);
+        };
+        if (STATE) {
+            // h0 is kept for the second launch, whose blocks may write hT over it
+            if (it.seg == 0 && p.h0) {
+                add_row(p.h0 + state_row(it.n), 0.f);
+                put_row(p.seg_state + state_row(it.slot + it.parts - 1));
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) S[c] = 0.f;
+            }
+        } else {
+            if (p.h0)
+                add_row(it.parts > 1 ? p.seg_state + state_row(it.slot + it.parts - 1)
+                                     : p.h0 + state_row(it.n), 0.f);
+            for (int m = 0; m < it.seg; ++m)
+                add_row(p.seg_state + state_row(it.slot + m),
+                        exp_centred(p.seg_log[static_cast<long long>(it.slot + m) * p.H + h]));
+            if (nch > 0) put_copy();
+        }
+        float total = 0.f;
+        bool ok = true;
+#pragma unroll 1
+        for (int u = 0; u < nch; ++u) {
+            if (!(ok = wait2(kGFull, u) && wait1(kSum, u))) break;
+            tc_fence_after();
+            const float a = gates[u & 1].all;
+            if (STATE) total += gates[u & 1].total;
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+                uint32_t x[16], y[16], z[16];
+                tmem_ld16(tmem + lanes + kTSum + c, x);
+                tmem_ld16(tmem + lanes + kTSum + kCols + c, y);
+                tmem_ld16(tmem + lanes + kTSum + 2 * kCols + c, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    S[c + j] = fmaf(a, S[c + j], __uint_as_float(x[j]) +
+                                                     (__uint_as_float(y[j]) + __uint_as_float(z[j])));
+            }
+            tc_fence_before();
+            arrive(kSumFree);
+            arrive(kGFree + (u & 1));
+            if (!STATE && u + 1 < nch) {
+                if (!(ok = wait1(kQS, u))) break;
+                put_copy();
+            }
+        }
+        if (ok) {
+            if (STATE) {
+                put_row(p.seg_state + state_row(it.slot + it.seg));
+                if (tid == 0 && tile == 0)
+                    p.seg_log[static_cast<long long>(it.slot + it.seg) * p.H + h] = total;
+            } else if (p.hT && it.seg == it.parts - 1) {
+                put_row(p.hT + state_row(it.n));
+            }
+        }
+    } else if (warp < 8) {
+        // ================================================================ scores
+        const int w = warp - 4, t = tid - 128;
+#pragma unroll 1
+        for (int u = 0; !STATE && u < nch; ++u) {
+            if (!(wait2(kGFull, u) && wait2(kScore, u))) break;
+            tc_fence_after();
+            const Gates &g = gates[u & 1];
+            const uint32_t at = tmem + lanes + kTScore + (u & 1) * C;
+            const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
+            const bool deep = g.deep;
+            const float base = deep ? -g.e[t] - fmaxf(-g.e[t], kFloor) : 0.f;
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t out[16];
+                if (b > w) {   // tokens behind all of this warp's
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) out[j] = 0u;
+                } else {
+                    uint32_t r[32];
+                    tmem_ld32(at + 32 * b, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 e = e4[(32 * b + j) / 4];
+                        float f[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (deep) f[k] = ex2f(base + f[k]);
+                            f[k] = 32 * b + j + k <= t ? __uint_as_float(r[j + k]) * f[k] : 0.f;
+                        }
+                        out[j / 2] = pack_bf16x2(f[0], f[1]);
+                        out[j / 2 + 1] = pack_bf16x2(f[2], f[3]);
+                    }
+                }
+                tmem_st16(at + 16 * b, out);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(kP + (u & 1));
+            arrive(kGFree + (u & 1));
+        }
+    } else if (warp < 12) {
+        // ================================================================ values, outputs
+        const int t = tid - 256;
+        auto parts = [&](int u) {
+            if (!(wait2(kFull, u) && wait2(kGFull, u) && (u == 0 || wait1(kSum, u - 1)))) return false;
+            uint8_t *st = sm + (u & 1) * Smem::kStage;
+            const float f = gates[u & 1].w[t];
+            const bool real = u * C + t < it.rows;
+#pragma unroll
+            for (int c = 0; c < kCols / 8; ++c) {
+                const uint32_t o = at_tile(t, c);
+                uint4 hi = make_uint4(0, 0, 0, 0), mid = hi, lo = hi;
+                if (real) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(st + Smem::kV + o);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t part[4][3];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        split3(f * __uint_as_float(in[j] << 16),
+                               f * __uint_as_float(in[j] & 0xffff0000u), part[j]);
+                    hi = make_uint4(part[0][0], part[1][0], part[2][0], part[3][0]);
+                    mid = make_uint4(part[0][1], part[1][1], part[2][1], part[3][1]);
+                    lo = make_uint4(part[0][2], part[1][2], part[2][2], part[3][2]);
+                } else {
+                    // the next sequence's rows, which may hold anything: no part of any product
+                    *reinterpret_cast<uint4 *>(st + Smem::kV + o) = hi;
+                    *reinterpret_cast<uint4 *>(st + Smem::kK + o) = hi;
+                    if (kblocks == 2) *reinterpret_cast<uint4 *>(st + Smem::kK + kBlk + o) = hi;
+                }
+                *reinterpret_cast<uint4 *>(sm + Smem::kW + o) = hi;
+                *reinterpret_cast<uint4 *>(sm + Smem::kW + kBlk + o) = mid;
+                *reinterpret_cast<uint4 *>(sm + Smem::kW + 2 * kBlk + o) = lo;
+            }
+            fence_proxy_async_smem();
+            arrive(kParts);
+            if (STATE) arrive(kGFree + (u & 1));
+            return true;
+        };
+        bool ok = nch > 0 && parts(0);
+#pragma unroll 1
+        for (int u = 0; ok && u < nch; ++u) {
+            if (u + 1 < nch && !(ok = parts(u + 1))) break;
+            if (STATE) continue;
+            if (!wait2(kDone, u)) break;
+            tc_fence_after();
+            const float e = gates[u & 1].e[t];
+            const float f = p.scale * (gates[u & 1].deep ? ex2f(fmaxf(-e, kFloor)) : 1.f / e);
+            uint32_t r[2][32];
+            tmem_ld32(tmem + lanes + kTOut, r[0]);
+            tmem_ld32(tmem + lanes + kTOut + 32, r[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(kOFree);
+            arrive(kGFree + (u & 1));
+            if (u * C + t < it.rows) {
+                __nv_bfloat16 *to =
+                    p.o + (static_cast<long long>(it.row + u * C + t) * p.H + h) * p.dv + c0;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = pack_bf16x2(f * __uint_as_float(r[c / 32][c % 32 + 2 * j]),
+                                           f * __uint_as_float(r[c / 32][c % 32 + 2 * j + 1]));
+                    if (p.wide_store) {
+                        if (c0 + c < p.dv) store32(to + c, v);
+                    } else {
+                        if (c0 + c < p.dv)
+                            *reinterpret_cast<uint4 *>(to + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if (c0 + c + 8 < p.dv)
+                            *reinterpret_cast<uint4 *>(to + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+        }
+    } else if (warp == 12) {
+        // ================================================================ loads and gates
+        int loads = 0;
+        auto load = [&](int u) {   // lane 0
+            uint8_t *st = sm + (u & 1) * Smem::kStage;
+            uint64_t *full = &bar[kFull + (u & 1)];
+            const int t0 = it.row + u * C;
+            mbar_arrive_expect_tx(full, (kblocks * (STATE ? 1 : 2) + 1) * kBlk);
+            for (int b = 0; b < kblocks; ++b) {
+                if (!STATE) tma_load_3d(st + Smem::kQ + b * kBlk, &p.tq, full, b * 64, hk * p.q_step, t0);
+                tma_load_3d(st + Smem::kK + b * kBlk, &p.tk, full, b * 64, hk * p.k_step, t0);
+            }
+            tma_load_3d(st + Smem::kV, &p.tv, full, c0, h * p.v_step, t0);
+            loads = u + 1;
+        };
+        float g[4];
+        if (lane == 0)
+            for (int u = 0; u < 2 && u < nch; ++u) load(u);
+#pragma unroll 1
+        for (int u = 0; u < 2 && u < nch; ++u) {
+            load_gates(p, it.row + u * C, min(C, it.rows - u * C), h, g);
+            write_gates<STATE>(g, gates[u]);
+            arrive(kGFull + u);
+        }
+#pragma unroll 1
+        for (int u = 2; u < nch; ++u) {
+            load_gates(p, it.row + u * C, min(C, it.rows - u * C), h, g);
+            if (!wait2(kDone, u - 2)) break;
+            if (lane == 0) load(u);
+            __syncwarp();
+            if (!wait2(kGFree, u - 2)) break;
+            write_gates<STATE>(g, gates[u & 1]);
+            arrive(kGFull + (u & 1));
+        }
+        // loads that an expired wait left under way land before the block gives up its memory
+        if (lane == 0)
+            for (int u = max(0, loads - 2); u < loads; ++u)
+                mbar_wait_bounded(&bar[kFull + (u & 1)], static_cast<uint32_t>(u >> 1) & 1u, status);
+    } else if (lane == 0) {
+        // ================================================================ products
+        auto until2 = [&](int b, int u) {
+            return mbar_wait_bounded(&bar[b + (u & 1)], static_cast<uint32_t>(u >> 1) & 1u, status);
+        };
+        auto until1 = [&](int b, int u) {
+            return mbar_wait_bounded(&bar[b], static_cast<uint32_t>(u) & 1u, status);
+        };
+        auto scores = [&](int u) {
+            constexpr uint32_t id = idesc_bf16(C, C, false, false);   // Q [t][c], K [i][c]
+            const uint32_t st = a0 + (u & 1) * Smem::kStage;
+            tc_fence_after();
+            for (int k = 0; k < ksteps; ++k) {
+                const uint32_t o = (k >> 2) * kBlk + (k & 3) * 32;
+                mma_bf16_ss(tmem + kTScore + (u & 1) * C, sw128_desc(st + Smem::kQ + o, 16, 1024),
+                            sw128_desc(st + Smem::kK + o, 16, 1024), id, k > 0);
+            }
+            mma_commit(&bar[kScore + (u & 1)]);
+        };
+        if (!STATE && nch > 0 && until2(kFull, 0)) scores(0);
+#pragma unroll 1
+        for (int u = 0; u < nch; ++u) {
+            const uint32_t st = a0 + (u & 1) * Smem::kStage;
+            if (!(until2(kFull, u) && until1(kParts, u) && (u == 0 || until1(kSumFree, u - 1)))) break;
+            tc_fence_after();
+            // K^T [c][t] by the parts [t][3 x 64]
+            constexpr uint32_t id_sum = idesc_bf16(128, 3 * kCols, true, true);
+#pragma unroll
+            for (int k = 0; k < C / 16; ++k)
+                mma_bf16_ss(tmem + kTSum, sw128_desc(st + Smem::kK + k * 2048, kBlk, 1024),
+                            sw128_desc(a0 + Smem::kW + k * 2048, kBlk, 1024), id_sum, k > 0);
+            mma_commit(&bar[kSum]);
+            if (STATE) {
+                mma_commit(&bar[kDone + (u & 1)]);
+                continue;
+            }
+            if (!(until1(kCopy, u) && (u == 0 || until1(kOFree, u - 1)))) break;
+            tc_fence_after();
+            // Q [t][c] by S [c][64]
+            constexpr uint32_t id_out = idesc_bf16(C, kCols, false, true);
+            for (int k = 0; k < ksteps; ++k)
+                mma_bf16_ss(tmem + kTOut,
+                            sw128_desc(st + Smem::kQ + (k >> 2) * kBlk + (k & 3) * 32, 16, 1024),
+                            sw128_desc(a0 + Smem::kS + k * 2048, kBlk, 1024), id_out, k > 0);
+            mma_commit(&bar[kQS]);
+            if (u + 1 < nch) {
+                // the scores of chunk u - 1 lay where these go
+                if (!(until2(kFull, u + 1) && (u == 0 || until2(kDone, u - 1)))) break;
+                scores(u + 1);
+            }
+            if (!until2(kP, u)) break;
+            tc_fence_after();
+            // P [t][i] by V [i][64], onto Q S
+#pragma unroll
+            for (int k = 0; k < C / 16; ++k)
+                mma_bf16_ts(tmem + kTOut, tmem + kTScore + (u & 1) * C + k * 8,
+                            sw128_desc(st + Smem::kV + k * 2048, kBlk, 1024), id_out, 1u);
+            mma_commit(&bar[kDone + (u & 1)]);
+        }
+        // every product ends before TMEM and shared memory are given up
+        mma_commit(&bar[kDrain]);
+        mbar_wait_bounded(&bar[kDrain], 0, status);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- the plan
+
+// How the sequences are cut: chunks of a segment, at most (INT_MAX: none is cut), and slots of
+// scratch.
+struct Plan {
+    int most;
+    long long slots;
+};
+
+int chunks_of(const int *cu, int n) { return (cu[n + 1] - cu[n] + C - 1) / C; }
+int parts_of(int chunks, int most) { return chunks > most ? (chunks + most - 1) / most : 1; }
+
+// The blocks of all heads and column tiles run in rounds on the SMs; a launch takes at least its
+// longest segment, and at least its share of all chunks.  Cutting costs a launch that walks all
+// but the last segments for their sums (kSumCost of a chunk's whole work each) and what it takes
+// to begin.  Of one cut and of 2 to 32 parts for the longest sequence, the one that this says
+// is the quickest.
+Plan make_plan(const int *cu, int N, int H, int dv) {
+    constexpr double kSms = 152, kSumCost = 0.5, kBegin = 4;
+    const double lanes = static_cast<double>(H) * ((dv + kCols - 1) / kCols) / kSms;
+    int longest = 0;
+    long long all = 0;
+    for (int n = 0; n < N; ++n) {
+        longest = std::max(longest, chunks_of(cu, n));
+        all += chunks_of(cu, n);
+    }
+    Plan best = {INT_MAX, 0};
+    double least = std::max<double>(longest, all * lanes);
+    for (int k = 2; k <= 32 && k <= longest; ++k) {
+        const int most = (longest + k - 1) / k;
+        const double whole = std::max<double>(most, all * lanes);
+        if (whole + kBegin >= least) continue;   // not even with the first launch for nothing
+        long long first = 0, slots = 0;
+        for (int n = 0; n < N; ++n) {
+            const int c = chunks_of(cu, n), parts = parts_of(c, most);
+            if (parts == 1) continue;
+            first += c - c / parts;
+            slots += parts;
+        }
+        const double cost = whole + kBegin + kSumCost * std::max<double>(most, first * lanes);
+        if (cost < least) {
+            least = cost;
+            best = {most, slots};
+        }
+    }
+    return best;
+}
+
+size_t scratch_of(const Plan &plan, int H, int dk, int dv) {
+    return static_cast<size_t>(plan.slots) * H * (static_cast<size_t>(dk) * dv + 4) * sizeof(float);
 }
 
 bool bounds_ok(const int *cu, int N, int T) {
@@ -93,49 +644,124 @@ bool bounds_ok(const int *cu, int N, int T) {
     return true;
 }
 
+template <bool STATE>
+bool prepared() {
+    // the attribute belongs to the device's copy of the function
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(headgate_chunk_kernel<STATE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(Smem::kBytes)) != cudaSuccess)
+        return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
+}
+
+template <bool STATE>
+bool launch(Args &a, const std::vector<Item> &items, cudaStream_t stream) {
+    if (items.empty()) return true;
+    if (!prepared<STATE>()) return false;
+    for (size_t first = 0; first < items.size(); first += kItems) {
+        const size_t n = std::min<size_t>(kItems, items.size() - first);
+        std::copy(items.begin() + first, items.begin() + first + n, a.items);
+        const unsigned grid = static_cast<unsigned>(n) * a.H * a.tiles;
+        headgate_chunk_kernel<STATE><<<grid, kThreads, Smem::kBytes, stream>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return false;
+    }
+    return true;
+}
+
+int run(Args &a, const int *cu, int N, const Plan &plan, cudaStream_t stream) {
+    std::vector<Item> whole, sums;
+    int slot = 0;
+    for (int n = 0; n < N; ++n) {
+        const int chunks = chunks_of(cu, n), parts = parts_of(chunks, plan.most);
+        for (int s = 0, c = 0; s < parts; ++s) {
+            const int next = static_cast<int>(static_cast<long long>(chunks) * (s + 1) / parts);
+            const int row = cu[n] + c * C, end = s + 1 < parts ? cu[n] + next * C : cu[n + 1];
+            const Item it = {row, end - row, n, parts > 1 ? slot : -1, s, parts};
+            whole.push_back(it);
+            if (s + 1 < parts) sums.push_back(it);
+            c = next;
+        }
+        if (parts > 1) slot += parts;
+    }
+    // the longest first, so that the last round is short
+    auto longer = [](const Item &x, const Item &y) { return x.rows > y.rows; };
+    std::stable_sort(whole.begin(), whole.end(), longer);
+    std::stable_sort(sums.begin(), sums.end(), longer);
+    return launch<true>(a, sums, stream) && launch<false>(a, whole, stream) ? GLA_OK : GLA_ERR_LAUNCH;
+}
+
 }  // namespace
 }  // namespace gla
 
 extern "C" {
 
-unsigned long gla_headgate_fwd_varlen_scratch(const int *, int, int, int, int) { return 0; }
+unsigned long gla_headgate_fwd_varlen_scratch(const int *cu_seqlens, int N, int H, int dk, int dv) {
+    using namespace gla;
+    if (N <= 0 || H <= 0 || dk <= 0 || dv <= 0 || !cu_seqlens ||
+        !bounds_ok(cu_seqlens, N, cu_seqlens[N]))
+        return 0;
+    return scratch_of(make_plan(cu_seqlens, N, H, dv), H, dk, dv);
+}
 
 int gla_headgate_fwd_varlen(const void *q, const void *k, const void *v, const float *log_alpha,
                             float scale, const float *h0, void *o, float *hT,
                             const int *cu_seqlens, int N, int T_total, int Hk, int H, int dk,
-                            int dv, const gla_headgate_layout *layout, void *, unsigned long,
-                            cudaStream_t stream) {
+                            int dv, const gla_headgate_layout *layout, void *scratch,
+                            unsigned long scratch_bytes, cudaStream_t stream) {
     using namespace gla;
     if (!layout || !bounds_ok(cu_seqlens, N, T_total)) return GLA_ERR_ARG;
     if (T_total > 0 && (!q || !k || !v || !log_alpha || !o)) return GLA_ERR_ARG;
-    if ((reinterpret_cast<uintptr_t>(h0) | reinterpret_cast<uintptr_t>(hT)) & 15) return GLA_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(h0) | reinterpret_cast<uintptr_t>(hT) |
+         reinterpret_cast<uintptr_t>(scratch)) & 15)
+        return GLA_ERR_ARG;
     int st = headgate_check(q, k, v, log_alpha, nullptr, o, Hk, H, dk, dv, *layout);
     if (st != GLA_OK) return st;
     if (T_total > 1 && (!layout->q_st || !layout->k_st || !layout->v_st)) return GLA_ERR_ARG;
+    // a chunk's last row is counted on past the last token in 32 bits
+    if (T_total > INT_MAX - C) return GLA_ERR_ARG;
+    const Plan plan = make_plan(cu_seqlens, N, H, dv);
+    if (plan.slots > INT_MAX) return GLA_ERR_ARG;
+    const size_t need = scratch_of(plan, H, dk, dv);
+    if (need > 0 && (!scratch || scratch_bytes < need)) return GLA_ERR_SCRATCH;
     int sms = 0;
-    st = usable_device(&sms);
+    Args a = {};
+    st = usable_device(&sms, &a.status);
     if (st != GLA_OK) return st;
-    TokenArgs a = {};
-    a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.k = static_cast<const __nv_bfloat16 *>(k);
-    a.v = static_cast<const __nv_bfloat16 *>(v);
-    a.log_alpha = log_alpha;
+    a.la = log_alpha;
     a.h0 = h0;
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.hT = hT;
-    a.lay = *layout;
+    a.seg_state = static_cast<float *>(scratch);
+    a.seg_log = a.seg_state + static_cast<size_t>(plan.slots) * H * dk * dv;
+    a.a_st = layout->a_st;
+    a.a_sh = layout->a_sh;
     a.scale = scale;
     a.H = H;
     a.share = H / Hk;
     a.dk = dk;
     a.dv = dv;
-    for (a.first = 0; a.first < N; a.first += kBounds) {
-        const int n = std::min(kBounds, N - a.first);
-        std::copy(cu_seqlens + a.first, cu_seqlens + a.first + n + 1, a.bounds);
-        headgate_token_kernel<<<dim3(H, (dv + kCols - 1) / kCols, n), kCols, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return GLA_ERR_LAUNCH;
+    a.tiles = (dv + kCols - 1) / kCols;
+    a.wide_store = dv % 16 == 0 && (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    if (T_total > 0) {
+        const gla_headgate_layout &l = *layout;
+        a.q_step = Hk > 1 && l.q_sh;
+        a.k_step = Hk > 1 && l.k_sh;
+        a.v_step = H > 1 && l.v_sh;
+        if (!head_map(&a.tq, q, dk, a.q_step ? Hk : 1, T_total, l.q_sh, l.q_st, C) ||
+            !head_map(&a.tk, k, dk, a.k_step ? Hk : 1, T_total, l.k_sh, l.k_st, C) ||
+            !head_map(&a.tv, v, dv, a.v_step ? H : 1, T_total, l.v_sh, l.v_st, C))
+            return GLA_ERR_LAUNCH;
     }
-    return GLA_OK;
+    try {
+        return run(a, cu_seqlens, N, plan, stream);
+    } catch (const std::bad_alloc &) {
+        return GLA_ERR_ALLOC;
+    }
 }
 
 }  // extern "C"

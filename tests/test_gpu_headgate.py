@@ -122,9 +122,12 @@ def test_gates_of_zero_cut_the_sequence():
     la[:, :] = -0.01
     la[200] = -float("inf")
     o, hT = gla.gla_headgate_fwd_varlen(q, k, v, la, [0, 400], 1.0)
-    o2, hT2 = gla.gla_headgate_fwd_varlen(q[200:], k[200:], v[200:], la[200:], [0, 200], 1.0)
-    assert torch.allclose(hT, hT2, rtol=1e-4, atol=1e-4)
-    assert torch.allclose(o[200:].float(), o2.float(), rtol=2e-2, atol=2e-1)
+    # (a gate of 0 leaves nothing of what was before: the bounds are those of the rows behind it,
+    # o's of up to 2^-8 A for a rounding to 16 bits of every score, A some 30 times o here)
+    want = ref.walk(*(ref.num(t[200:]) for t in (q, k, v, la)), 1.0)
+    bo, bh = ref.prompt_bounds(400, *want[2:])
+    ref.assert_within(o[200:], want[0], bo, "o behind a cut")
+    ref.assert_within(hT[0], want[1], bh, "hT behind a cut")
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
