@@ -19,17 +19,18 @@
 //
 // One block takes 64 columns of v of one head of a sequence (or of a segment of it) and walks
 // its chunks:
-//   warps 0-3   state: thread i holds row i of S; adds the chunk's sum, writes the bf16 copy
+//   warps 0-3   state: thread i holds row i of S; adds the chunk's sum, writes the bf16 copy; then
+//               the outputs of row i of the chunk
 //   warps 4-7   scores: thread t reads row t of Q K^T, decays and masks it, leaves it in TMEM
-//   warps 8-11  values: thread t writes row t of the decayed V in three parts; then the
-//               outputs of row t
-//   warp 12     loads: lane 0 queues the next chunk's tiles by TMA; the warp sums its gates
-//   warp 13     issues every product
+//   warps 8-11  values: thread t writes row t of the decayed V in three parts
+//   warp 12     queues the next tiles by TMA
+//   warp 13     sums the chunk's gates
+//   warp 14     issues every product
 // Products of chunk u, in this order, and when they may start:
 //   K^T [V'1 | V'2 | V'3]   the parts are written, the last chunk's sum is read
 //   Q S                     the copy of S is written, the last chunk's outputs are read
-//   Q K^T of chunk u + 1    its tiles are there, chunk u - 1 is done
 //   P V, onto Q S           the scores are written
+//   Q K^T of chunk u + 1    its tiles are there, chunk u - 1 is done
 // so that every warp has the time of the other products for its part.
 //
 // Long sequences in small numbers are cut into segments: a first launch walks all but the last
@@ -72,7 +73,7 @@ namespace {
 
 constexpr int C = 128;                   // tokens of a chunk
 constexpr int kCols = 64;                // columns of v of a block
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kItems = 200;              // segments of one launch: their table is a parameter
 constexpr float kFloor = -60.f;          // of R_t
 constexpr float kLog2e = 1.4426950408889634f;
@@ -101,20 +102,21 @@ struct Gates {
 static_assert(sizeof(Gates) == 1040, "room in Smem");
 
 // Barriers; those of two are taken in turn, chunk u the (u & 1)th.
-constexpr int kFull = 0;       // [2] tiles loaded
-constexpr int kDone = 2;       // [2] every product of the chunk done: tiles free, outputs there
-constexpr int kGFull = 4;      // [2] gates written
-constexpr int kGFree = 6;      // [2] gates read by all
-constexpr int kScore = 8;      // [2] Q K^T done
-constexpr int kP = 10;         // [2] scores written
-constexpr int kParts = 12;     // parts of the decayed V written
-constexpr int kSum = 13;       // the chunk's sum done, the parts free
-constexpr int kSumFree = 14;   // the sum read
-constexpr int kCopy = 15;      // copy of the state written
-constexpr int kQS = 16;        // Q S done, the copy free
-constexpr int kOFree = 17;     // outputs read
-constexpr int kDrain = 18;
-constexpr int kBars = 19;
+constexpr int kFull = 0;       // [2] Q and K loaded
+constexpr int kFullV = 2;      // [2] V loaded
+constexpr int kDone = 4;       // [2] every product of the chunk done: V free, outputs there
+constexpr int kGFull = 6;      // [2] gates written
+constexpr int kGFree = 8;      // [2] gates read by all
+constexpr int kScore = 10;     // [2] Q K^T done
+constexpr int kP = 12;         // [2] scores written
+constexpr int kParts = 14;     // parts of the decayed V written
+constexpr int kSum = 15;       // the chunk's sum done: K and the parts free
+constexpr int kSumFree = 16;   // the sum read
+constexpr int kCopy = 17;      // copy of the state written
+constexpr int kQS = 18;        // Q S done: Q and the copy free
+constexpr int kOFree = 19;     // outputs read
+constexpr int kDrain = 20;
+constexpr int kBars = 21;
 static_assert(kBars * 8 <= 256, "room in Smem");
 
 // A segment of a sequence.
@@ -151,14 +153,16 @@ __device__ __forceinline__ void load_gates(const Args &p, long long row, int n, 
     for (int j = 0; j < 4; ++j) {
         const int i = 4 * lane + j;
         g[j] = i < n ? __ldg(p.la + (row + i) * p.a_st + h * p.a_sh) : 0.f;
-        // exp(-111) is 0 in 32 bits: a gate of 0 takes part in the sums as this
-        if (g[j] < -111.f) g[j] = -111.f;
     }
 }
 
 template <bool STATE>
-__device__ __forceinline__ void write_gates(const float (&g)[4], Gates &out) {
+__device__ __forceinline__ void write_gates(float (&g)[4], Gates &out) {
     const int lane = threadIdx.x & 31;
+    // exp(-111) is 0 in 32 bits: a gate of 0 takes part in the sums as this
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (g[j] < -111.f) g[j] = -111.f;
     const float p[4] = {g[0], g[0] + g[1], g[0] + g[1] + g[2], (g[0] + g[1]) + (g[2] + g[3])};
     // sums of the lanes before and behind, each by additions alone: small sums stay exact
     float before = p[3], behind = p[3];
@@ -194,13 +198,49 @@ __device__ __forceinline__ void write_gates(const float (&g)[4], Gates &out) {
     }
 }
 
+// Two fp32 values, for operations on both in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(uint32_t a, uint32_t b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+    return pair_of(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ float2 both(Pair r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t narrow(Pair p) {
+    const float2 v = both(p);
+    return pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ Pair widen(uint32_t w) { return pair_of(w << 16, w & 0xffff0000u); }
+
 // A pair of values as three pairs of bf16 numbers that add up to it.
-__device__ __forceinline__ void split3(float x, float y, uint32_t (&part)[3]) {
+__device__ __forceinline__ void split3(Pair x, uint32_t (&part)[3]) {
+    const Pair minus = pair_of(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        part[i] = pack_bf16x2(x, y);
-        x -= __uint_as_float(part[i] << 16);
-        y -= __uint_as_float(part[i] & 0xffff0000u);
+        part[i] = narrow(x);
+        if (i < 2) x = fma2(widen(part[i]), minus, x);
     }
 }
 
@@ -225,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     const int tile = blockIdx.x % p.tiles, h = blockIdx.x / p.tiles % p.H;
     const Item &it = p.items[blockIdx.x / p.tiles / p.H];
     const int hk = h / p.share, c0 = tile * kCols, dk = p.dk;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in a warp, to the compiler too
     const int nch = (it.rows + C - 1) / C;
     const int kblocks = dk > 64 ? 2 : 1, ksteps = (dk + 15) / 16;
     const uint32_t a0 = smem_u32(sm);
@@ -252,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;   // the warp's lanes
     // a warp's wait for the barrier's phase of chunk u (of two in turn, or one)
     auto wait2 = [&](int b, int u) {
@@ -271,38 +312,41 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     if (warp < 4) {
         // ================================================================ state
         const int i = tid;
-        float S[kCols];
+        Pair S[kCols / 2];
+        auto clear = [&]() {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) S[c] = 0.f;
+            for (int c = 0; c < kCols / 2; ++c) S[c] = 0;
+        };
+        clear();
         auto state_row = [&](long long entry) {   // of [.][H][dk][dv]
             return ((entry * p.H + h) * dk + i) * p.dv + c0;
         };
         auto add_row = [&](const float *from, float a) {
             if (i >= dk) return;
+            const Pair aa = pair_of(a, a);
 #pragma unroll
             for (int c = 0; c < kCols; c += 4)
                 if (c0 + c < p.dv) {
                     const float4 x = *reinterpret_cast<const float4 *>(from + c);
-                    S[c] = fmaf(a, S[c], x.x);
-                    S[c + 1] = fmaf(a, S[c + 1], x.y);
-                    S[c + 2] = fmaf(a, S[c + 2], x.z);
-                    S[c + 3] = fmaf(a, S[c + 3], x.w);
+                    S[c / 2] = fma2(aa, S[c / 2], pair_of(x.x, x.y));
+                    S[c / 2 + 1] = fma2(aa, S[c / 2 + 1], pair_of(x.z, x.w));
                 }
         };
         auto put_row = [&](float *to) {
             if (i >= dk) return;
 #pragma unroll
             for (int c = 0; c < kCols; c += 4)
-                if (c0 + c < p.dv)
-                    *reinterpret_cast<float4 *>(to + c) =
-                        make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+                if (c0 + c < p.dv) {
+                    const float2 x = both(S[c / 2]), y = both(S[c / 2 + 1]);
+                    *reinterpret_cast<float4 *>(to + c) = make_float4(x.x, x.y, y.x, y.y);
+                }
         };
         auto put_copy = [&]() {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8)
-                *reinterpret_cast<uint4 *>(sm + Smem::kS + at_tile(i, c / 8)) = make_uint4(
-                    pack_bf16x2(S[c], S[c + 1]), pack_bf16x2(S[c + 2], S[c + 3]),
-                    pack_bf16x2(S[c + 4], S[c + 5]), pack_bf16x2(S[c + 6], S[c + 7]));
+            for (int c = 0; c < kCols / 8; ++c)
+                *reinterpret_cast<uint4 *>(sm + Smem::kS + at_tile(i, c)) =
+                    make_uint4(narrow(S[4 * c]), narrow(S[4 * c + 1]), narrow(S[4 * c + 2]),
+                               narrow(S[4 * c + 3]));
             fence_proxy_async_smem();
             arrive(kCopy);
         };
@@ -311,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             if (it.seg == 0 && p.h0) {
                 add_row(p.h0 + state_row(it.n), 0.f);
                 put_row(p.seg_state + state_row(it.slot + it.parts - 1));
-#pragma unroll
-                for (int c = 0; c < kCols; ++c) S[c] = 0.f;
+                clear();
             }
         } else {
             if (p.h0)
@@ -327,28 +370,72 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
         bool ok = true;
 #pragma unroll 1
         for (int u = 0; u < nch; ++u) {
-            if (!(ok = wait2(kGFull, u) && wait1(kSum, u))) break;
+            if (!(ok = wait2(kGFull, u))) break;
+            const Gates &g = gates[u & 1];
+            const Pair a = pair_of(g.all, g.all);
+            const float f =
+                STATE ? 0.f : p.scale * (g.deep ? ex2f(fmaxf(-g.e[i], kFloor)) : 1.f / g.e[i]);
+            const Pair ff = pair_of(f, f);
+            if (STATE) total += g.total;
+            arrive(kGFree + (u & 1));
+            if (!(ok = wait1(kSum, u))) break;
             tc_fence_after();
-            const float a = gates[u & 1].all;
-            if (STATE) total += gates[u & 1].total;
+            // the next 8 columns are on their way while these are added
+            uint32_t x[2][3][8];
+            auto fetch = [&](int c) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-                uint32_t x[16], y[16], z[16];
-                tmem_ld16(tmem + lanes + kTSum + c, x);
-                tmem_ld16(tmem + lanes + kTSum + kCols + c, y);
-                tmem_ld16(tmem + lanes + kTSum + 2 * kCols + c, z);
+                for (int i = 0; i < 3; ++i)
+                    tmem_ld8(tmem + lanes + kTSum + i * kCols + c, x[c / 8 & 1][i]);
+            };
+            fetch(0);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8) {
                 tmem_wait_ld();
+                if (c + 8 < kCols) fetch(c + 8);
+                const uint32_t(&now)[3][8] = x[c / 8 & 1];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    S[c + j] = fmaf(a, S[c + j], __uint_as_float(x[j]) +
-                                                     (__uint_as_float(y[j]) + __uint_as_float(z[j])));
+                for (int j = 0; j < 8; j += 2)
+                    S[(c + j) / 2] = fma2(a, S[(c + j) / 2],
+                                          add2(pair_of(now[0][j], now[0][j + 1]),
+                                               add2(pair_of(now[1][j], now[1][j + 1]),
+                                                    pair_of(now[2][j], now[2][j + 1]))));
             }
             tc_fence_before();
             arrive(kSumFree);
-            arrive(kGFree + (u & 1));
-            if (!STATE && u + 1 < nch) {
+            if (STATE) continue;
+            if (u + 1 < nch) {
                 if (!(ok = wait1(kQS, u))) break;
                 put_copy();
+            }
+            // the outputs of row t = i
+            const int left = u * C + i < it.rows ? p.dv - c0 : 0;
+            __nv_bfloat16 *to =
+                p.o + (static_cast<long long>(it.row + u * C + i) * p.H + h) * p.dv + c0;
+            if (!(ok = wait2(kDone, u))) break;
+            tc_fence_after();
+            uint32_t r[2][16];
+            tmem_ld16(tmem + lanes + kTOut, r[0]);
+#pragma unroll
+            for (int c = 0; c < kCols; c += 16) {
+                tmem_wait_ld();
+                if (c + 16 < kCols) {
+                    tmem_ld16(tmem + lanes + kTOut + c + 16, r[c / 16 + 1 & 1]);
+                } else {
+                    tc_fence_before();
+                    arrive(kOFree);
+                }
+                uint32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[j] = narrow(mul2(ff, pair_of(r[c / 16 & 1][2 * j], r[c / 16 & 1][2 * j + 1])));
+                if (p.wide_store) {
+                    if (c < left) store32(to + c, v);
+                } else {
+                    if (c < left)
+                        *reinterpret_cast<uint4 *>(to + c) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (c + 8 < left)
+                        *reinterpret_cast<uint4 *>(to + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                }
             }
         }
         if (ok) {
@@ -372,211 +459,214 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
             const bool deep = g.deep;
             const float base = deep ? -g.e[t] - fmaxf(-g.e[t], kFloor) : 0.f;
+            uint32_t out[16];
+            // the tokens of warps before this one's, then its own, then those behind
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t out[16];
-                if (b > w) {   // tokens behind all of this warp's
+            for (int b = 0; b <= w; ++b) {
+                uint32_t r[32];
+                float4 e[8];
+                tmem_ld32(at + 32 * b, r);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = 0u;
-                } else {
-                    uint32_t r[32];
-                    tmem_ld32(at + 32 * b, r);
-                    tmem_wait_ld();
+                for (int j = 0; j < 8; ++j) e[j] = e4[8 * b + j];
+                tmem_wait_ld();
+                if (b == w) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j > lane) r[j] = 0u;
+                }
+                if (!deep) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 e = e4[(32 * b + j) / 4];
-                        float f[4] = {e.x, e.y, e.z, e.w};
+                        const float4 f = e[j / 4];
+                        out[j / 2] = narrow(mul2(pair_of(r[j], r[j + 1]), pair_of(f.x, f.y)));
+                        out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(f.z, f.w)));
+                    }
+                } else {
+                    // 2^(base - G_i) of a later token may be infinite: a masked score stays 0
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (deep) f[k] = ex2f(base + f[k]);
-                            f[k] = 32 * b + j + k <= t ? __uint_as_float(r[j + k]) * f[k] : 0.f;
-                        }
-                        out[j / 2] = pack_bf16x2(f[0], f[1]);
-                        out[j / 2 + 1] = pack_bf16x2(f[2], f[3]);
+                    for (int j = 0; j < 32; j += 2) {
+                        const float f0 = j % 4 ? e[j / 4].z : e[j / 4].x;
+                        const float f1 = j % 4 ? e[j / 4].w : e[j / 4].y;
+                        const int i = 32 * b + j;
+                        out[j / 2] = pack_bf16x2(
+                            i <= t ? __uint_as_float(r[j]) * ex2f(base + f0) : 0.f,
+                            i + 1 <= t ? __uint_as_float(r[j + 1]) * ex2f(base + f1) : 0.f);
                     }
                 }
                 tmem_st16(at + 16 * b, out);
             }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) out[j] = 0u;
+#pragma unroll 1
+            for (int b = w + 1; b < 4; ++b) tmem_st16(at + 16 * b, out);
             tmem_wait_st();
             tc_fence_before();
             arrive(kP + (u & 1));
             arrive(kGFree + (u & 1));
         }
     } else if (warp < 12) {
-        // ================================================================ values, outputs
+        // ================================================================ values
         const int t = tid - 256;
-        auto parts = [&](int u) {
-            if (!(wait2(kFull, u) && wait2(kGFull, u) && (u == 0 || wait1(kSum, u - 1)))) return false;
+#pragma unroll 1
+        for (int u = 0; u < nch; ++u) {
+            const bool short_chunk = it.rows - u * C < C;   // whose rows of K are cleared too
+            if (!(wait2(kFullV, u) && (!short_chunk || wait2(kFull, u)) && wait2(kGFull, u) &&
+                  (u == 0 || wait1(kSum, u - 1))))
+                break;
             uint8_t *st = sm + (u & 1) * Smem::kStage;
-            const float f = gates[u & 1].w[t];
+            const float w = gates[u & 1].w[t];
+            const Pair f = pair_of(w, w);
             const bool real = u * C + t < it.rows;
+            // half a row's loads before the first store, which the compiler has to keep in order
+#pragma unroll 1
+            for (int c0 = 0; c0 < kCols / 8; c0 += 4) {
+                uint4 v[4];
 #pragma unroll
-            for (int c = 0; c < kCols / 8; ++c) {
-                const uint32_t o = at_tile(t, c);
-                uint4 hi = make_uint4(0, 0, 0, 0), mid = hi, lo = hi;
-                if (real) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(st + Smem::kV + o);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t part[4][3];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        split3(f * __uint_as_float(in[j] << 16),
-                               f * __uint_as_float(in[j] & 0xffff0000u), part[j]);
-                    hi = make_uint4(part[0][0], part[1][0], part[2][0], part[3][0]);
-                    mid = make_uint4(part[0][1], part[1][1], part[2][1], part[3][1]);
-                    lo = make_uint4(part[0][2], part[1][2], part[2][2], part[3][2]);
-                } else {
-                    // the next sequence's rows, which may hold anything: no part of any product
-                    *reinterpret_cast<uint4 *>(st + Smem::kV + o) = hi;
-                    *reinterpret_cast<uint4 *>(st + Smem::kK + o) = hi;
-                    if (kblocks == 2) *reinterpret_cast<uint4 *>(st + Smem::kK + kBlk + o) = hi;
+                for (int c = 0; c < 4; ++c) {
+                    uint8_t *at = st + Smem::kV + at_tile(t, c0 + c);
+                    v[c] = *reinterpret_cast<const uint4 *>(at);
+                    if (!real) {
+                        // the next sequence's rows, which may hold anything: no part of any product
+                        v[c] = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(at) = v[c];
+                        at += Smem::kK - Smem::kV;
+                        *reinterpret_cast<uint4 *>(at) = v[c];
+                        if (kblocks == 2) *reinterpret_cast<uint4 *>(at + kBlk) = v[c];
+                    }
                 }
-                *reinterpret_cast<uint4 *>(sm + Smem::kW + o) = hi;
-                *reinterpret_cast<uint4 *>(sm + Smem::kW + kBlk + o) = mid;
-                *reinterpret_cast<uint4 *>(sm + Smem::kW + 2 * kBlk + o) = lo;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t part[4][3];
+                    split3(mul2(f, widen(v[c].x)), part[0]);
+                    split3(mul2(f, widen(v[c].y)), part[1]);
+                    split3(mul2(f, widen(v[c].z)), part[2]);
+                    split3(mul2(f, widen(v[c].w)), part[3]);
+                    uint8_t *to = sm + Smem::kW + at_tile(t, c0 + c);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        *reinterpret_cast<uint4 *>(to + i * kBlk) =
+                            make_uint4(part[0][i], part[1][i], part[2][i], part[3][i]);
+                }
             }
             fence_proxy_async_smem();
             arrive(kParts);
-            if (STATE) arrive(kGFree + (u & 1));
-            return true;
-        };
-        bool ok = nch > 0 && parts(0);
-#pragma unroll 1
-        for (int u = 0; ok && u < nch; ++u) {
-            if (u + 1 < nch && !(ok = parts(u + 1))) break;
-            if (STATE) continue;
-            if (!wait2(kDone, u)) break;
-            tc_fence_after();
-            const float e = gates[u & 1].e[t];
-            const float f = p.scale * (gates[u & 1].deep ? ex2f(fmaxf(-e, kFloor)) : 1.f / e);
-            uint32_t r[2][32];
-            tmem_ld32(tmem + lanes + kTOut, r[0]);
-            tmem_ld32(tmem + lanes + kTOut + 32, r[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive(kOFree);
             arrive(kGFree + (u & 1));
-            if (u * C + t < it.rows) {
-                __nv_bfloat16 *to =
-                    p.o + (static_cast<long long>(it.row + u * C + t) * p.H + h) * p.dv + c0;
-#pragma unroll
-                for (int c = 0; c < kCols; c += 16) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = pack_bf16x2(f * __uint_as_float(r[c / 32][c % 32 + 2 * j]),
-                                           f * __uint_as_float(r[c / 32][c % 32 + 2 * j + 1]));
-                    if (p.wide_store) {
-                        if (c0 + c < p.dv) store32(to + c, v);
-                    } else {
-                        if (c0 + c < p.dv)
-                            *reinterpret_cast<uint4 *>(to + c) = make_uint4(v[0], v[1], v[2], v[3]);
-                        if (c0 + c + 8 < p.dv)
-                            *reinterpret_cast<uint4 *>(to + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-                    }
-                }
-            }
         }
     } else if (warp == 12) {
-        // ================================================================ loads and gates
+        // ================================================================ loads
         int loads = 0;
-        auto load = [&](int u) {   // lane 0
-            uint8_t *st = sm + (u & 1) * Smem::kStage;
+        auto load_k = [&](int u) {
             uint64_t *full = &bar[kFull + (u & 1)];
-            const int t0 = it.row + u * C;
-            mbar_arrive_expect_tx(full, (kblocks * (STATE ? 1 : 2) + 1) * kBlk);
-            for (int b = 0; b < kblocks; ++b) {
-                if (!STATE) tma_load_3d(st + Smem::kQ + b * kBlk, &p.tq, full, b * 64, hk * p.q_step, t0);
-                tma_load_3d(st + Smem::kK + b * kBlk, &p.tk, full, b * 64, hk * p.k_step, t0);
-            }
-            tma_load_3d(st + Smem::kV, &p.tv, full, c0, h * p.v_step, t0);
+            warp_expect_tx(full, kblocks * (STATE ? 1 : 2) * kBlk);
+            for (int b = 0; b < kblocks; ++b)
+                warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kK + b * kBlk, &p.tk, full,
+                                 b * 64, hk * p.k_step, it.row + u * C);
             loads = u + 1;
         };
-        float g[4];
-        if (lane == 0)
-            for (int u = 0; u < 2 && u < nch; ++u) load(u);
+        auto load_q = [&](int u) {
+            for (int b = 0; !STATE && b < kblocks; ++b)
+                warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kQ + b * kBlk, &p.tq,
+                                 &bar[kFull + (u & 1)], b * 64, hk * p.q_step, it.row + u * C);
+        };
+        auto load_v = [&](int u) {
+            uint64_t *full = &bar[kFullV + (u & 1)];
+            warp_expect_tx(full, kBlk);
+            warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kV, &p.tv, full, c0,
+                             h * p.v_step, it.row + u * C);
+        };
 #pragma unroll 1
-        for (int u = 0; u < 2 && u < nch; ++u) {
-            load_gates(p, it.row + u * C, min(C, it.rows - u * C), h, g);
-            write_gates<STATE>(g, gates[u]);
-            arrive(kGFull + u);
+        for (int u = 0; u < nch; ++u) {
+            // each tile as soon as its last product of chunk u - 2 is done
+            if (u >= 2 && !wait1(kSum, u - 2)) break;
+            load_k(u);
+            if (!STATE && u >= 2 && !wait1(kQS, u - 2)) break;
+            load_q(u);
+            if (u >= 2 && !wait2(kDone, u - 2)) break;
+            load_v(u);
         }
+        // loads that an expired wait left under way land before the block gives up its memory
+        for (int u = max(0, loads - 2); u < loads; ++u) wait2(kFull, u), wait2(kFullV, u);
+    } else if (warp == 13) {
+        // ================================================================ gates
+        float g[4], next[4];
+        if (nch > 0) load_gates(p, it.row, min(C, it.rows), h, next);
 #pragma unroll 1
-        for (int u = 2; u < nch; ++u) {
-            load_gates(p, it.row + u * C, min(C, it.rows - u * C), h, g);
-            if (!wait2(kDone, u - 2)) break;
-            if (lane == 0) load(u);
-            __syncwarp();
-            if (!wait2(kGFree, u - 2)) break;
+        for (int u = 0; u < nch; ++u) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = next[j];
+            if (u + 1 < nch)
+                load_gates(p, it.row + (u + 1) * C, min(C, it.rows - (u + 1) * C), h, next);
+            if (u >= 2 && !wait2(kGFree, u - 2)) break;
             write_gates<STATE>(g, gates[u & 1]);
             arrive(kGFull + (u & 1));
         }
-        // loads that an expired wait left under way land before the block gives up its memory
-        if (lane == 0)
-            for (int u = max(0, loads - 2); u < loads; ++u)
-                mbar_wait_bounded(&bar[kFull + (u & 1)], static_cast<uint32_t>(u >> 1) & 1u, status);
-    } else if (lane == 0) {
+    } else {
         // ================================================================ products
-        auto until2 = [&](int b, int u) {
-            return mbar_wait_bounded(&bar[b + (u & 1)], static_cast<uint32_t>(u >> 1) & 1u, status);
-        };
-        auto until1 = [&](int b, int u) {
-            return mbar_wait_bounded(&bar[b], static_cast<uint32_t>(u) & 1u, status);
-        };
+        // a step of 16 of the common dimension, in descriptors: 16 rows of a tile whose rows are
+        // that dimension, 32 bytes of a row (and on to the next tile of 64 after four) otherwise
+        constexpr uint64_t kRows = 2048 >> 4, kBytes32 = 32 >> 4, kNext = (kBlk - 96) >> 4;
         auto scores = [&](int u) {
             constexpr uint32_t id = idesc_bf16(C, C, false, false);   // Q [t][c], K [i][c]
             const uint32_t st = a0 + (u & 1) * Smem::kStage;
+            uint64_t q = sw128_desc(st + Smem::kQ, 16, 1024), k = sw128_desc(st + Smem::kK, 16, 1024);
             tc_fence_after();
-            for (int k = 0; k < ksteps; ++k) {
-                const uint32_t o = (k >> 2) * kBlk + (k & 3) * 32;
-                mma_bf16_ss(tmem + kTScore + (u & 1) * C, sw128_desc(st + Smem::kQ + o, 16, 1024),
-                            sw128_desc(st + Smem::kK + o, 16, 1024), id, k > 0);
+#pragma unroll 1
+            for (int i = 0; i < ksteps; ++i) {
+                warp_mma_bf16_ss(tmem + kTScore + (u & 1) * C, q, k, id, i > 0);
+                const uint64_t on = (i & 3) == 3 ? kNext : kBytes32;
+                q += on;
+                k += on;
             }
-            mma_commit(&bar[kScore + (u & 1)]);
+            warp_mma_commit(&bar[kScore + (u & 1)]);
         };
-        if (!STATE && nch > 0 && until2(kFull, 0)) scores(0);
+        if (!STATE && nch > 0 && wait2(kFull, 0)) scores(0);
 #pragma unroll 1
         for (int u = 0; u < nch; ++u) {
             const uint32_t st = a0 + (u & 1) * Smem::kStage;
-            if (!(until2(kFull, u) && until1(kParts, u) && (u == 0 || until1(kSumFree, u - 1)))) break;
+            if (!(wait2(kFull, u) && wait1(kParts, u) && (u == 0 || wait1(kSumFree, u - 1)))) break;
             tc_fence_after();
             // K^T [c][t] by the parts [t][3 x 64]
             constexpr uint32_t id_sum = idesc_bf16(128, 3 * kCols, true, true);
-#pragma unroll
-            for (int k = 0; k < C / 16; ++k)
-                mma_bf16_ss(tmem + kTSum, sw128_desc(st + Smem::kK + k * 2048, kBlk, 1024),
-                            sw128_desc(a0 + Smem::kW + k * 2048, kBlk, 1024), id_sum, k > 0);
-            mma_commit(&bar[kSum]);
+            uint64_t x = sw128_desc(st + Smem::kK, kBlk, 1024);
+            uint64_t y = sw128_desc(a0 + Smem::kW, kBlk, 1024);
+#pragma unroll 1
+            for (int i = 0; i < C / 16; ++i, x += kRows, y += kRows)
+                warp_mma_bf16_ss(tmem + kTSum, x, y, id_sum, i > 0);
+            warp_mma_commit(&bar[kSum]);
             if (STATE) {
-                mma_commit(&bar[kDone + (u & 1)]);
+                warp_mma_commit(&bar[kDone + (u & 1)]);
                 continue;
             }
-            if (!(until1(kCopy, u) && (u == 0 || until1(kOFree, u - 1)))) break;
+            if (!(wait1(kCopy, u) && (u == 0 || wait1(kOFree, u - 1)))) break;
             tc_fence_after();
             // Q [t][c] by S [c][64]
             constexpr uint32_t id_out = idesc_bf16(C, kCols, false, true);
-            for (int k = 0; k < ksteps; ++k)
-                mma_bf16_ss(tmem + kTOut,
-                            sw128_desc(st + Smem::kQ + (k >> 2) * kBlk + (k & 3) * 32, 16, 1024),
-                            sw128_desc(a0 + Smem::kS + k * 2048, kBlk, 1024), id_out, k > 0);
-            mma_commit(&bar[kQS]);
-            if (u + 1 < nch) {
-                // the scores of chunk u - 1 lay where these go
-                if (!(until2(kFull, u + 1) && (u == 0 || until2(kDone, u - 1)))) break;
-                scores(u + 1);
+            x = sw128_desc(st + Smem::kQ, 16, 1024);
+            y = sw128_desc(a0 + Smem::kS, kBlk, 1024);
+#pragma unroll 1
+            for (int i = 0; i < ksteps; ++i, y += kRows) {
+                warp_mma_bf16_ss(tmem + kTOut, x, y, id_out, i > 0);
+                x += (i & 3) == 3 ? kNext : kBytes32;
             }
-            if (!until2(kP, u)) break;
+            warp_mma_commit(&bar[kQS]);
+            if (!wait2(kP, u)) break;
             tc_fence_after();
             // P [t][i] by V [i][64], onto Q S
-#pragma unroll
-            for (int k = 0; k < C / 16; ++k)
-                mma_bf16_ts(tmem + kTOut, tmem + kTScore + (u & 1) * C + k * 8,
-                            sw128_desc(st + Smem::kV + k * 2048, kBlk, 1024), id_out, 1u);
-            mma_commit(&bar[kDone + (u & 1)]);
+            y = sw128_desc(st + Smem::kV, kBlk, 1024);
+            uint32_t score = tmem + kTScore + (u & 1) * C;
+#pragma unroll 1
+            for (int i = 0; i < C / 16; ++i, y += kRows, score += 8)
+                warp_mma_bf16_ts(tmem + kTOut, score, y, id_out, 1u);
+            warp_mma_commit(&bar[kDone + (u & 1)]);
+            if (u + 1 < nch) {
+                // the scores of chunk u - 1 lay where these go
+                if (!(wait2(kFull, u + 1) && (u == 0 || wait2(kDone, u - 1)))) break;
+                scores(u + 1);
+            }
         }
         // every product ends before TMEM and shared memory are given up
-        mma_commit(&bar[kDrain]);
-        mbar_wait_bounded(&bar[kDrain], 0, status);
+        warp_mma_commit(&bar[kDrain]);
+        wait1(kDrain, 0);
     }
     __syncwarp();
     tc_fence_before();
