@@ -1036,25 +1036,6 @@ def _steps(name: str, meta, *dims) -> list:
     return [strides[i] if shape[i] > 1 else 0 for i in dims]
 
 
-def _span(t) -> tuple:
-    """The first address of a tensor's elements, and the one behind the last."""
-    first = t.data_ptr()
-    if t.numel() == 0:
-        return first, first
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-    return first, first + (last + 1) * t.element_size()
-
-
-def _clear_of(out, name: str, *others) -> None:
-    """`_apart` for inputs that may be strided."""
-    first, last = _span(out)
-    for t in others:
-        if t is not None:
-            begin, end = _span(t)
-            if first < end and begin < last:
-                raise ValueError(f"{name} must not share memory with an input")
-
-
 @functools.lru_cache(maxsize=256)
 def _headgate_checked(q, k, v, log_alpha, kinds):
     """The checks of a gla_headgate call's q, k, v and gates: (rows, Hk, H, dk, dv) and the C
@@ -1108,8 +1089,8 @@ def _headgate_lengths(cu: tuple, T: int, H: int, dk: int, dv: int):
         raise ValueError("cu_seqlens needs at least two entries")
     if cu[0] != 0 or cu[-1] != T or any(b < a for a, b in zip(cu, cu[1:])):
         raise ValueError("cu_seqlens must run from 0 to T_total without decreasing")
-    c = (ctypes.c_int * len(cu))(*cu)
-    return c, _entry("gla_headgate_fwd_varlen_scratch")(c, len(cu) - 1, H, dk, dv)
+    c = (ctypes.c_int * len(cu))(*map(int, cu))
+    return c, len(cu) - 1, _entry("gla_headgate_fwd_varlen_scratch")(c, len(cu) - 1, H, dk, dv)
 
 
 def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1134,9 +1115,8 @@ def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """
     (T, Hk, H, dk, dv), layout, _ = _headgate(q, k, v, log_alpha, torch.bfloat16)
     dev = q.device
-    cu = tuple(_bounds(cu_seqlens))
-    bounds, size = _headgate_lengths(cu, T, H, dk, dv)
-    N = len(cu) - 1
+    cu = tuple(cu_seqlens.tolist() if torch.is_tensor(cu_seqlens) else cu_seqlens)
+    bounds, N, size = _headgate_lengths(cu, T, H, dk, dv)
     state = (N, H, dk, dv)
     if h0 is not None:
         _need(h0, "h0", torch.float32, state, dev)
@@ -1147,9 +1127,7 @@ def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             hT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
             _need(hT, "final_state", torch.float32, state, dev)
-            _clear_of(hT, "final_state", q, k, v, log_alpha,
-                      None if h0 is None or h0.data_ptr() == hT.data_ptr() else h0)
-    o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
+    o = q.new_empty((T, H, dv))
     scratch = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     _call("gla_headgate_fwd_varlen", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_alpha.data_ptr(), dk ** -0.5 if scale is None else float(scale), _ptr(h0),
@@ -1181,12 +1159,10 @@ def gla_headgate_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alp
         _need(slots, "slots", torch.int64, (B,), dev)
     elif S < B:
         raise ValueError("h must have a state for each row, or slots be given")
-    _clear_of(h, "h", q, k, v, log_alpha, slots)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+        out = q.new_empty((B, H, dv))
     else:
         _need(out, "out", q.dtype, (B, H, dv), dev)
-        _clear_of(out, "out", q, k, v, log_alpha, slots, h)
     _call("gla_headgate_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_alpha.data_ptr(), dk ** -0.5 if scale is None else float(scale), h.data_ptr(),
           _ptr(slots), out.data_ptr(), B, S, Hk, H, dk, dv, layout, dtype)
@@ -1237,7 +1213,8 @@ def _norm_act_checked(x, gate, weight, bias, dx, norm, activation, eps):
     options = _lib.GlaNormActOptions(dtype=_DTYPES[kind], norm=_NORM_ACT_NORMS[norm],
                                      activation=_ACTIVATIONS[activation],
                                      per_channel=int(per_channel), eps=eps)
-    return B, T, H, d, ctypes.byref(layout), ctypes.byref(options)
+    scratch = 0 if dx is None else _entry("gla_group_norm_act_bwd_scratch")(B, T, H, d)
+    return B, T, H, d, ctypes.byref(layout), ctypes.byref(options), scratch
 
 
 def _norm_act_sizes(x, gate, weight, bias, dx, norm, activation, eps):
@@ -1269,9 +1246,9 @@ def gla_group_norm_act_fwd(x: torch.Tensor, gate: torch.Tensor | None = None,
     shape and type.  d is a multiple of 8 up to 512.
     """
     sizes = _norm_act_sizes(x, gate, weight, bias, None, norm, activation, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x.new_empty(x.shape)
     _call("gla_group_norm_act_fwd", x.device, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
-          y.data_ptr(), *sizes)
+          y.data_ptr(), *sizes[:6])
     return y
 
 
@@ -1279,19 +1256,17 @@ def _norm_act_bwd(dy, x, gate, weight, bias, options, need_dweight, need_dbias):
     # the gradient of x lies as x does where x has no gaps and no overlaps
     dx = torch.empty_like(x)
     if dx.stride(-1) != 1:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = x.new_empty(x.shape)
     sizes = _norm_act_sizes(x, gate, weight, bias, dx, *options)
-    dev = x.device
-    dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dgate = None if gate is None else x.new_empty(x.shape)
     dw = torch.empty_like(weight) if weight is not None and need_dweight else None
     db = torch.empty_like(bias) if bias is not None and need_dbias else None
-    scratch, size = None, 0
+    scratch = None
     if dw is not None or db is not None:
-        size = _entry("gla_group_norm_act_bwd_scratch")(*sizes[:4])
-        scratch = torch.empty(size, dtype=torch.uint8, device=dev)
-    _call("gla_group_norm_act_bwd", dev, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
-          dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), *sizes, _ptr(scratch),
-          size)
+        scratch = torch.empty(sizes[6], dtype=torch.uint8, device=x.device)
+    _call("gla_group_norm_act_bwd", x.device, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
+          dy.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), *sizes[:6],
+          _ptr(scratch), sizes[6])
     return dx, dgate, dw, db
 
 

@@ -69,6 +69,18 @@ int headgate_check(const void *q, const void *k, const void *v, const float *log
     return GLA_OK;
 }
 
+void headgate_inputs(Span (&in)[4], const void *q, const void *k, const void *v,
+                     const float *log_alpha, int rows, int Hk, int H, int dk, int dv, int size,
+                     const gla_headgate_layout &lay) {
+    const auto reach = [&](long long st, long long sh, int heads, int d) {
+        return rows > 0 ? static_cast<unsigned long long>((rows - 1) * st + (heads - 1) * sh + d) : 0;
+    };
+    in[0] = span_of(q, reach(lay.q_st, lay.q_sh, Hk, dk), size);
+    in[1] = span_of(k, reach(lay.k_st, lay.k_sh, Hk, dk), size);
+    in[2] = span_of(v, reach(lay.v_st, lay.v_sh, H, dv), size);
+    in[3] = span_of(log_alpha, reach(lay.a_st, lay.a_sh, H, 1), 4);
+}
+
 namespace {
 
 constexpr int C = 128;                   // tokens of a chunk
@@ -814,6 +826,14 @@ int gla_headgate_fwd_varlen(const void *q, const void *k, const void *v, const f
     if (T_total > 1 && (!layout->q_st || !layout->k_st || !layout->v_st)) return GLA_ERR_ARG;
     // a chunk's last row is counted on past the last token in 32 bits
     if (T_total > INT_MAX - C) return GLA_ERR_ARG;
+    Span in[4];
+    headgate_inputs(in, q, k, v, log_alpha, T_total, Hk, H, dk, dv, 2, *layout);
+    const unsigned long long states = static_cast<unsigned long long>(N) * H * dk * dv;
+    const Span out = span_of(o, static_cast<unsigned long long>(T_total) * H * dv, 2);
+    const Span begin = span_of(h0, states, 4), end = span_of(hT, states, 4);
+    if (meets_any(out, in) || meets_any(end, in) || meet(out, begin) || meet(out, end) ||
+        (h0 != hT && meet(begin, end)))
+        return GLA_ERR_ARG;
     const Plan plan = make_plan(cu_seqlens, N, H, dv);
     if (plan.slots > INT_MAX) return GLA_ERR_ARG;
     const size_t need = scratch_of(plan, H, dk, dv);

@@ -179,6 +179,15 @@ extern "C" int gla_headgate_step(const void *q, const void *k, const void *v,
     if ((reinterpret_cast<uintptr_t>(h) & 15) || (reinterpret_cast<uintptr_t>(slots) & 7))
         return GLA_ERR_ARG;
     if (static_cast<long long>(B) * H > INT_MAX) return GLA_ERR_ARG;
+    const int size = dtype == GLA_BF16 ? 2 : 4;
+    Span in[4];
+    headgate_inputs(in, q, k, v, log_alpha, B, Hk, H, dk, dv, size, *layout);
+    const Span pool = span_of(h, static_cast<unsigned long long>(S) * H * dk * dv, 4);
+    const Span out = span_of(o, static_cast<unsigned long long>(B) * H * dv, size);
+    const Span names = span_of(slots, B, 8);
+    if (meets_any(pool, in) || meets_any(out, in) || meet(pool, out) || meet(pool, names) ||
+        meet(out, names))
+        return GLA_ERR_ARG;
     StepArgs a = {};
     int sms = 0;
     const int dev = usable_device(&sms, &a.status);

@@ -185,9 +185,35 @@ bool head_map(CUtensorMap *map, const void *ptr, int d, int heads, int tokens, l
 // word, when it is an sm_103; returns a GLA status.
 int usable_device(int *sm_count, unsigned int **status = nullptr);
 
+// Memory that a tensor takes up, from its first element to the end of its last; and whether two
+// share some.  Null pointers share nothing.
+struct Span {
+    const void *at;
+    unsigned long long bytes;
+};
+inline Span span_of(const void *p, unsigned long long elements, unsigned long long size) {
+    return {p, elements * size};
+}
+inline bool meet(const Span &a, const Span &b) {
+    const unsigned long long x = reinterpret_cast<unsigned long long>(a.at);
+    const unsigned long long y = reinterpret_cast<unsigned long long>(b.at);
+    return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// Whether `out` shares memory with one of the tensors.
+template <int N>
+bool meets_any(const Span &out, const Span (&others)[N]) {
+    for (const Span &o : others)
+        if (meet(out, o)) return true;
+    return false;
+}
+
 // What every gla_headgate_* call asks of its pointers, sizes and strides; a GLA status.
 int headgate_check(const void *q, const void *k, const void *v, const float *log_alpha,
                    const float *h, const void *o, int Hk, int H, int dk, int dv,
                    const gla_headgate_layout &lay);
+// The memory of q, k, v and log_alpha, in this order; `size`: bytes of an element of q, k and v.
+void headgate_inputs(Span (&in)[4], const void *q, const void *k, const void *v,
+                     const float *log_alpha, int rows, int Hk, int H, int dk, int dv, int size,
+                     const gla_headgate_layout &lay);
 
 }  // namespace gla

@@ -8,7 +8,15 @@
 // A warp keeps its heads (a group of lanes and 8 or 16 values a lane for each) and walks
 // tokens, so that weights and the sums for their gradients stay in registers, whether every
 // head has its own or not.  Eight warps take eight neighbouring tokens: head-first rows of a
-// block are then contiguous runs too.
+// block are then contiguous runs too.  The next token's rows are loaded while one is worked on
+// (two ahead are slower: 255 us for 250 of B2 T32768, 16 heads of 256), and the offsets go on
+// by additions (a division by T for each row took 40 us where it is 35 at B8 T2048).
+//
+// Bound by HBM where instructions leave it room (6 bytes a bf16 value forward with a gate, 10
+// backward).  Measured on one GB300, bf16, gate: B2 T32768, 16 heads of 256, mean, weights and
+// biases of every channel 252 us (6.4 TB/s of a copy's 6.79); B8 T2048, 16 heads of 128,
+// head-first in, gate in a wider tensor 35.5 us (5.7 TB/s); B4 T4096 of the same forward 35 us and
+// backward 73 us (4.6 TB/s) with its second launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,8 +32,13 @@ namespace gla {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr long long kFwdBlocks = 4864;   // thread blocks of the forward, at most (32 an SM)
-constexpr long long kBwdBlocks = 608;    // of the backward, where that keeps kSumRows (4 an SM)
+// Thread blocks of an SM that run at once, and of a launch (a second round of blocks only costs
+// its beginning: twice as many forward 41.0 us for 40.4 at B8 T2048, 16 heads of 128, backward
+// 134 for 123).  The backward's are a constant of 152 SMs, since its scratch is sized by the
+// tensors alone.
+template <typename E, int NB>
+constexpr int kFwdPerSm = NB > 1 ? 2 : sizeof(E) == 2 ? 4 : 3;
+constexpr long long kBwdBlocks = 304;    // 2 an SM, more where that keeps kSumRows
 constexpr int kSumRows = 1024;           // rows that a lane adds in 32 bits
 
 struct NormArgs {
@@ -40,46 +53,102 @@ struct NormArgs {
     float inv_d, eps;
 };
 
-// Eight neighbouring values of a row, in 32 bits.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
-    const unsigned w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+// Two fp32 values, for operations on both in one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(float a, float b) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ Pair twice(float a) { return pair_of(a, a); }
+__device__ __forceinline__ float2 both(Pair r) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+    return v;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
+// Eight neighbouring values of a row, as they lie in memory.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        v = __ldg(reinterpret_cast<const uint4 *>(p));
+    }
+    __device__ __forceinline__ static Pair widen(unsigned w) {
+        return pair_of(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ __forceinline__ void get(Pair (&x)[4]) const {
+        x[0] = widen(v.x), x[1] = widen(v.y), x[2] = widen(v.z), x[3] = widen(v.w);
+    }
+    __device__ __forceinline__ static unsigned narrow(Pair p) {
+        const float2 f = both(p);
+        return pack_bf16x2(f.x, f.y);
+    }
+    __device__ __forceinline__ static void store(__nv_bfloat16 *p, const Pair (&x)[4]) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(narrow(x[0]), narrow(x[1]), narrow(x[2]), narrow(x[3]));
+    }
+};
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void get(Pair (&x)[4]) const {
+        x[0] = pair_of(a.x, a.y), x[1] = pair_of(a.z, a.w);
+        x[2] = pair_of(b.x, b.y), x[3] = pair_of(b.z, b.w);
+    }
+    __device__ __forceinline__ static void store(float *p, const Pair (&x)[4]) {
+        const float2 u = both(x[0]), v = both(x[1]), w = both(x[2]), z = both(x[3]);
+        reinterpret_cast<float4 *>(p)[0] = make_float4(u.x, u.y, v.x, v.y);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(w.x, w.y, z.x, z.y);
+    }
+};
+
 template <int LANES>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float group_sum(Pair v) {
+    const float2 f = both(v);
+    float s = f.x + f.y;
 #pragma unroll
-    for (int off = LANES / 2; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+    for (int off = LANES / 2; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    return s;
 }
 
 // s(z) = 1 / (1 + exp(-z)).  Rows that end in bf16 take the hardware's 2^x and reciprocal (each
 // within a few roundings of 2^-23), fp32 rows CUDA's own.
-__device__ __forceinline__ float sigmoid(float z, __nv_bfloat16) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2f(-1.4426950408889634f * z)));
-    return r;
+__device__ __forceinline__ Pair sigmoid(Pair z, __nv_bfloat16) {
+    const float2 x = both(mul2(z, twice(-1.4426950408889634f)));
+    const float2 d = both(add2(pair_of(ex2f(x.x), ex2f(x.y)), twice(1.f)));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+    return pair_of(r.x, r.y);
 }
-__device__ __forceinline__ float sigmoid(float z, float) { return 1.f / (1.f + expf(-z)); }
+__device__ __forceinline__ Pair sigmoid(Pair z, float) {
+    const float2 x = both(z);
+    return pair_of(1.f / (1.f + expf(-x.x)), 1.f / (1.f + expf(-x.y)));
+}
 
 // A warp's place: its lanes' heads and channels.
 template <int LANES, int NB>
@@ -103,105 +172,160 @@ struct Place {
 
 template <int LANES, int NB>
 __device__ __forceinline__ void load_weights(const NormArgs &p, const Place<LANES, NB> &at,
-                                             float (&w)[NB][8], float (&b)[NB][8]) {
+                                             Pair (&w)[NB][4], Pair (&b)[NB][4]) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[i][e] = 1.f, b[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) w[i][e] = twice(1.f), b[i][e] = 0;
         if (!at.there[i]) continue;
         const int o = (p.per_channel ? at.h * p.d : 0) + at.c[i];
-        if (p.w) load8(p.w + o, w[i]);
-        if (p.b) load8(p.b + o, b[i]);
+        Raw<float> r;
+        if (p.w) r.load(p.w + o), r.get(w[i]);
+        if (p.b) r.load(p.b + o), r.get(b[i]);
     }
 }
 
-// Where a token's row starts, in elements.
-__device__ __forceinline__ long long row_of(const NormArgs &p, unsigned n, long long sb,
-                                            long long st) {
-    if (p.T == p.tokens) return n * st;
-    const unsigned b = n / p.T;
-    return b * sb + (n - b * p.T) * st;
-}
+// A walk over tokens n, n + step, ...: the offset of a row's start (in elements) goes on by what a
+// step adds in whole sequences and tokens, and once more by what a token past a sequence's end is
+// off, without a division after the first.
+struct Walk {
+    long long at, on, wrap;
+
+    __device__ __forceinline__ Walk(const NormArgs &p, unsigned n, unsigned step, int h,
+                                    long long sb, long long st, long long sh) {
+        const unsigned b = n / p.T, q = step / p.T;
+        at = b * sb + (n - b * p.T) * st + h * sh;
+        on = q * sb + (step - q * p.T) * st;
+        wrap = sb - p.T * st;
+    }
+    __device__ __forceinline__ void next(bool wraps) { at += wraps ? on + wrap : on; }
+};
+// The token of a walk: whether its step goes past the end of its sequence.
+struct Token {
+    unsigned n, t, step, rest;
+
+    __device__ __forceinline__ Token(const NormArgs &p, unsigned first, unsigned by)
+        : n(first), t(first % p.T), step(by), rest(by % p.T) {}
+    __device__ __forceinline__ bool next(const NormArgs &p) {
+        n += step;
+        t += rest;
+        const bool wraps = t >= p.T;
+        if (wraps) t -= p.T;
+        return wraps;
+    }
+};
+
+// A lane's part of one row of each input, on its way.
+template <typename E, int NB, bool GATE, bool BACKWARD>
+struct Row {
+    Raw<E> x[NB], g[GATE ? NB : 1], dy[BACKWARD ? NB : 1];
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            x[i].clear();
+            if (GATE) g[i].clear();
+            if (BACKWARD) dy[i].clear();
+        }
+    }
+};
+
+// The walk of the inputs, ahead of the work.
+template <typename E, int LANES, int NB, bool GATE, bool BACKWARD>
+struct Loads {
+    Token token;
+    Walk x, g;
+    long long flat, flat_on;     // dy, contiguous
+
+    __device__ __forceinline__ Loads(const NormArgs &p, int h, unsigned n, unsigned step)
+        : token(p, n, step), x(p, n, step, h, p.lay.x_sb, p.lay.x_st, p.lay.x_sh),
+          g(p, n, step, h, p.lay.g_sb, p.lay.g_st, p.lay.g_sh),
+          flat((static_cast<long long>(n) * p.H + h) * p.d),
+          flat_on(static_cast<long long>(step) * p.H * p.d) {}
+    __device__ __forceinline__ void next(const NormArgs &p, const Place<LANES, NB> &at,
+                                         Row<E, NB, GATE, BACKWARD> &row) {
+        if (token.n < p.tokens) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                if (at.there[i]) {
+                    row.x[i].load(static_cast<const E *>(p.x) + x.at + at.c[i]);
+                    if (GATE) row.g[i].load(static_cast<const E *>(p.gate) + g.at + at.c[i]);
+                    if (BACKWARD) row.dy[i].load(static_cast<const E *>(p.dy) + flat + at.c[i]);
+                }
+        }
+        const bool wraps = token.next(p);
+        x.next(wraps);
+        if (GATE) g.next(wraps);
+        if (BACKWARD) flat += flat_on;
+    }
+};
 
 // x becomes xhat; returns r.
 template <int LANES, int NB>
 __device__ __forceinline__ float normalise(const NormArgs &p, const Place<LANES, NB> &at,
-                                           float (&x)[NB][8]) {
+                                           Pair (&x)[NB][4]) {
     if (p.layer) {
-        float s = 0.f;
+        Pair s = 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s += x[i][e];
-        const float mean = group_sum<LANES>(s) * p.inv_d;
+            for (int e = 0; e < 4; ++e) s = add2(s, x[i][e]);
+        const Pair mean = twice(-p.inv_d * group_sum<LANES>(s));
 #pragma unroll
         for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = at.there[i] ? x[i][e] - mean : 0.f;
+            for (int e = 0; e < 4; ++e) x[i][e] = at.there[i] ? add2(x[i][e], mean) : 0;
     }
-    float s = 0.f;
+    Pair s = 0;
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(x[i][e], x[i][e], s);
+        for (int e = 0; e < 4; ++e) s = fma2(x[i][e], x[i][e], s);
     const float r = rsqrtf(fmaf(group_sum<LANES>(s), p.inv_d, p.eps));
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] *= r;
+        for (int e = 0; e < 4; ++e) x[i][e] = mul2(x[i][e], twice(r));
     return r;
 }
 
 template <typename E, int LANES, int NB, bool GATE>
-__global__ void __launch_bounds__(32 * kWarps) norm_fwd_kernel(const NormArgs p) {
-    constexpr int U = NB == 1 ? 2 : 1;   // tokens whose loads are under way together
+__global__ void __launch_bounds__(32 * kWarps, kFwdPerSm<E, NB>) norm_fwd_kernel(const NormArgs p) {
     const Place<LANES, NB> at(p);
-    float w[NB][8], b[NB][8];
+    Pair w[NB][4], b[NB][4];
     load_weights<LANES, NB>(p, at, w, b);
-    const unsigned step = gridDim.x / p.groups * kWarps * U;
-    for (unsigned n0 = blockIdx.x / p.groups * kWarps * U + threadIdx.x / 32; n0 < p.tokens;
-         n0 += step) {
-        float x[U][NB][8], g[U][NB][8];
+    const unsigned step = gridDim.x / p.groups * kWarps;
+    unsigned n = blockIdx.x / p.groups * kWarps + threadIdx.x / 32;
+    Loads<E, LANES, NB, GATE, false> loads(p, at.h, n, step);
+    Row<E, NB, GATE, false> row, next;   // the next token's loads are on their way
+    row.clear();
+    next.clear();
+    loads.next(p, at, row);
+    E *py = static_cast<E *>(p.y) + (static_cast<long long>(n) * p.H + at.h) * p.d;
+    for (; n < p.tokens; n += step, py += static_cast<long long>(step) * p.H * p.d) {
+        loads.next(p, at, next);
+        Pair x[NB][4];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const unsigned n = n0 + k * kWarps;
-            const bool real = n < p.tokens;
-            const E *px = static_cast<const E *>(p.x) + row_of(p, n, p.lay.x_sb, p.lay.x_st) +
-                          at.h * p.lay.x_sh;
-            const E *pg = nullptr;
+        for (int i = 0; i < NB; ++i) row.x[i].get(x[i]);
+        normalise<LANES, NB>(p, at, x);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            Pair m[4], z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = z[e] = fma2(x[i][e], w[i][e], b[i][e]);
+            if (GATE) row.g[i].get(z);
+            Pair f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = sigmoid(z[e], E{});
+            if (p.silu)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = mul2(f[e], z[e]);
             if (GATE)
-                pg = static_cast<const E *>(p.gate) + row_of(p, n, p.lay.g_sb, p.lay.g_st) +
-                     at.h * p.lay.g_sh;
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[k][i][e] = g[k][i][e] = 0.f;
-                if (real && at.there[i]) {
-                    load8(px + at.c[i], x[k][i]);
-                    if (GATE) load8(pg + at.c[i], g[k][i]);
-                }
-            }
+                for (int e = 0; e < 4; ++e) f[e] = mul2(f[e], m[e]);
+            if (at.there[i]) Raw<E>::store(py + at.c[i], f);
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const unsigned n = n0 + k * kWarps;
-            normalise<LANES, NB>(p, at, x[k]);
-            E *py = static_cast<E *>(p.y) +
-                    (static_cast<long long>(n) * p.H + at.h) * p.d;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float m = fmaf(x[k][i][e], w[i][e], b[i][e]);
-                    const float z = GATE ? g[k][i][e] : m;
-                    const float s = sigmoid(z, E{});
-                    const float f = p.silu ? z * s : s;
-                    y[e] = GATE ? m * f : f;
-                }
-                if (n < p.tokens && at.there[i]) store8(py + at.c[i], y);
-            }
-        }
+        row = next;
     }
 }
 
@@ -209,7 +333,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_fwd_kernel(const NormArgs p)
 // share a weight.  v: a lane's values; out: the block's row of the partial sums.
 template <int LANES, int NB>
 __device__ __forceinline__ void block_sums(const NormArgs &p, const Place<LANES, NB> &at,
-                                           float (*buf)[32][NB][8], float (&v)[NB][8],
+                                           float (*buf)[32][NB][8], const Pair (&v)[NB][4],
                                            float *out) {
     constexpr int ROWS = 32 / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -217,7 +341,7 @@ __device__ __forceinline__ void block_sums(const NormArgs &p, const Place<LANES,
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) buf[warp][lane][i][e] = v[i][e];
+        for (int e = 0; e < 4; ++e) reinterpret_cast<Pair *>(buf[warp][lane][i])[e] = v[i][e];
     __syncthreads();
     // one thread a value: per head [ROWS][d], or summed over the rows [d]
     const int values = p.per_channel ? ROWS * p.d : p.d;
@@ -232,69 +356,80 @@ __device__ __forceinline__ void block_sums(const NormArgs &p, const Place<LANES,
 }
 
 template <typename E, int LANES, int NB, bool GATE>
-__global__ void __launch_bounds__(32 * kWarps) norm_bwd_kernel(const NormArgs p) {
-    __shared__ float buf[kWarps][32][NB][8];
+__global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 2 : 1) norm_bwd_kernel(const NormArgs p) {
+    __shared__ __align__(16) float buf[kWarps][32][NB][8];
     const Place<LANES, NB> at(p);
-    float w[NB][8], b[NB][8], dw[NB][8], db[NB][8];
+    Pair w[NB][4], b[NB][4], dw[NB][4], db[NB][4];
     load_weights<LANES, NB>(p, at, w, b);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) dw[i][e] = db[i][e] = 0;
     const unsigned step = gridDim.x / p.groups * kWarps;
-    for (unsigned n = blockIdx.x / p.groups * kWarps + threadIdx.x / 32; n < p.tokens; n += step) {
-        float x[NB][8], g[NB][8], dy[NB][8];
-        const E *px = static_cast<const E *>(p.x) + row_of(p, n, p.lay.x_sb, p.lay.x_st) +
-                      at.h * p.lay.x_sh;
-        const E *pg = nullptr;
-        if (GATE)
-            pg = static_cast<const E *>(p.gate) + row_of(p, n, p.lay.g_sb, p.lay.g_st) +
-                 at.h * p.lay.g_sh;
-        const long long flat = (static_cast<long long>(n) * p.H + at.h) * p.d;
+    const unsigned n = blockIdx.x / p.groups * kWarps + threadIdx.x / 32;
+    Loads<E, LANES, NB, GATE, true> loads(p, at.h, n, step);
+    Token token(p, n, step);
+    Walk out(p, n, step, at.h, p.lay.dx_sb, p.lay.dx_st, p.lay.dx_sh);
+    Row<E, NB, GATE, true> row, next;   // the next token's loads are on their way
+    row.clear();
+    next.clear();
+    loads.next(p, at, row);
+    long long flat = (static_cast<long long>(n) * p.H + at.h) * p.d;
+    while (token.n < p.tokens) {
+        loads.next(p, at, next);
+        Pair x[NB][4], u[NB][4];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = g[i][e] = dy[i][e] = 0.f;
-            if (at.there[i]) {
-                load8(px + at.c[i], x[i]);
-                load8(static_cast<const E *>(p.dy) + flat + at.c[i], dy[i]);
-                if (GATE) load8(pg + at.c[i], g[i]);
-            }
-        }
+        for (int i = 0; i < NB; ++i) row.x[i].get(x[i]);
         const float r = normalise<LANES, NB>(p, at, x);
-        float su = 0.f, sux = 0.f;
+        Pair su = 0, sux = 0;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            float dg[8];
+            Pair m[4], z[4], dy[4], s[4], f[4];
+            row.dy[i].get(dy);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float m = fmaf(x[i][e], w[i][e], b[i][e]);
-                const float z = GATE ? g[i][e] : m;
-                const float s = sigmoid(z, E{});
-                const float f = p.silu ? z * s : s;
-                const float slope = p.silu ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
-                const float dn = dy[i][e] * (GATE ? f : slope);
-                dg[e] = dy[i][e] * m * slope;
-                dw[i][e] = fmaf(dn, x[i][e], dw[i][e]);
-                db[i][e] += dn;
-                const float u = dn * w[i][e];
-                dy[i][e] = u;
-                su += u;
-                sux = fmaf(u, x[i][e], sux);
+            for (int e = 0; e < 4; ++e) m[e] = z[e] = fma2(x[i][e], w[i][e], b[i][e]);
+            if (GATE) row.g[i].get(z);
+            // f and, in s, its slope
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[e] = sigmoid(z[e], E{});
+                s[e] = fma2(f[e], twice(-1.f), twice(1.f));
             }
-            if (GATE && at.there[i]) store8(static_cast<E *>(p.dgate) + flat + at.c[i], dg);
+            if (p.silu) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[e] = mul2(f[e], fma2(z[e], s[e], twice(1.f)));
+                    f[e] = mul2(f[e], z[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = mul2(f[e], s[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Pair dn = mul2(dy[e], GATE ? f[e] : s[e]);
+                if (GATE) s[e] = mul2(mul2(dy[e], m[e]), s[e]);
+                dw[i][e] = fma2(dn, x[i][e], dw[i][e]);
+                db[i][e] = add2(db[i][e], dn);
+                u[i][e] = mul2(dn, w[i][e]);
+                su = add2(su, u[i][e]);
+                sux = fma2(u[i][e], x[i][e], sux);
+            }
+            if (GATE && at.there[i]) Raw<E>::store(static_cast<E *>(p.dgate) + flat + at.c[i], s);
         }
-        const float m1 = group_sum<LANES>(sux) * p.inv_d;
-        const float m0 = p.layer ? group_sum<LANES>(su) * p.inv_d : 0.f;
-        E *pd = static_cast<E *>(p.dx) + row_of(p, n, p.lay.dx_sb, p.lay.dx_st) +
-                at.h * p.lay.dx_sh;
+        const Pair m1 = twice(-p.inv_d * group_sum<LANES>(sux));
+        const Pair m0 = twice(p.layer ? -p.inv_d * group_sum<LANES>(su) : 0.f);
+        E *pd = static_cast<E *>(p.dx) + out.at;
+        out.next(token.next(p));
+        flat += static_cast<long long>(step) * p.H * p.d;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = r * (dy[i][e] - m0 - x[i][e] * m1);
-            if (at.there[i]) store8(pd + at.c[i], v);
+            for (int e = 0; e < 4; ++e)
+                u[i][e] = mul2(twice(r), fma2(x[i][e], m1, add2(u[i][e], m0)));
+            if (at.there[i]) Raw<E>::store(pd + at.c[i], u[i]);
         }
+        row = next;
     }
     if (p.partial) {
         constexpr int ROWS = 32 / LANES;
@@ -338,15 +473,14 @@ int rows_of(int d) { return d <= 64 ? 4 : d <= 128 ? 2 : 1; }
 
 // Blocks for each group of heads: enough for the GPU, no more than there are tokens, and in the
 // backward no fewer than keep a lane's sums to kSumRows rows.
-long long token_blocks(long long tokens, int groups, int each, long long most, int sum_rows) {
-    const long long want = std::min((tokens + kWarps * each - 1) / (kWarps * each),
-                                    std::max(1LL, most / groups));
+long long token_blocks(long long tokens, int groups, long long most, int sum_rows) {
+    const long long want = std::min((tokens + kWarps - 1) / kWarps, std::max(1LL, most / groups));
     return std::max(want, sum_rows ? (tokens + kWarps * sum_rows - 1) / (kWarps * sum_rows) : 1);
 }
 
 template <typename E, int LANES, int NB>
-int launch_fwd(const NormArgs &a, cudaStream_t stream) {
-    const long long tb = token_blocks(a.tokens, a.groups, NB == 1 ? 2 : 1, kFwdBlocks, 0);
+int launch_fwd(const NormArgs &a, int sms, cudaStream_t stream) {
+    const long long tb = token_blocks(a.tokens, a.groups, sms * kFwdPerSm<E, NB>, 0);
     if (tb * a.groups > INT_MAX) return -1;
     const unsigned grid = static_cast<unsigned>(tb * a.groups);
     if (a.gate) norm_fwd_kernel<E, LANES, NB, true><<<grid, 32 * kWarps, 0, stream>>>(a);
@@ -356,7 +490,7 @@ int launch_fwd(const NormArgs &a, cudaStream_t stream) {
 
 template <typename E, int LANES, int NB>
 int launch_bwd(const NormArgs &a, float *dw, float *db, cudaStream_t stream) {
-    const long long tb = token_blocks(a.tokens, a.groups, 1, kBwdBlocks, kSumRows);
+    const long long tb = token_blocks(a.tokens, a.groups, kBwdBlocks, kSumRows);
     if (tb * a.groups > INT_MAX) return -1;
     const unsigned grid = static_cast<unsigned>(tb * a.groups);
     if (a.gate) norm_bwd_kernel<E, LANES, NB, true><<<grid, 32 * kWarps, 0, stream>>>(a);
@@ -371,11 +505,11 @@ int launch_bwd(const NormArgs &a, float *dw, float *db, cudaStream_t stream) {
 }
 
 template <typename E>
-int fwd(const NormArgs &a, cudaStream_t stream) {
-    if (a.d <= 64) return launch_fwd<E, 8, 1>(a, stream);
-    if (a.d <= 128) return launch_fwd<E, 16, 1>(a, stream);
-    if (a.d <= 256) return launch_fwd<E, 32, 1>(a, stream);
-    return launch_fwd<E, 32, 2>(a, stream);
+int fwd(const NormArgs &a, int sms, cudaStream_t stream) {
+    if (a.d <= 64) return launch_fwd<E, 8, 1>(a, sms, stream);
+    if (a.d <= 128) return launch_fwd<E, 16, 1>(a, sms, stream);
+    if (a.d <= 256) return launch_fwd<E, 32, 1>(a, sms, stream);
+    return launch_fwd<E, 32, 2>(a, sms, stream);
 }
 
 template <typename E>
@@ -437,6 +571,19 @@ int bind(NormArgs *a, const void *x, const void *gate, const float *weight, cons
     return GLA_OK;
 }
 
+// The memory of x, gate, weight and bias, in this order.
+void inputs_of(Span (&in)[4], const NormArgs &a, int B, int T, const gla_norm_act_layout &lay,
+               int size) {
+    const auto reach = [&](long long sb, long long st, long long sh) {
+        return static_cast<unsigned long long>((B - 1) * sb + (T - 1) * st + (a.H - 1) * sh + a.d);
+    };
+    const unsigned long long weights = a.per_channel ? static_cast<unsigned long long>(a.H) * a.d : a.d;
+    in[0] = span_of(a.x, reach(lay.x_sb, lay.x_st, lay.x_sh), size);
+    in[1] = span_of(a.gate, reach(lay.g_sb, lay.g_st, lay.g_sh), size);
+    in[2] = span_of(a.w, weights, 4);
+    in[3] = span_of(a.b, weights, 4);
+}
+
 }  // namespace
 }  // namespace gla
 
@@ -452,10 +599,16 @@ int gla_group_norm_act_fwd(const void *x, const void *gate, const float *weight,
     int st = bind(&a, x, gate, weight, bias, B, T, H, d, *layout, *options, false);
     if (st != GLA_OK) return st;
     a.y = y;
+    const int size = options->dtype == GLA_BF16 ? 2 : 4;
+    Span in[4];
+    inputs_of(in, a, B, T, *layout, size);
+    if (meets_any(span_of(y, static_cast<unsigned long long>(a.tokens) * H * d, size), in))
+        return GLA_ERR_ARG;
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
-    const int e = options->dtype == GLA_BF16 ? fwd<__nv_bfloat16>(a, stream) : fwd<float>(a, stream);
+    const int e = options->dtype == GLA_BF16 ? fwd<__nv_bfloat16>(a, sms, stream)
+                                             : fwd<float>(a, sms, stream);
     return e == 0 ? GLA_OK : e < 0 ? GLA_ERR_ARG : GLA_ERR_LAUNCH;
 }
 
@@ -463,7 +616,7 @@ unsigned long gla_group_norm_act_bwd_scratch(int B, int T, int H, int d) {
     using namespace gla;
     if (B <= 0 || T <= 0 || H <= 0 || d <= 0) return 0;
     const int rows = rows_of(d), groups = (H + rows - 1) / rows;
-    const long long tb = token_blocks(static_cast<long long>(B) * T, groups, 1, kBwdBlocks, kSumRows);
+    const long long tb = token_blocks(static_cast<long long>(B) * T, groups, kBwdBlocks, kSumRows);
     return 2ul * sizeof(float) * tb * groups * rows * d;
 }
 
@@ -487,6 +640,22 @@ int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
         if (scratch_bytes < gla_group_norm_act_bwd_scratch(B, T, H, d)) return GLA_ERR_SCRATCH;
         if (!aligned(grad_weight, 4) || !aligned(grad_bias, 4)) return GLA_ERR_ARG;
         a.partial = static_cast<float *>(scratch);
+    }
+    const int size = options->dtype == GLA_BF16 ? 2 : 4;
+    const unsigned long long n = static_cast<unsigned long long>(a.tokens) * H * d;
+    const unsigned long long weights =
+        options->per_channel ? static_cast<unsigned long long>(H) * d : d;
+    const unsigned long long reach = static_cast<unsigned long long>(
+        (B - 1) * layout->dx_sb + (T - 1) * layout->dx_st + (H - 1) * layout->dx_sh + d);
+    Span in[4];
+    inputs_of(in, a, B, T, *layout, size);
+    const Span up = span_of(dy, n, size);
+    const Span outs[4] = {span_of(grad_x, reach, size), span_of(grad_gate, n, size),
+                          span_of(grad_weight, weights, 4), span_of(grad_bias, weights, 4)};
+    for (int i = 0; i < 4; ++i) {
+        if (meets_any(outs[i], in) || meet(outs[i], up)) return GLA_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (meet(outs[i], outs[j])) return GLA_ERR_ARG;
     }
     int sms = 0;
     st = usable_device(&sms);

@@ -87,6 +87,7 @@ def test_norm_gradients_are_central_differences(norm, act, gated):
 # ---------------------------------------------------------------- refusals of the C calls
 
 P = 0x100000     # a fake address: the checks never look behind it
+Q, R, S4 = P << 12, P << 13, P << 14     # others far from it, for outputs
 ARG, SHAPE, SCRATCH, DEVICE = (_lib.GLA_ERR_ARG, _lib.GLA_ERR_SHAPE, _lib.GLA_ERR_SCRATCH,
                                _lib.GLA_ERR_DEVICE)
 OK_HERE = (_lib.GLA_ERR_DEVICE,) if not torch.cuda.is_available() else ()
@@ -98,14 +99,14 @@ def _layout(**kw):
     return ctypes.byref(_lib.GlaHeadgateLayout(**lay))
 
 
-def _prompt(lib, *, q=P, k=P, v=P, a=P, h0=None, o=P, hT=None, cu=(0, 5, 16), N=2, T=16, Hk=4,
+def _prompt(lib, *, q=P, k=P, v=P, a=P, h0=None, o=Q, hT=None, cu=(0, 5, 16), N=2, T=16, Hk=4,
             H=4, dk=64, dv=64, lay=None, scratch=None, size=0):
     c = None if cu is None else (ctypes.c_int * len(cu))(*cu)
     return lib.gla_headgate_fwd_varlen(q, k, v, a, 0.125, h0, o, hT, c, N, T, Hk, H, dk, dv,
                                        lay or _layout(), scratch, size, None)
 
 
-def _step(lib, *, q=P, k=P, v=P, a=P, h=P, slots=None, o=P, B=4, S=4, Hk=4, H=4, dk=64, dv=64,
+def _step(lib, *, q=P, k=P, v=P, a=P, h=R, slots=None, o=Q, B=4, S=4, Hk=4, H=4, dk=64, dv=64,
           lay=None, dtype=_lib.GLA_BF16):
     return lib.gla_headgate_step(q, k, v, a, 0.125, h, slots, o, B, S, Hk, H, dk, dv,
                                  lay or _layout(), dtype, None)
@@ -113,7 +114,8 @@ def _step(lib, *, q=P, k=P, v=P, a=P, h=P, slots=None, o=P, B=4, S=4, Hk=4, H=4,
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(k=None), dict(v=None), dict(a=None),
                                  dict(o=None), dict(q=P + 8), dict(v=P + 2), dict(a=P + 2),
-                                 dict(h0=P + 4), dict(hT=P + 8), dict(cu=None), dict(N=0),
+                                 dict(h0=P + 4), dict(hT=R + 8), dict(hT=P), dict(o=P + 64),
+                                 dict(h0=R, hT=R + 64), dict(h0=Q), dict(hT=Q), dict(cu=None), dict(N=0),
                                  dict(T=-1), dict(cu=(1, 5, 16)), dict(cu=(0, 5, 15)),
                                  dict(cu=(0, 17, 16)), dict(Hk=0), dict(H=0), dict(Hk=3),
                                  dict(H=65536, Hk=1), dict(T=2 ** 31 - 1),
@@ -130,8 +132,9 @@ def test_headgate_refuses_shapes(lib, dims):
     assert _step(lib, **dims) in (want, SHAPE)
 
 
-@pytest.mark.parametrize("bad", [dict(q=None), dict(h=None), dict(o=None), dict(h=P + 8),
-                                 dict(o=P + 8), dict(slots=P + 4), dict(B=0), dict(S=0),
+@pytest.mark.parametrize("bad", [dict(q=None), dict(h=None), dict(o=None), dict(h=R + 8),
+                                 dict(o=Q + 8), dict(h=P), dict(o=P), dict(o=R), dict(slots=R),
+                                 dict(slots=Q), dict(slots=S4 + 4), dict(B=0), dict(S=0),
                                  dict(S=3), dict(dtype=2), dict(Hk=3), dict(H=65540),
                                  dict(lay=_layout(q_sh=4)), dict(lay=_layout(a_sh=-2))])
 def test_step_refuses_arguments(lib, bad):
@@ -142,7 +145,7 @@ def test_valid_calls_reach_the_device_check(lib):
     if not torch.cuda.is_available():
         assert _prompt(lib) == DEVICE
         assert _prompt(lib, lay=_layout(a_st=0), Hk=2, dk=8, dv=256) == DEVICE
-        assert _step(lib) == DEVICE and _step(lib, slots=P, S=1) == DEVICE
+        assert _step(lib) == DEVICE and _step(lib, slots=S4, S=1) == DEVICE
         assert _norm(lib) == DEVICE and _norm(lib, gate=None) == DEVICE
         assert _norm_bwd(lib) == DEVICE
 
@@ -160,12 +163,12 @@ def _norm_op(**kw):
     return ctypes.byref(_lib.GlaNormActOptions(**op))
 
 
-def _norm(lib, *, x=P, gate=P, w=P, b=None, y=P, B=2, T=3, H=8, d=64, lay=None, op=None):
+def _norm(lib, *, x=P, gate=P, w=P, b=None, y=Q, B=2, T=3, H=8, d=64, lay=None, op=None):
     return lib.gla_group_norm_act_fwd(x, gate, w, b, y, B, T, H, d, lay or _norm_lay(),
                                       op or _norm_op(), None)
 
 
-def _norm_bwd(lib, *, x=P, gate=P, w=P, b=None, dy=P, dx=P, dg=P, dw=P, db=None, B=2, T=3, H=8,
+def _norm_bwd(lib, *, x=P, gate=P, w=P, b=None, dy=P, dx=Q, dg=R, dw=S4, db=None, B=2, T=3, H=8,
               d=64, lay=None, op=None, scratch=P, size=1 << 30):
     return lib.gla_group_norm_act_bwd(x, gate, w, b, dy, dx, dg, dw, db, B, T, H, d,
                                       lay or _norm_lay(), op or _norm_op(), scratch, size, None)
@@ -180,14 +183,16 @@ NORM_BAD = [dict(x=None), dict(x=P + 8), dict(gate=P + 2), dict(w=P + 4), dict(b
             dict(op=_norm_op(eps=float("nan")))]
 
 
-@pytest.mark.parametrize("bad", NORM_BAD + [dict(y=None), dict(y=P + 4)])
+@pytest.mark.parametrize("bad", NORM_BAD + [dict(y=None), dict(y=Q + 4), dict(y=P + 16)])
 def test_norm_refuses_arguments(lib, bad):
     assert _norm(lib, **bad) == ARG
 
 
-@pytest.mark.parametrize("bad", NORM_BAD + [dict(dy=None), dict(dx=None), dict(dx=P + 8),
+@pytest.mark.parametrize("bad", NORM_BAD + [dict(dy=None), dict(dx=None), dict(dx=Q + 8),
                                             dict(dg=None), dict(gate=None), dict(w=None),
-                                            dict(db=P), dict(scratch=None),
+                                            dict(db=P), dict(scratch=None), dict(dx=P),
+                                            dict(dg=Q), dict(dw=Q + 64), dict(dw=P),
+                                            dict(b=P, db=S4),
                                             dict(lay=_norm_lay(dx_st=12))])
 def test_norm_backward_refuses_arguments(lib, bad):
     assert _norm_bwd(lib, **bad) == ARG
