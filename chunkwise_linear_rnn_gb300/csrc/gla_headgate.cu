@@ -17,21 +17,27 @@
 // enters as the sum of three bf16 numbers, which hold all 24 bits of it, and S' is summed in
 // fp32 registers.
 //
-// One block takes 64 columns of v of one head of a sequence (or of a segment of it) and walks
+// One block takes 128 columns of v of one head of a sequence (or of a segment of it) and walks
 // its chunks:
-//   warps 0-3   state: thread i holds row i of S; adds the chunk's sum, writes the bf16 copy; then
-//               the outputs of row i of the chunk
-//   warps 4-7   scores: thread t reads row t of Q K^T, decays and masks it, leaves it in TMEM
-//   warps 8-11  values: thread t writes row t of the decayed V in three parts
+//   warps 0-7   values and state.  Of the decayed V, transposed on its way from shared memory, each
+//               warp writes 32 columns of 64 tokens to TMEM, part by part; of the state, thread
+//               (column, half) holds 64 channels, adds the chunk's sum and writes the bf16 copy
+//   warps 8-11  scores and outputs: thread t reads row t of Q K^T, decays and masks it, leaves it
+//               in TMEM; later it stores row t of the outputs
 //   warp 12     queues the next tiles by TMA
 //   warp 13     sums the chunk's gates
 //   warp 14     issues every product
 // Products of chunk u, in this order, and when they may start:
-//   K^T [V'1 | V'2 | V'3]   the parts are written, the last chunk's sum is read
-//   Q S                     the copy of S is written, the last chunk's outputs are read
-//   P V, onto Q S           the scores are written
-//   Q K^T of chunk u + 1    its tiles are there, chunk u - 1 is done
-// so that every warp has the time of the other products for its part.
+//   V'1^T K            the first part is written, the last chunk's sum is read
+//   Q K^T              chunk u - 1 is done
+//   V'2^T K, V'3^T K   onto the first; their parts are written (two slots take turns)
+//   Q S                the copy of S is written, the last chunk's outputs are read
+//   P V, onto Q S      the scores are written
+//
+// Shared memory's 128 bytes a cycle bound it (the tensor cores' operands, TMA's tiles): 416 KB a
+// chunk with 128 channels and columns, 3,328 cycles, where the products alone take 3,120.  That is
+// why the values' parts are the operand that lies in TMEM, which costs their transposition: with
+// parts in shared memory and 64 columns a block the same work took 7,300 cycles.
 //
 // Long sequences in small numbers are cut into segments: a first launch walks all but the last
 // one from a state of zero (k and v alone), and each segment then starts from the states before
@@ -42,6 +48,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <new>
 #include <vector>
@@ -84,19 +91,18 @@ void headgate_inputs(Span (&in)[4], const void *q, const void *k, const void *v,
 namespace {
 
 constexpr int C = 128;                   // tokens of a chunk
-constexpr int kCols = 64;                // columns of v of a block
-constexpr int kThreads = 480;
+constexpr int kCols = 128;               // columns of v of a block
+constexpr int kThreads = 512;
 constexpr int kItems = 200;              // segments of one launch: their table is a parameter
 constexpr float kFloor = -60.f;          // of R_t
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kBlk = C * 128;       // a tile of 128 rows of 64 bf16
 
 struct Smem {
-    // the loaded tiles of a chunk, twice: Q and K by blocks of 64 channels, V
-    static constexpr uint32_t kQ = 0, kK = 2 * kBlk, kV = 4 * kBlk, kStage = 5 * kBlk;
-    static constexpr uint32_t kW = 2 * kStage;            // the three parts of the decayed V
-    static constexpr uint32_t kS = kW + 3 * kBlk;         // bf16 copy of the state
-    static constexpr uint32_t kGates = kS + kBlk;         // twice
+    // the loaded tiles by blocks of 64 channels or columns: Q, K of two chunks, V of three
+    static constexpr uint32_t kQ = 0, kK = 2 * kBlk, kV = 6 * kBlk, kTile = 2 * kBlk;
+    static constexpr uint32_t kS = 12 * kBlk;            // bf16 copy of the state [column][channel]
+    static constexpr uint32_t kGates = kS + 2 * kBlk;     // twice
     static constexpr uint32_t kBar = kGates + 2 * 1040;
     static constexpr uint32_t kSlot = kBar + 256;
     static constexpr uint32_t kBytes = kSlot + 16;
@@ -113,22 +119,24 @@ struct Gates {
 };
 static_assert(sizeof(Gates) == 1040, "room in Smem");
 
-// Barriers; those of two are taken in turn, chunk u the (u & 1)th.
-constexpr int kFull = 0;       // [2] Q and K loaded
-constexpr int kFullV = 2;      // [2] V loaded
+// Barriers; those of two are taken in turn: chunk u the (u & 1)th, part j = 3 u + i the (j & 1)th.
+constexpr int kFull = 0;       // [2] K loaded
+constexpr int kFullV = 22;     // [3] V loaded; chunk u the (u % 3)th
 constexpr int kDone = 4;       // [2] every product of the chunk done: V free, outputs there
 constexpr int kGFull = 6;      // [2] gates written
 constexpr int kGFree = 8;      // [2] gates read by all
-constexpr int kScore = 10;     // [2] Q K^T done
-constexpr int kP = 12;         // [2] scores written
-constexpr int kParts = 14;     // parts of the decayed V written
-constexpr int kSum = 15;       // the chunk's sum done: K and the parts free
-constexpr int kSumFree = 16;   // the sum read
-constexpr int kCopy = 17;      // copy of the state written
-constexpr int kQS = 18;        // Q S done: Q and the copy free
-constexpr int kOFree = 19;     // outputs read
-constexpr int kDrain = 20;
-constexpr int kBars = 21;
+constexpr int kPart = 10;      // [2] part of the decayed V written
+constexpr int kPartFree = 12;  // [2] its product done
+constexpr int kScore = 14;     // Q K^T done
+constexpr int kP = 15;         // scores written
+constexpr int kSum = 16;       // the chunk's sum done, K free
+constexpr int kSumFree = 17;   // the sum read
+constexpr int kCopy = 18;      // copy of the state written
+constexpr int kQS = 19;        // Q S done: Q and the copy free
+constexpr int kOFree = 20;     // outputs read
+constexpr int kDrain = 21;
+constexpr int kFullQ = 2;      // Q loaded
+constexpr int kBars = 25;
 static_assert(kBars * 8 <= 256, "room in Smem");
 
 // A segment of a sequence.
@@ -154,9 +162,9 @@ struct Args {
     Item items[kItems];
 };
 
-// TMEM columns: two buffers of scores (Q K^T in fp32, the decayed scores over it), the chunk's
-// sum in its three parts, the outputs.
-constexpr uint32_t kTScore = 0, kTSum = 256, kTOut = 448;
+// TMEM columns: the scores (Q K^T in fp32, the decayed scores over it), two slots for parts of V',
+// the chunk's sum, the outputs.
+constexpr uint32_t kTScore = 0, kTPart = 128, kTSum = 256, kTOut = 384;
 
 // Four consecutive tokens' gates of a chunk of n tokens, by lane.
 __device__ __forceinline__ void load_gates(const Args &p, long long row, int n, int h, float (&g)[4]) {
@@ -235,25 +243,46 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t narrow(Pair p) {
     const float2 v = both(p);
     return pack_bf16x2(v.x, v.y);
 }
 __device__ __forceinline__ Pair widen(uint32_t w) { return pair_of(w << 16, w & 0xffff0000u); }
 
-// A pair of values as three pairs of bf16 numbers that add up to it.
-__device__ __forceinline__ void split3(Pair x, uint32_t (&part)[3]) {
-    const Pair minus = pair_of(-1.f, -1.f);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        part[i] = narrow(x);
-        if (i < 2) x = fma2(widen(part[i]), minus, x);
-    }
+// What is left of a pair of values after a pair of bf16 numbers.
+__device__ __forceinline__ Pair left_of(Pair x, uint32_t part) {
+    return fma2(widen(part), pair_of(-1.f, -1.f), x);
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l gets row l / 4 of each, columns
+// 2 (l % 4) and one more.
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+// 16 lanes of TMEM from the one in taddr, 32 columns: registers 2 k and 2 k + 1 are such matrices
+// of columns 4 k to 4 k + 3, lanes 0-7 and 8-15.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Registers of a thread from here on; a group of four warps together.  The block was launched with
+// 128 for each of 512 threads: 2 x 168 + 112 + 64 a group of four.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Where 16 bytes of row `row` of a tile lie: column group c8 of 8.
@@ -281,27 +310,21 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the same in a warp, to the compiler too
     const int nch = (it.rows + C - 1) / C;
     const int kblocks = dk > 64 ? 2 : 1, ksteps = (dk + 15) / 16;
+    const int cblocks = p.dv - c0 > 64 ? 2 : 1;
     const uint32_t a0 = smem_u32(sm);
     unsigned int *status = p.status;
 
     if (warp == 0) tmem_alloc(slot, 512);
     if (tid == 32) {
         for (int i = 0; i < kBars; ++i) {
-            const bool by_warps = i == kP || i == kP + 1 || i == kParts || i == kSumFree ||
-                                  i == kCopy || i == kOFree;
-            const bool by_all = i == kGFree || i == kGFree + 1;
-            mbar_init(&bar[i], by_all ? (STATE ? 8 : 12) : by_warps ? 4 : 1);
+            int count = 1;
+            if (i == kGFree || i == kGFree + 1) count = STATE ? 8 : 12;
+            if (i == kPart || i == kPart + 1 || i == kSumFree || i == kCopy) count = 8;
+            if (i == kP || i == kOFree) count = 4;
+            mbar_init(&bar[i], count);
         }
         fence_mbar_init();
     }
-    // channels past the first block: rows of the state that stay 0
-    if (kblocks == 1)
-        for (uint32_t i = tid * 16; i < kBlk; i += kThreads * 16)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                *reinterpret_cast<uint4 *>(sm + s * Smem::kStage + Smem::kK + kBlk + i) =
-                    make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -316,161 +339,216 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
         return __all_sync(0xffffffffu,
                           mbar_wait_bounded(&bar[b], static_cast<uint32_t>(u) & 1u, status));
     };
+    auto wait3 = [&](int b, int u) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(&bar[b + u % 3],
+                                                         static_cast<uint32_t>(u / 3) & 1u, status));
+    };
     auto arrive = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar[b]);
     };
 
-    if (warp < 4) {
-        // ================================================================ state
-        const int i = tid;
-        Pair S[kCols / 2];
+    if (warp < 8) {
+        // ================================================================ values and state
+        registers_up<168>();
+        const int half = warp >> 2, c = 32 * (warp & 3) + lane;   // of the state: channels, column
+        const bool mine = c0 + c < p.dv;
+        Pair S[32];
         auto clear = [&]() {
 #pragma unroll
-            for (int c = 0; c < kCols / 2; ++c) S[c] = 0;
+            for (int i = 0; i < 32; ++i) S[i] = 0;
         };
         clear();
-        auto state_row = [&](long long entry) {   // of [.][H][dk][dv]
-            return ((entry * p.H + h) * dk + i) * p.dv + c0;
+        const int rows = min(64, dk - 64 * half);                 // channels there are
+        auto state_at = [&](long long entry) {                    // of [.][H][dk][dv]
+            return ((entry * p.H + h) * dk + 64 * half) * p.dv + c0 + c;
         };
-        auto add_row = [&](const float *from, float a) {
-            if (i >= dk) return;
+        auto add_state = [&](const float *from, float a) {
             const Pair aa = pair_of(a, a);
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4)
-                if (c0 + c < p.dv) {
-                    const float4 x = *reinterpret_cast<const float4 *>(from + c);
-                    S[c / 2] = fma2(aa, S[c / 2], pair_of(x.x, x.y));
-                    S[c / 2 + 1] = fma2(aa, S[c / 2 + 1], pair_of(x.z, x.w));
-                }
-        };
-        auto put_row = [&](float *to) {
-            if (i >= dk) return;
+            for (int i = 0; i < 64; i += 32) {
+                float x[32];   // all on their way before the first is added
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4)
-                if (c0 + c < p.dv) {
-                    const float2 x = both(S[c / 2]), y = both(S[c / 2 + 1]);
-                    *reinterpret_cast<float4 *>(to + c) = make_float4(x.x, x.y, y.x, y.y);
+                for (int j = 0; j < 32; ++j)
+                    x[j] = mine && i + j < rows ? __ldcg(from + static_cast<long long>(i + j) * p.dv) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; j += 2)
+                    S[(i + j) / 2] = fma2(aa, S[(i + j) / 2], pair_of(x[j], x[j + 1]));
+            }
+        };
+        auto put_state = [&](float *to) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 2)
+                if (mine && i < rows) {
+                    const float2 x = both(S[i / 2]);
+                    to[static_cast<long long>(i) * p.dv] = x.x;
+                    to[static_cast<long long>(i + 1) * p.dv] = x.y;
                 }
         };
         auto put_copy = [&]() {
 #pragma unroll
-            for (int c = 0; c < kCols / 8; ++c)
-                *reinterpret_cast<uint4 *>(sm + Smem::kS + at_tile(i, c)) =
-                    make_uint4(narrow(S[4 * c]), narrow(S[4 * c + 1]), narrow(S[4 * c + 2]),
-                               narrow(S[4 * c + 3]));
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(sm + Smem::kS + half * kBlk + at_tile(c, i)) =
+                    make_uint4(narrow(S[4 * i]), narrow(S[4 * i + 1]), narrow(S[4 * i + 2]),
+                               narrow(S[4 * i + 3]));
             fence_proxy_async_smem();
             arrive(kCopy);
+        };
+        // this warp's 32 columns of 64 tokens of the decayed V: what the parts so far leave of them
+        Pair left[2][16];
+        float decay = 0.f, total = 0.f;
+        const uint32_t part_lanes = tmem + lanes + kTPart + 32 * half;
+        // writes part i of chunk u from registers, 16 columns at a time
+        auto put_part = [&](int u, int i, int cols, const uint32_t(&out)[16]) {
+            tmem_st_16x32(part_lanes + (static_cast<uint32_t>(16 * cols) << 16) + ((3 * u + i) & 1) * 64,
+                          out);
+        };
+        auto part_done = [&](int u, int i) {
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(kPart + ((3 * u + i) & 1));
+        };
+        auto part_free = [&](int u, int i) {
+            const int j = 3 * u + i;
+            return j < 2 || wait2(kPartFree, j - 2);
+        };
+        auto first_part = [&](int u) {
+            const bool cut = it.rows - u * C < C;
+            if (!(wait3(kFullV, u) && (!cut || wait2(kFull, u)) && wait2(kGFull, u) && part_free(u, 0)))
+                return false;
+            tc_fence_after();
+            uint8_t *k_tile = sm + Smem::kK + (u & 1) * Smem::kTile;
+            uint8_t *v_tile = sm + Smem::kV + u % 3 * Smem::kTile;
+            if (cut) {
+                // the next sequence's rows, which may hold anything: no part of any product
+                // (each warp its own part of V, and as much of K)
+                for (int i = lane; i < 256; i += 32) {
+                    const int t = 64 * half + (i >> 2);
+                    const uint32_t at = ((warp & 3) >> 1) * kBlk + at_tile(t, 4 * (warp & 1) + (i & 3));
+                    if (u * C + t >= it.rows) {
+                        *reinterpret_cast<uint4 *>(k_tile + at) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(v_tile + at) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const Gates &g = gates[u & 1];
+            decay = g.all;
+            if (STATE) total += g.total;
+            Pair w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 x =
+                    *reinterpret_cast<const float2 *>(g.w + 64 * half + 8 * k + 2 * (lane & 3));
+                w[k] = pair_of(x.x, x.y);
+            }
+            arrive(kGFree + (u & 1));
+            // lanes 0-7 point at 8 tokens of 8 columns, 8-15 at the next columns', 16-31 at the
+            // next tokens'
+            const int q = warp & 3, t = 64 * half + (lane >> 4) * 8 + (lane & 7);
+            const uint32_t from = smem_u32(v_tile) + (q >> 1) * kBlk + t * 128;
+#pragma unroll
+            for (int cols = 0; cols < 2; ++cols) {
+                const int group = (4 * (q & 1) + 2 * cols + ((lane >> 3) & 1)) ^ (t & 7);
+                uint32_t out[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[4];
+                    load_transposed(from + k * 2048 + (group << 4), v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const Pair x = mul2(w[2 * k + j / 2], widen(v[j]));
+                        out[4 * k + j] = narrow(x);
+                        left[cols][4 * k + j] = left_of(x, out[4 * k + j]);
+                    }
+                }
+                put_part(u, 0, cols, out);
+            }
+            part_done(u, 0);
+            return true;
+        };
+        auto next_part = [&](int u, int i) {
+            if (!part_free(u, i)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int cols = 0; cols < 2; ++cols) {
+                uint32_t out[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    out[k] = narrow(left[cols][k]);
+                    left[cols][k] = left_of(left[cols][k], out[k]);
+                }
+                put_part(u, i, cols, out);
+            }
+            part_done(u, i);
+            return true;
         };
         if (STATE) {
             // h0 is kept for the second launch, whose blocks may write hT over it
             if (it.seg == 0 && p.h0) {
-                add_row(p.h0 + state_row(it.n), 0.f);
-                put_row(p.seg_state + state_row(it.slot + it.parts - 1));
+                add_state(p.h0 + state_at(it.n), 0.f);
+                put_state(p.seg_state + state_at(it.slot + it.parts - 1));
                 clear();
             }
         } else {
             if (p.h0)
-                add_row(it.parts > 1 ? p.seg_state + state_row(it.slot + it.parts - 1)
-                                     : p.h0 + state_row(it.n), 0.f);
+                add_state(it.parts > 1 ? p.seg_state + state_at(it.slot + it.parts - 1)
+                                       : p.h0 + state_at(it.n), 0.f);
             for (int m = 0; m < it.seg; ++m)
-                add_row(p.seg_state + state_row(it.slot + m),
-                        exp_centred(p.seg_log[static_cast<long long>(it.slot + m) * p.H + h]));
+                add_state(p.seg_state + state_at(it.slot + m),
+                          exp_centred(p.seg_log[static_cast<long long>(it.slot + m) * p.H + h]));
             if (nch > 0) put_copy();
         }
-        float total = 0.f;
-        bool ok = true;
+        bool ok = nch == 0 || first_part(0);
 #pragma unroll 1
-        for (int u = 0; u < nch; ++u) {
-            if (!(ok = wait2(kGFull, u))) break;
-            const Gates &g = gates[u & 1];
-            const Pair a = pair_of(g.all, g.all);
-            const float f =
-                STATE ? 0.f : p.scale * (g.deep ? ex2f(fmaxf(-g.e[i], kFloor)) : 1.f / g.e[i]);
-            const Pair ff = pair_of(f, f);
-            if (STATE) total += g.total;
-            arrive(kGFree + (u & 1));
+        for (int u = 0; ok && u < nch; ++u) {
+            const Pair a = pair_of(decay, decay);
+#pragma unroll 1
+            for (int i = 1; ok && i < 3; ++i) ok = next_part(u, i);
+            if (!ok || (u + 1 < nch && !(ok = first_part(u + 1)))) break;
             if (!(ok = wait1(kSum, u))) break;
             tc_fence_after();
-            // the next 8 columns are on their way while these are added
-            uint32_t x[2][3][8];
-            auto fetch = [&](int c) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    tmem_ld8(tmem + lanes + kTSum + i * kCols + c, x[c / 8 & 1][i]);
-            };
-            fetch(0);
-#pragma unroll
-            for (int c = 0; c < kCols; c += 8) {
+            for (int i = 0; i < 64; i += 32) {
+                uint32_t x[32];
+                tmem_ld32(tmem + lanes + kTSum + 64 * half + i, x);
                 tmem_wait_ld();
-                if (c + 8 < kCols) fetch(c + 8);
-                const uint32_t(&now)[3][8] = x[c / 8 & 1];
 #pragma unroll
-                for (int j = 0; j < 8; j += 2)
-                    S[(c + j) / 2] = fma2(a, S[(c + j) / 2],
-                                          add2(pair_of(now[0][j], now[0][j + 1]),
-                                               add2(pair_of(now[1][j], now[1][j + 1]),
-                                                    pair_of(now[2][j], now[2][j + 1]))));
+                for (int j = 0; j < 32; j += 2)
+                    S[(i + j) / 2] = fma2(a, S[(i + j) / 2], pair_of(x[j], x[j + 1]));
             }
             tc_fence_before();
             arrive(kSumFree);
-            if (STATE) continue;
-            if (u + 1 < nch) {
+            if (!STATE && u + 1 < nch) {
                 if (!(ok = wait1(kQS, u))) break;
                 put_copy();
-            }
-            // the outputs of row t = i
-            const int left = u * C + i < it.rows ? p.dv - c0 : 0;
-            __nv_bfloat16 *to =
-                p.o + (static_cast<long long>(it.row + u * C + i) * p.H + h) * p.dv + c0;
-            if (!(ok = wait2(kDone, u))) break;
-            tc_fence_after();
-            uint32_t r[2][16];
-            tmem_ld16(tmem + lanes + kTOut, r[0]);
-#pragma unroll
-            for (int c = 0; c < kCols; c += 16) {
-                tmem_wait_ld();
-                if (c + 16 < kCols) {
-                    tmem_ld16(tmem + lanes + kTOut + c + 16, r[c / 16 + 1 & 1]);
-                } else {
-                    tc_fence_before();
-                    arrive(kOFree);
-                }
-                uint32_t v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = narrow(mul2(ff, pair_of(r[c / 16 & 1][2 * j], r[c / 16 & 1][2 * j + 1])));
-                if (p.wide_store) {
-                    if (c < left) store32(to + c, v);
-                } else {
-                    if (c < left)
-                        *reinterpret_cast<uint4 *>(to + c) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (c + 8 < left)
-                        *reinterpret_cast<uint4 *>(to + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-                }
             }
         }
         if (ok) {
             if (STATE) {
-                put_row(p.seg_state + state_row(it.slot + it.seg));
+                put_state(p.seg_state + state_at(it.slot + it.seg));
                 if (tid == 0 && tile == 0)
                     p.seg_log[static_cast<long long>(it.slot + it.seg) * p.H + h] = total;
             } else if (p.hT && it.seg == it.parts - 1) {
-                put_row(p.hT + state_row(it.n));
+                put_state(p.hT + state_at(it.n));
             }
         }
-    } else if (warp < 8) {
-        // ================================================================ scores
-        const int w = warp - 4, t = tid - 128;
+    } else if (warp < 12) {
+        // ================================================================ scores and outputs
+        registers_down<112>();
+        const int w = warp & 3, t = 32 * w + lane;
+        const uint32_t at = tmem + lanes + kTScore;
 #pragma unroll 1
         for (int u = 0; !STATE && u < nch; ++u) {
-            if (!(wait2(kGFull, u) && wait2(kScore, u))) break;
+            if (!(wait2(kGFull, u) && wait1(kScore, u))) break;
             tc_fence_after();
             const Gates &g = gates[u & 1];
-            const uint32_t at = tmem + lanes + kTScore + (u & 1) * C;
             const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
             const bool deep = g.deep;
-            const float base = deep ? -g.e[t] - fmaxf(-g.e[t], kFloor) : 0.f;
+            const float own = g.e[t];
+            const float base = deep ? -own - fmaxf(-own, kFloor) : 0.f;
+            const float f = p.scale * (deep ? ex2f(fmaxf(-own, kFloor)) : 1.f / own);
             uint32_t out[16];
             // the tokens of warps before this one's, then its own, then those behind
 #pragma unroll 1
@@ -489,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                 if (!deep) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float4 f = e[j / 4];
-                        out[j / 2] = narrow(mul2(pair_of(r[j], r[j + 1]), pair_of(f.x, f.y)));
-                        out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(f.z, f.w)));
+                        const float4 x = e[j / 4];
+                        out[j / 2] = narrow(mul2(pair_of(r[j], r[j + 1]), pair_of(x.x, x.y)));
+                        out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(x.z, x.w)));
                     }
                 } else {
                     // 2^(base - G_i) of a later token may be infinite: a masked score stays 0
@@ -513,93 +591,96 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             for (int b = w + 1; b < 4; ++b) tmem_st16(at + 16 * b, out);
             tmem_wait_st();
             tc_fence_before();
-            arrive(kP + (u & 1));
+            arrive(kP);
             arrive(kGFree + (u & 1));
-        }
-    } else if (warp < 12) {
-        // ================================================================ values
-        const int t = tid - 256;
+            // the outputs of row t
+            const Pair ff = pair_of(f, f);
+            const int there = u * C + t < it.rows ? p.dv - c0 : 0;
+            __nv_bfloat16 *to =
+                p.o + (static_cast<long long>(it.row + u * C + t) * p.H + h) * p.dv + c0;
+            if (!wait2(kDone, u)) break;
+            tc_fence_after();
 #pragma unroll 1
-        for (int u = 0; u < nch; ++u) {
-            const bool short_chunk = it.rows - u * C < C;   // whose rows of K are cleared too
-            if (!(wait2(kFullV, u) && (!short_chunk || wait2(kFull, u)) && wait2(kGFull, u) &&
-                  (u == 0 || wait1(kSum, u - 1))))
-                break;
-            uint8_t *st = sm + (u & 1) * Smem::kStage;
-            const float w = gates[u & 1].w[t];
-            const Pair f = pair_of(w, w);
-            const bool real = u * C + t < it.rows;
-            // half a row's loads before the first store, which the compiler has to keep in order
-#pragma unroll 1
-            for (int c0 = 0; c0 < kCols / 8; c0 += 4) {
-                uint4 v[4];
+            for (int c = 0; c < 64 * cblocks; c += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + lanes + kTOut + c, r);
+                tmem_wait_ld();
+                if (c + 32 == 64 * cblocks) {
+                    tc_fence_before();
+                    arrive(kOFree);
+                }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint8_t *at = st + Smem::kV + at_tile(t, c0 + c);
-                    v[c] = *reinterpret_cast<const uint4 *>(at);
-                    if (!real) {
-                        // the next sequence's rows, which may hold anything: no part of any product
-                        v[c] = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(at) = v[c];
-                        at += Smem::kK - Smem::kV;
-                        *reinterpret_cast<uint4 *>(at) = v[c];
-                        if (kblocks == 2) *reinterpret_cast<uint4 *>(at + kBlk) = v[c];
+                for (int i = 0; i < 32; i += 16) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = narrow(mul2(ff, pair_of(r[i + 2 * j], r[i + 2 * j + 1])));
+                    if (p.wide_store) {
+                        if (c + i < there) store32(to + c + i, v);
+                    } else {
+                        if (c + i < there)
+                            *reinterpret_cast<uint4 *>(to + c + i) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        if (c + i + 8 < there)
+                            *reinterpret_cast<uint4 *>(to + c + i + 8) =
+                                make_uint4(v[4], v[5], v[6], v[7]);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t part[4][3];
-                    split3(mul2(f, widen(v[c].x)), part[0]);
-                    split3(mul2(f, widen(v[c].y)), part[1]);
-                    split3(mul2(f, widen(v[c].z)), part[2]);
-                    split3(mul2(f, widen(v[c].w)), part[3]);
-                    uint8_t *to = sm + Smem::kW + at_tile(t, c0 + c);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        *reinterpret_cast<uint4 *>(to + i * kBlk) =
-                            make_uint4(part[0][i], part[1][i], part[2][i], part[3][i]);
-                }
             }
-            fence_proxy_async_smem();
-            arrive(kParts);
-            arrive(kGFree + (u & 1));
         }
     } else if (warp == 12) {
         // ================================================================ loads
-        int loads = 0;
+        registers_down<64>();
+        int ks = 0, qs = 0, vs = 0;   // loads queued
         auto load_k = [&](int u) {
             uint64_t *full = &bar[kFull + (u & 1)];
-            warp_expect_tx(full, kblocks * (STATE ? 1 : 2) * kBlk);
+            warp_expect_tx(full, kblocks * kBlk);
             for (int b = 0; b < kblocks; ++b)
-                warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kK + b * kBlk, &p.tk, full,
+                warp_tma_load_3d(sm + Smem::kK + (u & 1) * Smem::kTile + b * kBlk, &p.tk, full,
                                  b * 64, hk * p.k_step, it.row + u * C);
-            loads = u + 1;
+            ks = u + 1;
         };
         auto load_q = [&](int u) {
-            for (int b = 0; !STATE && b < kblocks; ++b)
-                warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kQ + b * kBlk, &p.tq,
-                                 &bar[kFull + (u & 1)], b * 64, hk * p.q_step, it.row + u * C);
+            if (STATE) return;
+            warp_expect_tx(&bar[kFullQ], kblocks * kBlk);
+            for (int b = 0; b < kblocks; ++b)
+                warp_tma_load_3d(sm + Smem::kQ + b * kBlk, &p.tq, &bar[kFullQ], b * 64,
+                                 hk * p.q_step, it.row + u * C);
+            qs = u + 1;
         };
         auto load_v = [&](int u) {
-            uint64_t *full = &bar[kFullV + (u & 1)];
-            warp_expect_tx(full, kBlk);
-            warp_tma_load_3d(sm + (u & 1) * Smem::kStage + Smem::kV, &p.tv, full, c0,
-                             h * p.v_step, it.row + u * C);
+            uint64_t *full = &bar[kFullV + u % 3];
+            warp_expect_tx(full, cblocks * kBlk);
+            for (int b = 0; b < cblocks; ++b)
+                warp_tma_load_3d(sm + Smem::kV + u % 3 * Smem::kTile + b * kBlk, &p.tv, full,
+                                 c0 + b * 64, h * p.v_step, it.row + u * C);
+            vs = u + 1;
         };
+        // the first chunks' tiles, then each as soon as the last product of the tile before it in
+        // its place is done
+        if (nch > 0) load_k(0), load_q(0), load_v(0);
+        if (nch > 1) load_k(1), load_v(1);
+        if (nch > 2) load_v(2);
 #pragma unroll 1
-        for (int u = 0; u < nch; ++u) {
-            // each tile as soon as its last product of chunk u - 2 is done
-            if (u >= 2 && !wait1(kSum, u - 2)) break;
-            load_k(u);
-            if (!STATE && u >= 2 && !wait1(kQS, u - 2)) break;
-            load_q(u);
-            if (u >= 2 && !wait2(kDone, u - 2)) break;
-            load_v(u);
+        for (int u = 0; u + 1 < nch; ++u) {
+            if (!STATE && !wait1(kQS, u)) break;
+            load_q(u + 1);
+            if (u + 2 < nch) {
+                if (!wait1(kSum, u)) break;
+                load_k(u + 2);
+            }
+            if (u + 3 < nch) {
+                if (!wait2(kDone, u)) break;
+                load_v(u + 3);
+            }
         }
         // loads that an expired wait left under way land before the block gives up its memory
-        for (int u = max(0, loads - 2); u < loads; ++u) wait2(kFull, u), wait2(kFullV, u);
+        for (int u = max(0, ks - 2); u < ks; ++u) wait2(kFull, u);
+        for (int u = max(0, vs - 3); u < vs; ++u) wait3(kFullV, u);
+        if (qs > 0) wait1(kFullQ, qs - 1);
     } else if (warp == 13) {
         // ================================================================ gates
+        registers_down<64>();
         float g[4], next[4];
         if (nch > 0) load_gates(p, it.row, min(C, it.rows), h, next);
 #pragma unroll 1
@@ -612,73 +693,79 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             write_gates<STATE>(g, gates[u & 1]);
             arrive(kGFull + (u & 1));
         }
-    } else {
+    } else if (warp == 14) {
         // ================================================================ products
+        registers_down<64>();
         // a step of 16 of the common dimension, in descriptors: 16 rows of a tile whose rows are
         // that dimension, 32 bytes of a row (and on to the next tile of 64 after four) otherwise
         constexpr uint64_t kRows = 2048 >> 4, kBytes32 = 32 >> 4, kNext = (kBlk - 96) >> 4;
-        auto scores = [&](int u) {
-            constexpr uint32_t id = idesc_bf16(C, C, false, false);   // Q [t][c], K [i][c]
-            const uint32_t st = a0 + (u & 1) * Smem::kStage;
-            uint64_t q = sw128_desc(st + Smem::kQ, 16, 1024), k = sw128_desc(st + Smem::kK, 16, 1024);
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < ksteps; ++i) {
-                warp_mma_bf16_ss(tmem + kTScore + (u & 1) * C, q, k, id, i > 0);
-                const uint64_t on = (i & 3) == 3 ? kNext : kBytes32;
-                q += on;
-                k += on;
-            }
-            warp_mma_commit(&bar[kScore + (u & 1)]);
-        };
-        if (!STATE && nch > 0 && wait2(kFull, 0)) scores(0);
+        // [columns][tokens] by K [tokens][channels]; Q [t][c] by K [i][c]; by S [columns][c]; scores
+        // by V [tokens][columns]
+        const uint32_t id_sum = idesc_bf16(128, 64 * kblocks, false, true);
+        const uint32_t id_score = idesc_bf16(C, C, false, false);
+        const uint32_t id_qs = idesc_bf16(C, 64 * cblocks, false, false);
+        const uint32_t id_pv = idesc_bf16(C, 64 * cblocks, false, true);
 #pragma unroll 1
         for (int u = 0; u < nch; ++u) {
-            const uint32_t st = a0 + (u & 1) * Smem::kStage;
-            if (!(wait2(kFull, u) && wait1(kParts, u) && (u == 0 || wait1(kSumFree, u - 1)))) break;
-            tc_fence_after();
-            // K^T [c][t] by the parts [t][3 x 64]
-            constexpr uint32_t id_sum = idesc_bf16(128, 3 * kCols, true, true);
-            uint64_t x = sw128_desc(st + Smem::kK, kBlk, 1024);
-            uint64_t y = sw128_desc(a0 + Smem::kW, kBlk, 1024);
+            const uint32_t k_tile = a0 + Smem::kK + (u & 1) * Smem::kTile;
+            bool ok = wait2(kFull, u) && (u == 0 || wait1(kSumFree, u - 1));
 #pragma unroll 1
-            for (int i = 0; i < C / 16; ++i, x += kRows, y += kRows)
-                warp_mma_bf16_ss(tmem + kTSum, x, y, id_sum, i > 0);
+            for (int part = 0; ok && part < 3; ++part) {
+                const int j = 3 * u + part;
+                if (!(ok = wait2(kPart, j))) break;
+                tc_fence_after();
+                uint64_t k = sw128_desc(k_tile, kBlk, 1024);
+                uint32_t v = tmem + kTPart + (j & 1) * 64;
+#pragma unroll 1
+                for (int i = 0; i < C / 16; ++i, k += kRows, v += 8)
+                    warp_mma_bf16_ts(tmem + kTSum, v, k, id_sum, part + i > 0);
+                warp_mma_commit(&bar[kPartFree + (j & 1)]);
+                if (part > 0 || STATE) continue;
+                // the scores of chunk u - 1 lay where these go
+                if (!(ok = wait1(kFullQ, u) && (u == 0 || wait2(kDone, u - 1)))) break;
+                tc_fence_after();
+                uint64_t q = sw128_desc(a0 + Smem::kQ, 16, 1024);
+                k = sw128_desc(k_tile, 16, 1024);
+#pragma unroll 1
+                for (int i = 0; i < ksteps; ++i) {
+                    warp_mma_bf16_ss(tmem + kTScore, q, k, id_score, i > 0);
+                    const uint64_t on = (i & 3) == 3 ? kNext : kBytes32;
+                    q += on;
+                    k += on;
+                }
+                warp_mma_commit(&bar[kScore]);
+                if (!(ok = wait1(kCopy, u) && (u == 0 || wait1(kOFree, u - 1)))) break;
+                tc_fence_after();
+                q = sw128_desc(a0 + Smem::kQ, 16, 1024);
+                k = sw128_desc(a0 + Smem::kS, 16, 1024);
+#pragma unroll 1
+                for (int i = 0; i < ksteps; ++i) {
+                    warp_mma_bf16_ss(tmem + kTOut, q, k, id_qs, i > 0);
+                    const uint64_t on = (i & 3) == 3 ? kNext : kBytes32;
+                    q += on;
+                    k += on;
+                }
+                warp_mma_commit(&bar[kQS]);
+            }
+            if (!ok) break;
             warp_mma_commit(&bar[kSum]);
             if (STATE) {
                 warp_mma_commit(&bar[kDone + (u & 1)]);
                 continue;
             }
-            if (!(wait1(kCopy, u) && (u == 0 || wait1(kOFree, u - 1)))) break;
+            if (!wait1(kP, u)) break;
             tc_fence_after();
-            // Q [t][c] by S [c][64]
-            constexpr uint32_t id_out = idesc_bf16(C, kCols, false, true);
-            x = sw128_desc(st + Smem::kQ, 16, 1024);
-            y = sw128_desc(a0 + Smem::kS, kBlk, 1024);
+            uint64_t y = sw128_desc(a0 + Smem::kV + u % 3 * Smem::kTile, kBlk, 1024);
 #pragma unroll 1
-            for (int i = 0; i < ksteps; ++i, y += kRows) {
-                warp_mma_bf16_ss(tmem + kTOut, x, y, id_out, i > 0);
-                x += (i & 3) == 3 ? kNext : kBytes32;
-            }
-            warp_mma_commit(&bar[kQS]);
-            if (!wait2(kP, u)) break;
-            tc_fence_after();
-            // P [t][i] by V [i][64], onto Q S
-            y = sw128_desc(st + Smem::kV, kBlk, 1024);
-            uint32_t score = tmem + kTScore + (u & 1) * C;
-#pragma unroll 1
-            for (int i = 0; i < C / 16; ++i, y += kRows, score += 8)
-                warp_mma_bf16_ts(tmem + kTOut, score, y, id_out, 1u);
+            for (int i = 0; i < C / 16; ++i, y += kRows)
+                warp_mma_bf16_ts(tmem + kTOut, tmem + kTScore + 8 * i, y, id_pv, 1u);
             warp_mma_commit(&bar[kDone + (u & 1)]);
-            if (u + 1 < nch) {
-                // the scores of chunk u - 1 lay where these go
-                if (!(wait2(kFull, u + 1) && (u == 0 || wait2(kDone, u - 1)))) break;
-                scores(u + 1);
-            }
         }
         // every product ends before TMEM and shared memory are given up
         warp_mma_commit(&bar[kDrain]);
         wait1(kDrain, 0);
+    } else {
+        registers_down<64>();
     }
     __syncwarp();
     tc_fence_before();
@@ -699,14 +786,23 @@ struct Plan {
 int chunks_of(const int *cu, int n) { return (cu[n + 1] - cu[n] + C - 1) / C; }
 int parts_of(int chunks, int most) { return chunks > most ? (chunks + most - 1) / most : 1; }
 
-// The blocks of all heads and column tiles run in rounds on the SMs; a launch takes at least its
-// longest segment, and at least its share of all chunks.  Cutting costs a launch that walks all
-// but the last segments for their sums (kSumCost of a chunk's whole work each) and what it takes
-// to begin.  Of one cut and of 2 to 32 parts for the longest sequence, the one that this says
-// is the quickest.
+// How long a launch takes, in chunks: `items` segments (of at most `longest` chunks, `chunks` in all)
+// for each of `lanes` heads and column tiles, longest first, on the SMs.  Where they are all alike
+// they run in whole rounds; where they are not, the shorter ones fill the last round up.
+double launch_time(long long items, int longest, long long chunks, int lanes, double begin) {
+    constexpr double kSms = 152;
+    const double blocks = static_cast<double>(items) * lanes, most = longest + begin;
+    if (blocks <= kSms) return most;
+    return std::min(std::ceil(blocks / kSms) * most,
+                    (chunks + items * begin) * lanes / kSms + 0.5 * most);
+}
+
+// Cutting costs a launch that walks all but the last segments for their sums (kSumCost of a chunk's
+// whole work each) and what it takes to begin.  Of one cut and of 2 to 32 parts for the longest
+// sequence, the one that launch_time says is the quickest.
 Plan make_plan(const int *cu, int N, int H, int dv) {
-    constexpr double kSms = 152, kSumCost = 0.5, kBegin = 4;
-    const double lanes = static_cast<double>(H) * ((dv + kCols - 1) / kCols) / kSms;
+    constexpr double kSumCost = 0.5, kBegin = 1, kItem = 2, kJoin = 0.2;
+    const int lanes = H * ((dv + kCols - 1) / kCols);
     int longest = 0;
     long long all = 0;
     for (int n = 0; n < N; ++n) {
@@ -714,19 +810,22 @@ Plan make_plan(const int *cu, int N, int H, int dv) {
         all += chunks_of(cu, n);
     }
     Plan best = {INT_MAX, 0};
-    double least = std::max<double>(longest, all * lanes);
+    double least = launch_time(N, longest, all, lanes, kItem);
     for (int k = 2; k <= 32 && k <= longest; ++k) {
         const int most = (longest + k - 1) / k;
-        const double whole = std::max<double>(most, all * lanes);
-        if (whole + kBegin >= least) continue;   // not even with the first launch for nothing
-        long long first = 0, slots = 0;
+        // not even with the first launch for nothing
+        if (std::max<double>(most, all * lanes / 152.) + kBegin >= least) continue;
+        long long items = 0, first_items = 0, first = 0, slots = 0;
         for (int n = 0; n < N; ++n) {
             const int c = chunks_of(cu, n), parts = parts_of(c, most);
+            items += parts;
             if (parts == 1) continue;
+            first_items += parts - 1;
             first += c - c / parts;
             slots += parts;
         }
-        const double cost = whole + kBegin + kSumCost * std::max<double>(most, first * lanes);
+        const double cost = launch_time(items, most, all, lanes, kItem + kJoin * (k - 1)) + kBegin +
+                            kSumCost * launch_time(first_items, most, first, lanes, kItem);
         if (cost < least) {
             least = cost;
             best = {most, slots};
