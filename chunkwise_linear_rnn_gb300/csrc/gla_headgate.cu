@@ -104,7 +104,7 @@ struct Smem {
     static constexpr uint32_t kS = 12 * kBlk;            // bf16 copy of the state [column][channel]
     static constexpr uint32_t kGates = kS + 2 * kBlk;     // twice
     static constexpr uint32_t kBar = kGates + 2 * 1040;
-    static constexpr uint32_t kSlot = kBar + 256;
+    static constexpr uint32_t kSlot = kBar + 288;
     static constexpr uint32_t kBytes = kSlot + 16;
 };
 static_assert(Smem::kBytes <= 227 * 1024, "shared memory of one block");
@@ -119,25 +119,25 @@ struct Gates {
 };
 static_assert(sizeof(Gates) == 1040, "room in Smem");
 
-// Barriers; those of two are taken in turn: chunk u the (u & 1)th, part j = 3 u + i the (j & 1)th.
+// Barriers; those of two are taken in turn: chunk u the (u & 1)th, part j = 3 u + i by slots.
 constexpr int kFull = 0;       // [2] K loaded
-constexpr int kFullV = 22;     // [3] V loaded; chunk u the (u % 3)th
 constexpr int kDone = 4;       // [2] every product of the chunk done: V free, outputs there
 constexpr int kGFull = 6;      // [2] gates written
 constexpr int kGFree = 8;      // [2] gates read by all
-constexpr int kPart = 10;      // [2] part of the decayed V written
-constexpr int kPartFree = 12;  // [2] its product done
-constexpr int kScore = 14;     // Q K^T done
-constexpr int kP = 15;         // scores written
-constexpr int kSum = 16;       // the chunk's sum done, K free
-constexpr int kSumFree = 17;   // the sum read
-constexpr int kCopy = 18;      // copy of the state written
-constexpr int kQS = 19;        // Q S done: Q and the copy free
-constexpr int kOFree = 20;     // outputs read
-constexpr int kDrain = 21;
+constexpr int kScore = 10;     // Q K^T done
+constexpr int kP = 11;         // scores written
+constexpr int kSum = 12;       // [sums] the chunk's sum done, K free
+constexpr int kSumFree = 14;   // [sums] the sum read
+constexpr int kCopy = 16;      // copy of the state written
+constexpr int kQS = 17;        // Q S done: Q and the copy free
+constexpr int kOFree = 18;     // outputs read
+constexpr int kDrain = 19;
+constexpr int kFullV = 22;     // [3] V loaded; chunk u the (u % 3)th
 constexpr int kFullQ = 2;      // Q loaded
-constexpr int kBars = 25;
-static_assert(kBars * 8 <= 256, "room in Smem");
+constexpr int kPart = 25;      // [slots] part of the decayed V written
+constexpr int kPartFree = 29;  // [slots] its product done
+constexpr int kBars = 33;
+static_assert(kBars * 8 <= 288, "room in Smem");
 
 // A segment of a sequence.
 struct Item {
@@ -165,6 +165,15 @@ struct Args {
 // TMEM columns: the scores (Q K^T in fp32, the decayed scores over it), two slots for parts of V',
 // the chunk's sum, the outputs.
 constexpr uint32_t kTScore = 0, kTPart = 128, kTSum = 256, kTOut = 384;
+// The sums alone leave room for four slots and two sums.
+template <bool STATE>
+struct Turns {
+    static constexpr int kSlots = STATE ? 4 : 2, kSums = STATE ? 2 : 1;
+    __device__ __forceinline__ static uint32_t part(int j) {
+        return (STATE ? kTScore : kTPart) + j % kSlots * 64;
+    }
+    __device__ __forceinline__ static uint32_t sum(int u) { return kTSum + u % kSums * 128; }
+};
 
 // Four consecutive tokens' gates of a chunk of n tokens, by lane.
 __device__ __forceinline__ void load_gates(const Args &p, long long row, int n, int h, float (&g)[4]) {
@@ -319,7 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
         for (int i = 0; i < kBars; ++i) {
             int count = 1;
             if (i == kGFree || i == kGFree + 1) count = STATE ? 8 : 12;
-            if (i == kPart || i == kPart + 1 || i == kSumFree || i == kCopy) count = 8;
+            if ((i >= kPart && i < kPart + 4) || i == kSumFree || i == kSumFree + 1 || i == kCopy)
+                count = 8;
             if (i == kP || i == kOFree) count = 4;
             mbar_init(&bar[i], count);
         }
@@ -342,6 +352,17 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     auto wait3 = [&](int b, int u) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(&bar[b + u % 3],
                                                          static_cast<uint32_t>(u / 3) & 1u, status));
+    };
+    using Turn = Turns<STATE>;
+    auto wait_part = [&](int b, int j) {
+        return __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar[b + j % Turn::kSlots],
+                                            static_cast<uint32_t>(j / Turn::kSlots) & 1u, status));
+    };
+    auto wait_sum = [&](int b, int u) {
+        return __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&bar[b + u % Turn::kSums],
+                                            static_cast<uint32_t>(u / Turn::kSums) & 1u, status));
     };
     auto arrive = [&](int b) {
         __syncwarp();
@@ -397,20 +418,20 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
         // this warp's 32 columns of 64 tokens of the decayed V: what the parts so far leave of them
         Pair left[2][16];
         float decay = 0.f, total = 0.f;
-        const uint32_t part_lanes = tmem + lanes + kTPart + 32 * half;
+        const uint32_t part_lanes = tmem + lanes + 32 * half;
         // writes part i of chunk u from registers, 16 columns at a time
         auto put_part = [&](int u, int i, int cols, const uint32_t(&out)[16]) {
-            tmem_st_16x32(part_lanes + (static_cast<uint32_t>(16 * cols) << 16) + ((3 * u + i) & 1) * 64,
+            tmem_st_16x32(part_lanes + (static_cast<uint32_t>(16 * cols) << 16) + Turn::part(3 * u + i),
                           out);
         };
         auto part_done = [&](int u, int i) {
             tmem_wait_st();
             tc_fence_before();
-            arrive(kPart + ((3 * u + i) & 1));
+            arrive(kPart + (3 * u + i) % Turn::kSlots);
         };
         auto part_free = [&](int u, int i) {
             const int j = 3 * u + i;
-            return j < 2 || wait2(kPartFree, j - 2);
+            return j < Turn::kSlots || wait_part(kPartFree, j - Turn::kSlots);
         };
         auto first_part = [&](int u) {
             const bool cut = it.rows - u * C < C;
@@ -507,19 +528,19 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
 #pragma unroll 1
             for (int i = 1; ok && i < 3; ++i) ok = next_part(u, i);
             if (!ok || (u + 1 < nch && !(ok = first_part(u + 1)))) break;
-            if (!(ok = wait1(kSum, u))) break;
+            if (!(ok = wait_sum(kSum, u))) break;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 64; i += 32) {
                 uint32_t x[32];
-                tmem_ld32(tmem + lanes + kTSum + 64 * half + i, x);
+                tmem_ld32(tmem + lanes + Turn::sum(u) + 64 * half + i, x);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     S[(i + j) / 2] = fma2(a, S[(i + j) / 2], pair_of(x[j], x[j + 1]));
             }
             tc_fence_before();
-            arrive(kSumFree);
+            arrive(kSumFree + u % Turn::kSums);
             if (!STATE && u + 1 < nch) {
                 if (!(ok = wait1(kQS, u))) break;
                 put_copy();
@@ -666,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             if (!STATE && !wait1(kQS, u)) break;
             load_q(u + 1);
             if (u + 2 < nch) {
-                if (!wait1(kSum, u)) break;
+                if (!wait_sum(kSum, u)) break;
                 load_k(u + 2);
             }
             if (u + 3 < nch) {
@@ -708,18 +729,18 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
 #pragma unroll 1
         for (int u = 0; u < nch; ++u) {
             const uint32_t k_tile = a0 + Smem::kK + (u & 1) * Smem::kTile;
-            bool ok = wait2(kFull, u) && (u == 0 || wait1(kSumFree, u - 1));
+            bool ok = wait2(kFull, u) && (u < Turn::kSums || wait_sum(kSumFree, u - Turn::kSums));
 #pragma unroll 1
             for (int part = 0; ok && part < 3; ++part) {
                 const int j = 3 * u + part;
-                if (!(ok = wait2(kPart, j))) break;
+                if (!(ok = wait_part(kPart, j))) break;
                 tc_fence_after();
                 uint64_t k = sw128_desc(k_tile, kBlk, 1024);
-                uint32_t v = tmem + kTPart + (j & 1) * 64;
+                uint32_t v = tmem + Turn::part(j);
 #pragma unroll 1
                 for (int i = 0; i < C / 16; ++i, k += kRows, v += 8)
-                    warp_mma_bf16_ts(tmem + kTSum, v, k, id_sum, part + i > 0);
-                warp_mma_commit(&bar[kPartFree + (j & 1)]);
+                    warp_mma_bf16_ts(tmem + Turn::sum(u), v, k, id_sum, part + i > 0);
+                warp_mma_commit(&bar[kPartFree + j % Turn::kSlots]);
                 if (part > 0 || STATE) continue;
                 // the scores of chunk u - 1 lay where these go
                 if (!(ok = wait1(kFullQ, u) && (u == 0 || wait2(kDone, u - 1)))) break;
@@ -748,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                 warp_mma_commit(&bar[kQS]);
             }
             if (!ok) break;
-            warp_mma_commit(&bar[kSum]);
+            warp_mma_commit(&bar[kSum + u % Turn::kSums]);
             if (STATE) {
                 warp_mma_commit(&bar[kDone + (u & 1)]);
                 continue;
