@@ -1127,7 +1127,7 @@ def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
             hT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
             _need(hT, "final_state", torch.float32, state, dev)
-    o = q.new_empty((T, H, dv))
+    o = torch.empty((T, H, dv), dtype=q.dtype, device=dev)
     scratch = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     _call("gla_headgate_fwd_varlen", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           log_alpha.data_ptr(), dk ** -0.5 if scale is None else float(scale), _ptr(h0),
@@ -1160,7 +1160,7 @@ def gla_headgate_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_alp
     elif S < B:
         raise ValueError("h must have a state for each row, or slots be given")
     if out is None:
-        out = q.new_empty((B, H, dv))
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
     else:
         _need(out, "out", q.dtype, (B, H, dv), dev)
     _call("gla_headgate_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -1246,7 +1246,7 @@ def gla_group_norm_act_fwd(x: torch.Tensor, gate: torch.Tensor | None = None,
     shape and type.  d is a multiple of 8 up to 512.
     """
     sizes = _norm_act_sizes(x, gate, weight, bias, None, norm, activation, eps)
-    y = x.new_empty(x.shape)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _call("gla_group_norm_act_fwd", x.device, x.data_ptr(), _ptr(gate), _ptr(weight), _ptr(bias),
           y.data_ptr(), *sizes[:6])
     return y
@@ -1256,9 +1256,11 @@ def _norm_act_bwd(dy, x, gate, weight, bias, options, need_dweight, need_dbias):
     # the gradient of x lies as x does where x has no gaps and no overlaps
     dx = torch.empty_like(x)
     if dx.stride(-1) != 1:
-        dx = x.new_empty(x.shape)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     sizes = _norm_act_sizes(x, gate, weight, bias, dx, *options)
-    dgate = None if gate is None else x.new_empty(x.shape)
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     dw = torch.empty_like(weight) if weight is not None and need_dweight else None
     db = torch.empty_like(bias) if bias is not None and need_dbias else None
     scratch = None
