@@ -30,14 +30,22 @@
 // Products of chunk u, in this order, and when they may start:
 //   V'1^T K            the first part is written, the last chunk's sum is read
 //   Q K^T              chunk u - 1 is done
-//   V'2^T K, V'3^T K   onto the first; their parts are written (two slots take turns)
 //   Q S                the copy of S is written, the last chunk's outputs are read
+//   V'2^T K, V'3^T K   onto the first; their parts are written (two slots take turns)
 //   P V, onto Q S      the scores are written
+// Q S comes early so that one tile of Q is enough, which leaves room for a third one of V.
 //
-// Shared memory's 128 bytes a cycle bound it (the tensor cores' operands, TMA's tiles): 416 KB a
-// chunk with 128 channels and columns, 3,328 cycles, where the products alone take 3,120.  That is
-// why the values' parts are the operand that lies in TMEM, which costs their transposition: with
-// parts in shared memory and 64 columns a block the same work took 7,300 cycles.
+// HBM's floor for 16,384 tokens, 16 heads of 128 and 128 is 40 us (268 MB); measured on one GB300
+// 58 us (0.68), with 128 of 152 SMs in use.  A chunk's products take 3,120 cycles, shared memory's
+// traffic 3,328 (416 KB at 128 bytes a cycle), the warps' instructions about 3,000 issue slots of
+// a scheduler; it takes about 6,000 in all, with none of the three above 45 % (tensor pipe 45 %,
+// L1 and shared memory 44 %, issue slots 40 %): what is left is the chain from warp to warp.
+// Without the values' splitting it would take 12 % less, without the outputs' stores 13 %,
+// without the work on states, scores or copies 2 to 4 % each.
+// Measured beside it, same case: parts of V' in shared memory and 64 columns a block, 78 us;
+// outputs through shared memory and TMA stores, 60; all outputs read before the first store, 67;
+// the next chunk's tiles pulled into L2 ahead of time, 60 to 63; the same products issued by one
+// lane alone (180-240 cycles each), 113 for 94 in the form with 64 columns.
 //
 // Long sequences in small numbers are cut into segments: a first launch walks all but the last
 // one from a state of zero (k and v alone), and each segment then starts from the states before
@@ -819,8 +827,10 @@ double launch_time(long long items, int longest, long long chunks, int lanes, do
 }
 
 // Cutting costs a launch that walks all but the last segments for their sums (kSumCost of a chunk's
-// whole work each) and what it takes to begin.  Of one cut and of 2 to 32 parts for the longest
-// sequence, the one that launch_time says is the quickest.
+// whole work each), and each block what it takes to begin (kItem) and to read the states before it
+// (kJoin each), all in chunks.  Of no cut and of 2 to 32 parts for the longest sequence, the one
+// that launch_time says is the quickest.  Two sequences of 32,768 tokens, 16 heads of 128 and 256:
+// 7 parts 559 us, 732 in one, 587, 605 and 602 in 2, 4 and 9.
 Plan make_plan(const int *cu, int N, int H, int dv) {
     constexpr double kSumCost = 0.5, kBegin = 1, kItem = 2, kJoin = 0.2;
     const int lanes = H * ((dv + kCols - 1) / kCols);

@@ -7,6 +7,8 @@
 // block takes one head's columns (or a tile of them); a thread owns one 16-byte column group of
 // up to 16 rows, all of whose loads are issued before any use.  The sum over the rows runs in
 // registers, over the lanes that share columns by shuffles, and over warps in shared memory.
+// Measured on one GB300: 256 rows of 32 heads of 128 x 128 157 us (6.9 TB/s, a copy's 6.79);
+// 4 rows of 16 heads 3.2 us, which is latency (slot, then state, then the sums).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -154,8 +156,9 @@ int launch_tile(const StepArgs &a, unsigned heads, cudaStream_t stream) {
 
 template <typename E>
 int launch(const StepArgs &a, unsigned heads, int sms, cudaStream_t stream) {
-    // the narrowest tile that holds the columns; few heads take tiles of 32 columns, so that
-    // more SMs have a part of them
+    // The narrowest tile that holds the columns; where heads are fewer than two for each SM, tiles
+    // of 32 columns, so that more SMs have a part of them (4 rows of 16 heads of 128 x 128: 3.2 us,
+    // 3.7 with whole rows; 256 rows of 32 heads: 157 us whole, 167 in tiles of 32).
     if (a.dv <= 32 || heads < 2u * sms) return launch_tile<E, 8>(a, heads, stream);
     if (a.dv <= 64) return launch_tile<E, 16>(a, heads, stream);
     if (a.dv <= 128) return launch_tile<E, 32>(a, heads, stream);

@@ -2,8 +2,10 @@
  * gla.h — C ABI of the GB300 (sm_103a) gated linear attention library: the
  * chunked forward, its backward, and the decode step; and, further down, the
  * gated delta rule, the gated linear recurrence of one value per channel
- * (gla_scan_*), and the norms of q and k with their rotation by position
- * (gla_qk_norm_rope_*).  What follows here is about the first.
+ * (gla_scan_*), the norms of q and k with their rotation by position
+ * (gla_qk_norm_rope_*), the same attention with one gate per head as it is served
+ * (gla_headgate_*), and the norm with activation that follows it
+ * (gla_group_norm_act_*).  What follows here is about the first.
  *
  * The operation (from "Gated Linear Attention (GLA): Mathematical Foundations,
  * Data-Dependent Gating, Chunkwise Parallel Forms, and Sub-Quadratic Sequence
@@ -645,7 +647,7 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
  * infinite or NaN ones included; an infinite or NaN value of a token may show in the
  * outputs of the up to 127 tokens before it, and does in the later ones.  A bounded
  * device wait that expires leaves the outputs unspecified and is reported by
- * gla_last_device_status (GLA_ERR_TIMEOUT).
+ * gla_last_device_status (GLA_ERR_TIMEOUT).  Scores |q_t k_i| have to stay below 2^60.
  */
 typedef struct gla_headgate_layout {
     long long q_st, q_sh;   /* strides of q over token (row of a step) and head */
