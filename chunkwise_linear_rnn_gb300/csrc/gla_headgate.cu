@@ -13,7 +13,7 @@
 // size or less where it should be less still.
 //
 // What is rounded to bf16: the scores and the copy of the state that q multiplies, once for
-// each output, as the output itself is.  The state does not lose anything by it: 2^(G_n - G_i) v_i
+// each output, as the output itself is (scores of batches of one chunk at most: twice as finely).  The state does not lose anything by it: 2^(G_n - G_i) v_i
 // enters as the sum of three bf16 numbers, which hold all 24 bits of it, and S' is summed in
 // fp32 registers.
 //
@@ -314,7 +314,10 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
 }
 
 // STATE: the first launch of divided sequences, whose segments' sums alone are wanted.
-template <bool STATE>
+// FINE: sequences of one chunk at most, where so few scores may make up the outputs that their
+// rounding does not average out: they are taken in two parts, 2^-16 off instead of 2^-8.  (A
+// kernel of its own: as a condition it costs the others 4 %.)
+template <bool STATE, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __grid_constant__ Args p) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Smem::kBar);
@@ -574,15 +577,15 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             tc_fence_after();
             const Gates &g = gates[u & 1];
             const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
-            const bool deep = g.deep;
+            const bool deep = g.deep, plain = !deep && !FINE;
             const float own = g.e[t];
             const float base = deep ? -own - fmaxf(-own, kFloor) : 0.f;
             const float f = p.scale * (deep ? ex2f(fmaxf(-own, kFloor)) : 1.f / own);
-            uint32_t out[16];
-            // the tokens of warps before this one's, then its own, then those behind
+            // the tokens of warps before this one's, then its own, then those behind: 32 scores
+            // become 16 columns, one block behind the other; or, in two parts, 32 in their place
 #pragma unroll 1
             for (int b = 0; b <= w; ++b) {
-                uint32_t r[32];
+                uint32_t r[32], out[16];
                 float4 e[8];
                 tmem_ld32(at + 32 * b, r);
 #pragma unroll
@@ -593,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                     for (int j = 0; j < 32; ++j)
                         if (j > lane) r[j] = 0u;
                 }
-                if (!deep) {
+                if (plain) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const float4 x = e[j / 4];
@@ -601,23 +604,32 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                         out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(x.z, x.w)));
                     }
                 } else {
-                    // 2^(base - G_i) of a later token may be infinite: a masked score stays 0
+                    uint32_t rest[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float f0 = j % 4 ? e[j / 4].z : e[j / 4].x;
-                        const float f1 = j % 4 ? e[j / 4].w : e[j / 4].y;
-                        const int i = 32 * b + j;
-                        out[j / 2] = pack_bf16x2(
-                            i <= t ? __uint_as_float(r[j]) * ex2f(base + f0) : 0.f,
-                            i + 1 <= t ? __uint_as_float(r[j + 1]) * ex2f(base + f1) : 0.f);
+                        float f0 = j % 4 ? e[j / 4].z : e[j / 4].x;
+                        float f1 = j % 4 ? e[j / 4].w : e[j / 4].y;
+                        if (deep) {
+                            // of a later token it may be infinite: a masked score stays 0
+                            f0 = 32 * b + j <= t ? ex2f(base + f0) : 0.f;
+                            f1 = 32 * b + j + 1 <= t ? ex2f(base + f1) : 0.f;
+                        }
+                        const Pair x = mul2(pair_of(r[j], r[j + 1]), pair_of(f0, f1));
+                        out[j / 2] = narrow(x);
+                        if (FINE) rest[j / 2] = narrow(left_of(x, out[j / 2]));
                     }
+                    if (FINE) tmem_st16(at + 32 * b + 16, rest);
                 }
-                tmem_st16(at + 16 * b, out);
+                tmem_st16(at + (FINE ? 32 : 16) * b, out);
             }
+            uint32_t none[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) out[j] = 0u;
+            for (int j = 0; j < 16; ++j) none[j] = 0u;
 #pragma unroll 1
-            for (int b = w + 1; b < 4; ++b) tmem_st16(at + 16 * b, out);
+            for (int b = w + 1; b < 4; ++b) {
+                tmem_st16(at + (FINE ? 32 : 16) * b, none);
+                if (FINE) tmem_st16(at + 32 * b + 16, none);
+            }
             tmem_wait_st();
             tc_fence_before();
             arrive(kP);
@@ -786,8 +798,14 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             tc_fence_after();
             uint64_t y = sw128_desc(a0 + Smem::kV + u % 3 * Smem::kTile, kBlk, 1024);
 #pragma unroll 1
-            for (int i = 0; i < C / 16; ++i, y += kRows)
+            for (int i = 0; !FINE && i < C / 16; ++i, y += kRows)
                 warp_mma_bf16_ts(tmem + kTOut, tmem + kTScore + 8 * i, y, id_pv, 1u);
+#pragma unroll 1
+            for (int i = 0; FINE && i < C / 8; ++i) {
+                // both parts of 16 tokens' scores
+                const uint32_t score = tmem + kTScore + (i >> 2) * 32 + (i & 1) * 16 + (i >> 1 & 1) * 8;
+                warp_mma_bf16_ts(tmem + kTOut, score, y + (i >> 1) * kRows, id_pv, 1u);
+            }
             warp_mma_commit(&bar[kDone + (u & 1)]);
         }
         // every product ends before TMEM and shared memory are given up
@@ -876,14 +894,14 @@ bool bounds_ok(const int *cu, int N, int T) {
     return true;
 }
 
-template <bool STATE>
+template <bool STATE, bool FINE>
 bool prepared() {
     // the attribute belongs to the device's copy of the function
     static std::atomic<bool> done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (done[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(headgate_chunk_kernel<STATE>,
+    if (cudaFuncSetAttribute(headgate_chunk_kernel<STATE, FINE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Smem::kBytes)) != cudaSuccess)
         return false;
@@ -891,15 +909,15 @@ bool prepared() {
     return true;
 }
 
-template <bool STATE>
+template <bool STATE, bool FINE>
 bool launch(Args &a, const std::vector<Item> &items, cudaStream_t stream) {
     if (items.empty()) return true;
-    if (!prepared<STATE>()) return false;
+    if (!prepared<STATE, FINE>()) return false;
     for (size_t first = 0; first < items.size(); first += kItems) {
         const size_t n = std::min<size_t>(kItems, items.size() - first);
         std::copy(items.begin() + first, items.begin() + first + n, a.items);
         const unsigned grid = static_cast<unsigned>(n) * a.H * a.tiles;
-        headgate_chunk_kernel<STATE><<<grid, kThreads, Smem::kBytes, stream>>>(a);
+        headgate_chunk_kernel<STATE, FINE><<<grid, kThreads, Smem::kBytes, stream>>>(a);
         if (cudaGetLastError() != cudaSuccess) return false;
     }
     return true;
@@ -924,7 +942,10 @@ int run(Args &a, const int *cu, int N, const Plan &plan, cudaStream_t stream) {
     auto longer = [](const Item &x, const Item &y) { return x.rows > y.rows; };
     std::stable_sort(whole.begin(), whole.end(), longer);
     std::stable_sort(sums.begin(), sums.end(), longer);
-    return launch<true>(a, sums, stream) && launch<false>(a, whole, stream) ? GLA_OK : GLA_ERR_LAUNCH;
+    const bool ok = sums.empty() && whole[0].rows <= C
+                        ? launch<false, true>(a, whole, stream)
+                        : launch<true, false>(a, sums, stream) && launch<false, false>(a, whole, stream);
+    return ok ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 }  // namespace

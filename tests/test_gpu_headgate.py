@@ -96,6 +96,21 @@ def test_many_short_sequences():
     check(*make(cu[-1], 1, 1, 32, 32), cu, states(700, 1, 32, 32))
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 10, 64, 127, 128])
+@pytest.mark.parametrize("rate", [0.05, 5.0])
+def test_scores_of_short_prompts_are_taken_in_two_parts(T, rate):
+    """Without a state before it a short prompt's outputs are off by their own rounding: scores in
+    two bf16 parts are 2^-16 off (2^-8 for the first of the second) instead of 2^-8."""
+    q, k, v, la = make(3 * T, 2, 4, 64, 72, seed=T, rate=rate)
+    cu = [0, T, 2 * T, 3 * T]
+    o, _ = gla.gla_headgate_fwd_varlen(q, k, v, la, cu, 0.125)
+    qn, kn, vn, ln = (ref.num(t) for t in (q, k, v, la))
+    for a, b in zip(cu, cu[1:]):
+        want = ref.walk(qn[a:b], kn[a:b], vn[a:b], ln[a:b], 0.125)
+        bo, _ = ref.prompt_bounds(T, *want[2:])
+        ref.assert_within(o[a:b], want[0], bo - (2.0 ** -8 - 2.0 ** -16) * want[2], f"T={T}")
+
+
 @pytest.mark.parametrize("T,Hk,H,dk,dv", [(20000, 1, 1, 128, 128), (9000, 1, 2, 64, 256),
                                           (6001, 2, 2, 128, 64), (30000, 1, 1, 16, 16)])
 def test_long_sequences_are_divided(T, Hk, H, dk, dv):
