@@ -64,7 +64,7 @@
 #include "gla.h"
 #include "gla_exp.cuh"
 #include "gla_internal.h"
-#include "gla_ptx.cuh"
+#include "gla_ptx_warp.cuh"
 
 namespace gla {
 

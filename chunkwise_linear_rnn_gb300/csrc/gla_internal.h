@@ -12,6 +12,10 @@
 
 namespace gla {
 
+// A bit of the device status word beside those of gla_ptx.cuh: a decode step met a slot that it
+// refuses.
+constexpr unsigned int kStatusSlot = 2u;
+
 struct ChunkLaunch {
     // 3-D tensor maps (channel, token, batch*head): q, k, log_alpha, v, and o
     // (32-token boxes: each TMEM warp stores its own rows)
