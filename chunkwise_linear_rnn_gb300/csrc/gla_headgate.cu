@@ -13,9 +13,9 @@
 // size or less where it should be less still.
 //
 // What is rounded to bf16: the scores and the copy of the state that q multiplies, once for
-// each output, as the output itself is (scores of batches of one chunk at most: twice as finely).  The state does not lose anything by it: 2^(G_n - G_i) v_i
-// enters as the sum of three bf16 numbers, which hold all 24 bits of it, and S' is summed in
-// fp32 registers.
+// each output, as the output itself is (scores of batches of one chunk at most enter in two
+// parts instead).  The state does not lose anything by it: 2^(G_n - G_i) v_i enters as the sum
+// of three bf16 numbers, which hold all 24 bits of it, and S' is summed in fp32 registers.
 //
 // One block takes 128 columns of v of one head of a sequence (or of a segment of it) and walks
 // its chunks:
@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                 float x[32];   // all on their way before the first is added
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    x[j] = mine && i + j < rows ? __ldcg(from + static_cast<long long>(i + j) * p.dv) : 0.f;
+                    x[j] = mine && i + j < rows ? __ldcg(from + static_cast<long long>(i + j) * p.dv)
+                                                : 0.f;
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     S[(i + j) / 2] = fma2(aa, S[(i + j) / 2], pair_of(x[j], x[j + 1]));
@@ -944,7 +945,8 @@ int run(Args &a, const int *cu, int N, const Plan &plan, cudaStream_t stream) {
     std::stable_sort(sums.begin(), sums.end(), longer);
     const bool ok = sums.empty() && whole[0].rows <= C
                         ? launch<false, true>(a, whole, stream)
-                        : launch<true, false>(a, sums, stream) && launch<false, false>(a, whole, stream);
+                        : launch<true, false>(a, sums, stream) &&
+                              launch<false, false>(a, whole, stream);
     return ok ? GLA_OK : GLA_ERR_LAUNCH;
 }
 

@@ -536,9 +536,13 @@ int bind(NormArgs *a, const void *x, const void *gate, const float *weight, cons
     if (!(op.eps > 0.f && op.eps <= 1.f)) return GLA_ERR_ARG;
     for (long long s : {lay.x_sb, lay.x_st, lay.x_sh, lay.g_sb, lay.g_st, lay.g_sh})
         if (s < 0 || s % 8) return GLA_ERR_ARG;
-    if (backward)
+    if (backward) {
         for (long long s : {lay.dx_sb, lay.dx_st, lay.dx_sh})
             if (s < 0 || s % 8) return GLA_ERR_ARG;
+        // x may be spread out from one row; its gradient is a row for each
+        if ((B > 1 && !lay.dx_sb) || (T > 1 && !lay.dx_st) || (H > 1 && !lay.dx_sh))
+            return GLA_ERR_ARG;
+    }
     if (d % 8 || d > 512) return GLA_ERR_SHAPE;
     const long long tokens = static_cast<long long>(B) * T;
     // token numbers are counted on past the last in 32 bits, channels of all heads in 31

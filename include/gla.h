@@ -721,7 +721,9 @@ int gla_group_norm_act_fwd(const void *x, const void *gate, const float *weight,
  * gla_group_norm_act_bwd — gradients of L = <dy, y>, the norms recomputed from x.  dy is
  * contiguous like y; grad_x is written through its own strides of `layout` (so that it can
  * lie as x does), grad_gate [B, T, H, d] contiguous (NULL with gate NULL); both in
- * dtype.  grad_weight and grad_bias are fp32 like weight and bias, each nullable (not
+ * dtype.  The rows of grad_x may not overlap (GLA_ERR_ARG for a stride of 0 that is
+ * stepped over, as x and gate may have: grad_x then holds a row for each use of theirs).
+ * grad_weight and grad_bias are fp32 like weight and bias, each nullable (not
  * wanted).  With either, `scratch` holds gla_group_norm_act_bwd_scratch(...) bytes of
  * device memory, 16-byte aligned, for their partial sums (GLA_ERR_SCRATCH when
  * scratch_bytes is smaller): a thread adds at most 2^10 rows in 32 bits, everything

@@ -193,7 +193,10 @@ def test_norm_refuses_arguments(lib, bad):
                                             dict(db=P), dict(scratch=None), dict(dx=P),
                                             dict(dg=Q), dict(dw=Q + 64), dict(dw=P),
                                             dict(b=P, db=S4),
-                                            dict(lay=_norm_lay(dx_st=12))])
+                                            dict(lay=_norm_lay(dx_st=12)),
+                                            dict(lay=_norm_lay(dx_sb=0)),
+                                            dict(lay=_norm_lay(dx_st=0)),
+                                            dict(lay=_norm_lay(dx_sh=0))])
 def test_norm_backward_refuses_arguments(lib, bad):
     assert _norm_bwd(lib, **bad) == ARG
 
