@@ -127,14 +127,17 @@ struct Gates {
 };
 static_assert(sizeof(Gates) == 1040, "room in Smem");
 
-// Barriers; those of two are taken in turn: chunk u the (u & 1)th, part j = 3 u + i by slots.
+// Barriers; those of two are taken in turn: chunk u the (u & 1)th, part j = 3 u + i by slots.  A
+// wait names its phase by parity alone, so the next phase of its barrier must need something that
+// comes after the wait.  The loads' wait for a chunk's sum is why kSum has two though there is one
+// sum: the next chunk's needs nothing that they queue behind it, the one after that does.
 constexpr int kFull = 0;       // [2] K loaded
-constexpr int kDone = 4;       // [2] every product of the chunk done: V free, outputs there
+constexpr int kDone = 4;       // [2] outputs there, V free (not for sums alone)
 constexpr int kGFull = 6;      // [2] gates written
 constexpr int kGFree = 8;      // [2] gates read by all
 constexpr int kScore = 10;     // Q K^T done
 constexpr int kP = 11;         // scores written
-constexpr int kSum = 12;       // [sums] the chunk's sum done, K free
+constexpr int kSum = 12;       // [2] the chunk's sum done, K free; for sums alone V too
 constexpr int kSumFree = 14;   // [sums] the sum read
 constexpr int kCopy = 16;      // copy of the state written
 constexpr int kQS = 17;        // Q S done: Q and the copy free
@@ -370,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                           mbar_wait_bounded(&bar[b + j % Turn::kSlots],
                                             static_cast<uint32_t>(j / Turn::kSlots) & 1u, status));
     };
-    auto wait_sum = [&](int b, int u) {
+    auto wait_sum_free = [&](int u) {
         return __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&bar[b + u % Turn::kSums],
+                          mbar_wait_bounded(&bar[kSumFree + u % Turn::kSums],
                                             static_cast<uint32_t>(u / Turn::kSums) & 1u, status));
     };
     auto arrive = [&](int b) {
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
 #pragma unroll 1
             for (int i = 1; ok && i < 3; ++i) ok = next_part(u, i);
             if (!ok || (u + 1 < nch && !(ok = first_part(u + 1)))) break;
-            if (!(ok = wait_sum(kSum, u))) break;
+            if (!(ok = wait2(kSum, u))) break;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 64; i += 32) {
@@ -708,11 +711,11 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             if (!STATE && !wait1(kQS, u)) break;
             load_q(u + 1);
             if (u + 2 < nch) {
-                if (!wait_sum(kSum, u)) break;
+                if (!wait2(kSum, u)) break;
                 load_k(u + 2);
             }
             if (u + 3 < nch) {
-                if (!wait2(kDone, u)) break;
+                if (!STATE && !wait2(kDone, u)) break;
                 load_v(u + 3);
             }
         }
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
 #pragma unroll 1
         for (int u = 0; u < nch; ++u) {
             const uint32_t k_tile = a0 + Smem::kK + (u & 1) * Smem::kTile;
-            bool ok = wait2(kFull, u) && (u < Turn::kSums || wait_sum(kSumFree, u - Turn::kSums));
+            bool ok = wait2(kFull, u) && (u < Turn::kSums || wait_sum_free(u - Turn::kSums));
 #pragma unroll 1
             for (int part = 0; ok && part < 3; ++part) {
                 const int j = 3 * u + part;
@@ -790,11 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
                 warp_mma_commit(&bar[kQS]);
             }
             if (!ok) break;
-            warp_mma_commit(&bar[kSum + u % Turn::kSums]);
-            if (STATE) {
-                warp_mma_commit(&bar[kDone + (u & 1)]);
-                continue;
-            }
+            warp_mma_commit(&bar[kSum + (u & 1)]);
+            if (STATE) continue;
             if (!wait1(kP, u)) break;
             tc_fence_after();
             uint64_t y = sw128_desc(a0 + Smem::kV + u % 3 * Smem::kTile, kBlk, 1024);
