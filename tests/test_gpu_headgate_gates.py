@@ -1,0 +1,79 @@
+"""Prompts with one gate per head whose gates fall steeply, many times in a chunk, and slowly behind
+that: against the 64-bit definition within the bounds of tests/headgate_reference.py."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+import chunkwise_linear_rnn_gb300 as gla
+import headgate_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from chunkwise_linear_rnn_gb300.build import build
+    build()
+
+
+def make(T, H=4, dk=64, dv=72, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.randn(T, H, d, generator=g).to(BF16).to(DEV) for d in (dk, dk, dv))
+    return q, k, v, (-0.02 * torch.rand(T, H, generator=g)).to(DEV)
+
+
+def check(q, k, v, la, cu, h0=None, less=0.0, what=""):
+    """less: how much of a score's rounding (of A) the bound of o is without."""
+    o, hT = gla.gla_headgate_fwd_varlen(q, k, v, la, cu, 0.125, h0)
+    qn, kn, vn, ln, hn = (ref.num(t) for t in (q, k, v, la, h0))
+    for n, (a, b) in enumerate(zip(cu, cu[1:])):
+        want = ref.walk(qn[a:b], kn[a:b], vn[a:b], ln[a:b], 0.125, None if hn is None else hn[n])
+        bo, bh = ref.prompt_bounds(b - a, *want[2:])
+        ref.assert_within(o[a:b], want[0], bo - less * want[2], f"{what} o of {n}")
+        ref.assert_within(hT[n], want[1], bh, f"{what} hT of {n}")
+    assert gla.gla_last_device_status() == 0
+
+
+def steep(la, kind, first, last):
+    """Steep gates in rows first to last, here and there slow ones among them."""
+    if kind == "cuts":
+        la[first:last] = -INF
+    elif kind == "strong":
+        la[first:last] = -100.0
+    elif kind == "uneven":
+        la[first:last:2] = -57.3
+        la[first + 1:last:7] = -19.7
+    else:
+        la[first:last:3] = -INF
+        la[first + 1:last:5] = -83.1
+    return la
+
+
+KINDS = ["cuts", "strong", "uneven", "both"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("count", [4, 32, 100, 127])
+def test_decays_behind_steep_gates(kind, count):
+    """One chunk, whose scores are two bf16 numbers each: the decays behind the steep gates are as
+    exact as if the sequence began there, 2^-16 of a score as for slow gates."""
+    q, k, v, la = make(3 * 128, seed=count)
+    for a in (0, 128, 256):
+        steep(la, kind, a, a + count)
+    check(q, k, v, la, [0, 128, 256, 384], less=2.0 ** -8 - 2.0 ** -16, what=f"{kind} {count}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("with_h0", [False, True])
+def test_steep_gates_of_longer_prompts(kind, with_h0):
+    """In the first, a middle and the last chunk, at its beginning, inside and at its end."""
+    q, k, v, la = make(1000)
+    for a, b in ((0, 60), (200, 256), (384, 500), (700, 701), (990, 1000)):
+        steep(la, kind, a, b)
+    h0 = torch.randn(2, 4, 64, 72, generator=torch.Generator().manual_seed(1)).to(DEV)
+    check(q, k, v, la, [0, 300, 1000], h0 if with_h0 else None, what=kind)
