@@ -9,8 +9,7 @@
 // One gate a token leaves q, k and v the bf16 numbers that they are: the decays go on the
 // scores, on the rows of the output and on v's rows.  A chunk whose gates fall below 2^-60 in
 // all takes its rows relative to R_t = max(G_t, -60) instead of G_t, with 2^(G_t - R_t - G_i) on
-// the scores, so that nothing overflows; the state's part of rows below is then 2^-60 of its
-// size or less where it should be less still.
+// the scores and 2^(G_t - R_t) on q_t S, so that nothing overflows.
 //
 // What is rounded to bf16: the scores and the copy of the state that q multiplies, once for
 // each output, as the output itself is (scores of batches of one chunk at most enter in two
@@ -683,6 +682,28 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             for (int b = w + 1; b < 4; ++b) {
                 tmem_st16(at + (FINE ? 32 : 16) * b, none);
                 if (FINE) tmem_st16(at + 32 * b + 16, none);
+            }
+            // q_t S of rows below the floor, in place before P V is added (8 prompts of 2,048 tokens, a
+            // ninth of whose heads forget as fast, 59.5 us for 57.8 without)
+            if (deep) {
+                if (!wait1(kQS, u)) break;
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, base < 0.f)) {
+                    const float left = ex2f(base + base_rest);
+#pragma unroll 1
+                    for (int c = 0; c < 64 * cblocks; c += 32) {
+                        uint32_t r[32], out[16];
+                        tmem_ld32(tmem + lanes + kTOut + c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 16) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                out[i] = __float_as_uint(left * __uint_as_float(r[j + i]));
+                            tmem_st16(tmem + lanes + kTOut + c + j, out);
+                        }
+                    }
+                }
             }
             tmem_wait_st();
             tc_fence_before();

@@ -77,3 +77,27 @@ def test_steep_gates_of_longer_prompts(kind, with_h0):
         steep(la, kind, a, b)
     h0 = torch.randn(2, 4, 64, 72, generator=torch.Generator().manual_seed(1)).to(DEV)
     check(q, k, v, la, [0, 300, 1000], h0 if with_h0 else None, what=kind)
+
+
+@pytest.mark.parametrize("size", [1.0, 1e10, 1e25])
+def test_nothing_of_a_state_is_left_behind_a_cut(size):
+    """Behind a gate of 0 the outputs are those without the state before it, whatever its size:
+    zeros where no value has come since."""
+    q, k, v, la = make(400)
+    la[150] = la[300, :2] = -INF
+    v[140:170] = 0
+    h0 = size * torch.randn(1, 4, 64, 72, generator=torch.Generator().manual_seed(2)).to(DEV)
+    o, _ = gla.gla_headgate_fwd_varlen(q, k, v, la, [0, 400], 0.125, h0)
+    assert o[:150].abs().max() >= size / 100
+    assert (o[150:170] == 0).all()
+    check(q, k, v, la, [0, 400], h0, what=f"{size}")
+
+
+def test_a_state_behind_steep_gates_falls_as_they_do():
+    """Gates that add up to less than 2^-60 in a chunk, without a cut: the part of a large state that
+    is left is what the gates leave of it, not 2^-60 of it."""
+    q, k, v, la = make(300)
+    la[:40] = -1.5                  # 2^-87 of the state is left behind them
+    v[:] = 0
+    h0 = 2.0 ** 100 * torch.randn(1, 4, 64, 72, generator=torch.Generator().manual_seed(3)).to(DEV)
+    check(q, k, v, la, [0, 300], h0, what="steep")

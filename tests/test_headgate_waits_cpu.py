@@ -44,10 +44,10 @@ class Barrier:
 
 class Kernel:
     """One block's walk over n chunks; `state`: the launch that wants the sums alone; `cut`: the
-    last chunk is not full; `deep`: chunks whose rows fall below the floor."""
+    last chunk is not full; `deep`: whose rows fall below the floor, by chunk."""
 
-    def __init__(self, n, state, cut, turns, state_loads_wait_done):
-        self.n, self.state, self.cut = n, state, cut
+    def __init__(self, n, state, cut, deep, turns, state_loads_wait_done):
+        self.n, self.state, self.cut, self.deep = n, state, cut, deep
         self.wait_done = state_loads_wait_done or not state
         slots, sums = (4, 2) if state else (2, 1)
         number = {"slots": slots, "sums": sums, "1": 1, "2": 2, "3": 3}
@@ -142,6 +142,8 @@ class Kernel:
         for u in range(self.n):
             yield self.wait("kGFull", u)
             yield self.wait("kScore", u)
+            if self.deep(u):
+                yield self.wait("kQS", u)
             self.arrive("kP", u)
             self.arrive("kGFree", u)
             yield self.wait("kDone", u)
@@ -214,9 +216,10 @@ def schedules(roles):
         yield lambda n, rng=rng: rng.sample(range(n), n)
 
 
-def ends(n, state, cut, turns, wait_done):
+def ends(n, state, cut, turns, wait_done, deep=lambda u: False):
     roles = 3 + VALUES + (0 if state else SCORES)
-    return all(Kernel(n, state, cut, turns, wait_done).run(order) for order in schedules(roles))
+    return all(Kernel(n, state, cut, deep, turns, wait_done).run(order)
+               for order in schedules(roles))
 
 
 @pytest.mark.parametrize("state", [False, True], ids=["outputs", "sums"])
@@ -225,7 +228,10 @@ def test_no_schedule_stops_the_kernel(state, cut):
     turns, wait_done = read_source()
     assert {"kFull", "kSum", "kSumFree", "kDone", "kDrain"} <= set(turns)
     for n in range(14):
-        assert ends(n, state, cut, turns, wait_done), f"{n} chunks"
+        for deep in (lambda u: False, lambda u: True, lambda u: u in (3, 6, 7)):
+            assert ends(n, state, cut, turns, wait_done, deep), f"{n} chunks"
+            if state:
+                break
 
 
 def test_the_model_sees_a_wait_that_can_be_missed():
