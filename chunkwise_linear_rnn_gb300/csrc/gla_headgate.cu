@@ -58,6 +58,7 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "gla.h"
@@ -202,8 +203,8 @@ __device__ __forceinline__ void load_gates(const Args &p, long long row, int n, 
     }
 }
 
-template <bool STATE, bool FINE>
-__device__ __forceinline__ void write_gates(float (&g)[4], Gates &out) {
+template <bool STATE>
+__device__ __forceinline__ void write_gates(float (&g)[4], Gates &out, bool fine) {
     const int lane = threadIdx.x & 31;
     // exp(-130) is 0 in 32 bits, 2^60 of it too: a gate of 0 takes part in the sums as this
 #pragma unroll
@@ -224,7 +225,7 @@ __device__ __forceinline__ void write_gates(float (&g)[4], Gates &out) {
     behind = __shfl_down_sync(0xffffffffu, behind, 1);
     if (lane == 0) before = 0.f;
     if (lane == 31) behind = 0.f;
-    const bool deep = total * kLog2e < kFloor, steep = FINE ? deep : total * kLog2e < kSteep;
+    const bool deep = total * kLog2e < kFloor, steep = fine ? deep : total * kLog2e < kSteep;
     if (!STATE) {
         float e[4];
         if (!steep) {
@@ -350,10 +351,7 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
 }
 
 // STATE: the first launch of divided sequences, whose segments' sums alone are wanted.
-// FINE: sequences of one chunk at most, where so few scores may make up the outputs that their
-// rounding does not average out: they are taken in two parts, 2^-16 off instead of 2^-8.  (A
-// kernel of its own: as a condition it costs the others 4 %.)
-template <bool STATE, bool FINE>
+template <bool STATE>
 __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __grid_constant__ Args p) {
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + Smem::kBar);
@@ -369,6 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
     const int cblocks = p.dv - c0 > 64 ? 2 : 1;
     const uint32_t a0 = smem_u32(sm);
     unsigned int *status = p.status;
+    // A sequence of one chunk at most: all of its outputs are made up of few scores, whose rounding
+    // does not average out.  They are taken in two parts, 2^-16 off instead of 2^-8.  This goes by
+    // the sequence's own length, so that a short prompt's outputs do not depend on the others of its
+    // batch.  (Loops of their own: as a condition in the walk it costs the others 4 %, as a launch of
+    // its own 14 us where both kinds are there, this way 1 to 2 %.)
+    const bool fine = !STATE && it.parts == 1 && it.rows <= C;
 
     if (warp == 0) tmem_alloc(slot, 512);
     if (tid == 32) {
@@ -608,142 +612,147 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
         registers_down<112>();
         const int w = warp & 3, t = 32 * w + lane;
         const uint32_t at = tmem + lanes + kTScore;
+        auto walk = [&](auto fine_scores) {
+            constexpr bool FINE = decltype(fine_scores)::value;
 #pragma unroll 1
-        for (int u = 0; !STATE && u < nch; ++u) {
-            if (!(wait2(kGFull, u) && wait1(kScore, u))) break;
-            tc_fence_after();
-            const Gates &g = gates[u & 1];
-            const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
-            const bool deep = g.deep, steep = g.steep, plain = !deep && !FINE;
-            const float own = g.e[t];
-            // G_t - R_t, in two parts as -G_i; and what of it is added to each -G_i by itself
-            const float base = deep ? -own - fmaxf(-own, kFloor) : 0.f, on = steep ? 0.f : base;
-            const uint32_t two = steep ? g.rest[t / 2] : 0u;
-            const float base_rest = -__uint_as_float(t & 1 ? two & 0xffff0000u : two << 16);
-            const float f = p.scale * (deep ? ex2f(fmaxf(-own, kFloor)) : 1.f / own);
-            // the tokens of warps before this one's, then its own, then those behind: 32 scores
-            // become 16 columns, one block behind the other; or, in two parts, 32 in their place
-#pragma unroll 1
-            for (int b = 0; b <= w; ++b) {
-                uint32_t r[32], out[16];
-                float4 e[8];
-                tmem_ld32(at + 32 * b, r);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = e4[8 * b + j];
-                tmem_wait_ld();
-                if (b == w) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j > lane) r[j] = 0u;
-                }
-                if (steep) {
-                    // the differences of the sums, then of their rests
-                    const Pair sum = pair_of(base, base), rest = pair_of(base_rest, base_rest);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t *of = g.rest + 16 * b + 2 * j;
-                        const float2 x = both(add2(add2(pair_of(e[j].x, e[j].y), sum),
-                                                   add2(widen(of[0]), rest)));
-                        const float2 y = both(add2(add2(pair_of(e[j].z, e[j].w), sum),
-                                                   add2(widen(of[1]), rest)));
-                        e[j] = make_float4(x.x, x.y, y.x, y.y);
-                    }
-                }
-                if (plain) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 x = e[j / 4];
-                        out[j / 2] = narrow(mul2(pair_of(r[j], r[j + 1]), pair_of(x.x, x.y)));
-                        out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(x.z, x.w)));
-                    }
-                } else {
-                    uint32_t rest[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float f0 = j % 4 ? e[j / 4].z : e[j / 4].x;
-                        float f1 = j % 4 ? e[j / 4].w : e[j / 4].y;
-                        if (deep) {
-                            // of a later token it may be infinite: a masked score stays 0
-                            f0 = 32 * b + j <= t ? ex2f(on + f0) : 0.f;
-                            f1 = 32 * b + j + 1 <= t ? ex2f(on + f1) : 0.f;
-                        }
-                        const Pair x = mul2(pair_of(r[j], r[j + 1]), pair_of(f0, f1));
-                        out[j / 2] = narrow(x);
-                        if (FINE) rest[j / 2] = narrow(left_of(x, out[j / 2]));
-                    }
-                    if (FINE) tmem_st16(at + 32 * b + 16, rest);
-                }
-                tmem_st16(at + (FINE ? 32 : 16) * b, out);
-            }
-            uint32_t none[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) none[j] = 0u;
-#pragma unroll 1
-            for (int b = w + 1; b < 4; ++b) {
-                tmem_st16(at + (FINE ? 32 : 16) * b, none);
-                if (FINE) tmem_st16(at + 32 * b + 16, none);
-            }
-            // q_t S of rows below the floor, in place before P V is added (8 prompts of 2,048 tokens, a
-            // ninth of whose heads forget as fast, 59.5 us for 57.8 without)
-            if (deep) {
-                if (!wait1(kQS, u)) break;
+            for (int u = 0; u < (FINE ? min(nch, 1) : nch); ++u) {
+                if (!(wait2(kGFull, u) && wait1(kScore, u))) break;
                 tc_fence_after();
-                if (__any_sync(0xffffffffu, base < 0.f)) {
-                    const float left = ex2f(base + base_rest);
+                const Gates &g = gates[u & 1];
+                const float4 *e4 = reinterpret_cast<const float4 *>(g.e);
+                const bool deep = g.deep, steep = g.steep, plain = !deep && !FINE;
+                const float own = g.e[t];
+                // G_t - R_t, in two parts as -G_i; and what of it is added to each -G_i by itself
+                const float base = deep ? -own - fmaxf(-own, kFloor) : 0.f, on = steep ? 0.f : base;
+                const uint32_t two = steep ? g.rest[t / 2] : 0u;
+                const float base_rest = -__uint_as_float(t & 1 ? two & 0xffff0000u : two << 16);
+                const float f = p.scale * (deep ? ex2f(fmaxf(-own, kFloor)) : 1.f / own);
+                // the tokens of warps before this one's, then its own, then those behind: 32 scores
+                // become 16 columns, one block behind the other; or, in two parts, 32 in their place
 #pragma unroll 1
-                    for (int c = 0; c < 64 * cblocks; c += 32) {
-                        uint32_t r[32], out[16];
-                        tmem_ld32(tmem + lanes + kTOut + c, r);
-                        tmem_wait_ld();
+                for (int b = 0; b <= w; ++b) {
+                    uint32_t r[32], out[16];
+                    float4 e[8];
+                    tmem_ld32(at + 32 * b, r);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 16) {
+                    for (int j = 0; j < 8; ++j) e[j] = e4[8 * b + j];
+                    tmem_wait_ld();
+                    if (b == w) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                out[i] = __float_as_uint(left * __uint_as_float(r[j + i]));
-                            tmem_st16(tmem + lanes + kTOut + c + j, out);
+                        for (int j = 0; j < 32; ++j)
+                            if (j > lane) r[j] = 0u;
+                    }
+                    if (steep) {
+                        // the differences of the sums, then of their rests
+                        const Pair sum = pair_of(base, base), rest = pair_of(base_rest, base_rest);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t *of = g.rest + 16 * b + 2 * j;
+                            const float2 x = both(add2(add2(pair_of(e[j].x, e[j].y), sum),
+                                                       add2(widen(of[0]), rest)));
+                            const float2 y = both(add2(add2(pair_of(e[j].z, e[j].w), sum),
+                                                       add2(widen(of[1]), rest)));
+                            e[j] = make_float4(x.x, x.y, y.x, y.y);
+                        }
+                    }
+                    if (plain) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 x = e[j / 4];
+                            out[j / 2] = narrow(mul2(pair_of(r[j], r[j + 1]), pair_of(x.x, x.y)));
+                            out[j / 2 + 1] = narrow(mul2(pair_of(r[j + 2], r[j + 3]), pair_of(x.z, x.w)));
+                        }
+                    } else {
+                        uint32_t rest[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float f0 = j % 4 ? e[j / 4].z : e[j / 4].x;
+                            float f1 = j % 4 ? e[j / 4].w : e[j / 4].y;
+                            if (deep) {
+                                // of a later token it may be infinite: a masked score stays 0
+                                f0 = 32 * b + j <= t ? ex2f(on + f0) : 0.f;
+                                f1 = 32 * b + j + 1 <= t ? ex2f(on + f1) : 0.f;
+                            }
+                            const Pair x = mul2(pair_of(r[j], r[j + 1]), pair_of(f0, f1));
+                            out[j / 2] = narrow(x);
+                            if (FINE) rest[j / 2] = narrow(left_of(x, out[j / 2]));
+                        }
+                        if (FINE) tmem_st16(at + 32 * b + 16, rest);
+                    }
+                    tmem_st16(at + (FINE ? 32 : 16) * b, out);
+                }
+                uint32_t none[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) none[j] = 0u;
+#pragma unroll 1
+                for (int b = w + 1; b < 4; ++b) {
+                    tmem_st16(at + (FINE ? 32 : 16) * b, none);
+                    if (FINE) tmem_st16(at + 32 * b + 16, none);
+                }
+                // q_t S of rows below the floor, in place before P V is added (8 prompts of 2,048 tokens, a
+                // ninth of whose heads forget as fast, 59.5 us for 57.8 without)
+                if (deep) {
+                    if (!wait1(kQS, u)) break;
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, base < 0.f)) {
+                        const float left = ex2f(base + base_rest);
+#pragma unroll 1
+                        for (int c = 0; c < 64 * cblocks; c += 32) {
+                            uint32_t r[32], out[16];
+                            tmem_ld32(tmem + lanes + kTOut + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; j += 16) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    out[i] = __float_as_uint(left * __uint_as_float(r[j + i]));
+                                tmem_st16(tmem + lanes + kTOut + c + j, out);
+                            }
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(kP);
+                arrive(kGFree + (u & 1));
+                // the outputs of row t
+                const Pair ff = pair_of(f, f);
+                const int there = u * C + t < it.rows ? p.dv - c0 : 0;
+                __nv_bfloat16 *to =
+                    p.o + (static_cast<long long>(it.row + u * C + t) * p.H + h) * p.dv + c0;
+                if (!wait2(kDone, u)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 64 * cblocks; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tmem + lanes + kTOut + c, r);
+                    tmem_wait_ld();
+                    if (c + 32 == 64 * cblocks) {
+                        tc_fence_before();
+                        arrive(kOFree);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = narrow(mul2(ff, pair_of(r[i + 2 * j], r[i + 2 * j + 1])));
+                        if (p.wide_store) {
+                            if (c + i < there) store32(to + c + i, v);
+                        } else {
+                            if (c + i < there)
+                                *reinterpret_cast<uint4 *>(to + c + i) =
+                                    make_uint4(v[0], v[1], v[2], v[3]);
+                            if (c + i + 8 < there)
+                                *reinterpret_cast<uint4 *>(to + c + i + 8) =
+                                    make_uint4(v[4], v[5], v[6], v[7]);
                         }
                     }
                 }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(kP);
-            arrive(kGFree + (u & 1));
-            // the outputs of row t
-            const Pair ff = pair_of(f, f);
-            const int there = u * C + t < it.rows ? p.dv - c0 : 0;
-            __nv_bfloat16 *to =
-                p.o + (static_cast<long long>(it.row + u * C + t) * p.H + h) * p.dv + c0;
-            if (!wait2(kDone, u)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 64 * cblocks; c += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + lanes + kTOut + c, r);
-                tmem_wait_ld();
-                if (c + 32 == 64 * cblocks) {
-                    tc_fence_before();
-                    arrive(kOFree);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; i += 16) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = narrow(mul2(ff, pair_of(r[i + 2 * j], r[i + 2 * j + 1])));
-                    if (p.wide_store) {
-                        if (c + i < there) store32(to + c + i, v);
-                    } else {
-                        if (c + i < there)
-                            *reinterpret_cast<uint4 *>(to + c + i) =
-                                make_uint4(v[0], v[1], v[2], v[3]);
-                        if (c + i + 8 < there)
-                            *reinterpret_cast<uint4 *>(to + c + i + 8) =
-                                make_uint4(v[4], v[5], v[6], v[7]);
-                    }
-                }
-            }
-        }
+        };
+        if (fine) walk(std::true_type{});
+        else if (!STATE) walk(std::false_type{});
     } else if (warp == 12) {
         // ================================================================ loads
         registers_down<64>();
@@ -806,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             if (u + 1 < nch)
                 load_gates(p, it.row + (u + 1) * C, min(C, it.rows - (u + 1) * C), h, next);
             if (u >= 2 && !wait2(kGFree, u - 2)) break;
-            write_gates<STATE, FINE>(g, gates[u & 1]);
+            write_gates<STATE>(g, gates[u & 1], fine);
             arrive(kGFull + (u & 1));
         }
     } else if (warp == 14) {
@@ -869,14 +878,18 @@ __global__ void __launch_bounds__(kThreads, 1) headgate_chunk_kernel(const __gri
             if (!wait1(kP, u)) break;
             tc_fence_after();
             uint64_t y = sw128_desc(a0 + Smem::kV + u % 3 * Smem::kTile, kBlk, 1024);
+            if (!fine) {
 #pragma unroll 1
-            for (int i = 0; !FINE && i < C / 16; ++i, y += kRows)
-                warp_mma_bf16_ts(tmem + kTOut, tmem + kTScore + 8 * i, y, id_pv, 1u);
+                for (int i = 0; i < C / 16; ++i, y += kRows)
+                    warp_mma_bf16_ts(tmem + kTOut, tmem + kTScore + 8 * i, y, id_pv, 1u);
+            } else {
 #pragma unroll 1
-            for (int i = 0; FINE && i < C / 8; ++i) {
-                // both parts of 16 tokens' scores
-                const uint32_t score = tmem + kTScore + (i >> 2) * 32 + (i & 1) * 16 + (i >> 1 & 1) * 8;
-                warp_mma_bf16_ts(tmem + kTOut, score, y + (i >> 1) * kRows, id_pv, 1u);
+                for (int i = 0; i < C / 8; ++i) {
+                    // both parts of 16 tokens' scores
+                    const uint32_t score =
+                        tmem + kTScore + (i >> 2) * 32 + (i & 1) * 16 + (i >> 1 & 1) * 8;
+                    warp_mma_bf16_ts(tmem + kTOut, score, y + (i >> 1) * kRows, id_pv, 1u);
+                }
             }
             warp_mma_commit(&bar[kDone + (u & 1)]);
         }
@@ -966,14 +979,14 @@ bool bounds_ok(const int *cu, int N, int T) {
     return true;
 }
 
-template <bool STATE, bool FINE>
+template <bool STATE>
 bool prepared() {
     // the attribute belongs to the device's copy of the function
     static std::atomic<bool> done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     if (done[dev].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(headgate_chunk_kernel<STATE, FINE>,
+    if (cudaFuncSetAttribute(headgate_chunk_kernel<STATE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Smem::kBytes)) != cudaSuccess)
         return false;
@@ -981,15 +994,15 @@ bool prepared() {
     return true;
 }
 
-template <bool STATE, bool FINE>
+template <bool STATE>
 bool launch(Args &a, const std::vector<Item> &items, cudaStream_t stream) {
     if (items.empty()) return true;
-    if (!prepared<STATE, FINE>()) return false;
+    if (!prepared<STATE>()) return false;
     for (size_t first = 0; first < items.size(); first += kItems) {
         const size_t n = std::min<size_t>(kItems, items.size() - first);
         std::copy(items.begin() + first, items.begin() + first + n, a.items);
         const unsigned grid = static_cast<unsigned>(n) * a.H * a.tiles;
-        headgate_chunk_kernel<STATE, FINE><<<grid, kThreads, Smem::kBytes, stream>>>(a);
+        headgate_chunk_kernel<STATE><<<grid, kThreads, Smem::kBytes, stream>>>(a);
         if (cudaGetLastError() != cudaSuccess) return false;
     }
     return true;
@@ -1014,11 +1027,7 @@ int run(Args &a, const int *cu, int N, const Plan &plan, cudaStream_t stream) {
     auto longer = [](const Item &x, const Item &y) { return x.rows > y.rows; };
     std::stable_sort(whole.begin(), whole.end(), longer);
     std::stable_sort(sums.begin(), sums.end(), longer);
-    const bool ok = sums.empty() && whole[0].rows <= C
-                        ? launch<false, true>(a, whole, stream)
-                        : launch<true, false>(a, sums, stream) &&
-                              launch<false, false>(a, whole, stream);
-    return ok ? GLA_OK : GLA_ERR_LAUNCH;
+    return launch<true>(a, sums, stream) && launch<false>(a, whole, stream) ? GLA_OK : GLA_ERR_LAUNCH;
 }
 
 }  // namespace
