@@ -1313,7 +1313,11 @@ def gla_group_norm_act(x: torch.Tensor, gate: torch.Tensor | None = None,
 
 
 def gla_last_device_status(device: torch.device | int | None = None) -> int:
-    """Synchronise the current stream and read/clear the library's device status word."""
+    """Synchronise the current stream and read the library's device status word.
+
+    Returns 0, GLA_ERR_TIMEOUT (a bounded wait gave up) or GLA_ERR_ARG (a decode step refused a slot),
+    and clears what it returns: with both, the next call returns the second.
+    """
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else
                        (device if isinstance(device, int) else device.index))
     with torch.cuda.device(dev):

@@ -1030,12 +1030,12 @@ int gla_last_device_status(cudaStream_t stream) {
         cudaGetLastError();
         return GLA_ERR_LAUNCH;
     }
-    if (word != 0) {
-        const unsigned int zero = 0;
-        cudaMemcpy(dev->status, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-        return word & kStatusTimeout ? GLA_ERR_TIMEOUT : GLA_ERR_ARG;
-    }
-    return GLA_OK;
+    if (word == 0) return GLA_OK;
+    // one at a time: what else there is stays for the next call
+    const bool timeout = word & kStatusTimeout;
+    word &= ~(timeout ? kStatusTimeout : kStatusSlot);
+    cudaMemcpy(dev->status, &word, sizeof(word), cudaMemcpyHostToDevice);
+    return timeout ? GLA_ERR_TIMEOUT : GLA_ERR_ARG;
 }
 
 }  // extern "C"

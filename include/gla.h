@@ -741,10 +741,11 @@ int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
 const char *gla_status_string(int status);
 
 /*
- * Synchronises `stream`, then reads and clears the library's device status
- * word on the current device.  Returns GLA_ERR_TIMEOUT if any kernel since
- * the last call gave up a bounded wait, GLA_ERR_ARG if gla_headgate_step met a slot that
- * it refuses, GLA_ERR_LAUNCH if the stream reports a CUDA error, else GLA_OK.
+ * Synchronises `stream`, then reads the library's device status word on the
+ * current device.  Returns GLA_ERR_TIMEOUT if a kernel gave up a bounded wait,
+ * GLA_ERR_ARG if gla_headgate_step met a slot that it refuses, GLA_ERR_LAUNCH if
+ * the stream reports a CUDA error, else GLA_OK.  What a call returns is cleared
+ * by it; with both a timeout and a slot, the next call returns the slot.
  */
 int gla_last_device_status(cudaStream_t stream);
 
