@@ -1071,6 +1071,9 @@ int gla_headgate_fwd_varlen(const void *q, const void *k, const void *v, const f
     if (plan.slots > INT_MAX) return GLA_ERR_ARG;
     const size_t need = scratch_of(plan, H, dk, dv);
     if (need > 0 && (!scratch || scratch_bytes < need)) return GLA_ERR_SCRATCH;
+    const Span work = span_of(scratch, need, 1);
+    if (meets_any(work, in) || meet(work, out) || meet(work, begin) || meet(work, end))
+        return GLA_ERR_ARG;
     int sms = 0;
     Args a = {};
     st = usable_device(&sms, &a.status);

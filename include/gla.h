@@ -629,8 +629,9 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
  * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256 (GLA_ERR_SHAPE
  * otherwise); H a multiple of Hk, up to 65535.  q, k, v, o and the states 16-byte
  * aligned, strides of q, k and v non-negative multiples of 8 elements (over the tokens
- * of a prompt positive ones), those of log_alpha non-negative (GLA_ERR_ARG otherwise).  No output may overlap an input
- * but hT, which may be h0 itself.
+ * of a prompt positive ones), those of log_alpha non-negative (GLA_ERR_ARG otherwise).
+ * No output may overlap an input but hT, which may be h0 itself; scratch may overlap
+ * neither.
  *
  * gla_headgate_fwd_varlen — prompts: a packed batch of N sequences, sequence n in
  * rows cu_seqlens[n] : cu_seqlens[n+1] (a HOST array of N + 1 ints from 0 to
