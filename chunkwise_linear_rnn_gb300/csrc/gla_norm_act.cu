@@ -664,6 +664,8 @@ int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
     int sms = 0;
     st = usable_device(&sms);
     if (st != GLA_OK) return st;
+    const Span work = span_of(a.partial, gla_group_norm_act_bwd_scratch(B, T, H, d), 1);
+    if (meets_any(work, in) || meet(work, up) || meets_any(work, outs)) return GLA_ERR_ARG;
     const int e = options->dtype == GLA_BF16
                       ? bwd<__nv_bfloat16>(a, grad_weight, grad_bias, stream)
                       : bwd<float>(a, grad_weight, grad_bias, stream);

@@ -698,7 +698,7 @@ int gla_headgate_step(const void *q, const void *k, const void *v, const float *
  * (0, 1], unknown dtype, norm, activation or per_channel, strides that are negative or
  * not multiples of 8 elements, tensors that are not 16-byte aligned, or more than
  * 2^31 - 1 thread blocks of work.  No output may overlap an input, and no output
- * another.
+ * another; scratch may overlap neither.
  */
 enum gla_activation { GLA_ACT_SILU = 0, GLA_ACT_SIGMOID = 1 };
 typedef struct gla_norm_act_layout {
