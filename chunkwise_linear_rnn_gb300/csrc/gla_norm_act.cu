@@ -45,7 +45,7 @@ struct NormArgs {
     const void *x, *gate, *dy;
     const float *w, *b;
     void *y, *dx, *dgate;
-    float *partial;          // backward with weights: see reduce_kernel
+    double *partial;         // backward with weights: see reduce_kernel
     gla_norm_act_layout lay;
     unsigned tokens, T;      // T = tokens where one stride steps over batch and tokens
     int H, d, groups;        // groups of the heads that a warp takes together
@@ -329,12 +329,13 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdPerSm<E, NB>) norm_fwd_kernel
     }
 }
 
-// The sums of a block: over its warps in their order, and over the heads of a warp where they
-// share a weight.  v: a lane's values; out: the block's row of the partial sums.
+// The sums of a block in 64 bits: over its warps in their order, and over the heads of a warp where
+// they share a weight.  v: a lane's values, sums of at most kSumRows rows; out: the block's row of
+// the partial sums.
 template <int LANES, int NB>
 __device__ __forceinline__ void block_sums(const NormArgs &p, const Place<LANES, NB> &at,
                                            float (*buf)[32][NB][8], const Pair (&v)[NB][4],
-                                           float *out) {
+                                           double *out) {
     constexpr int ROWS = 32 / LANES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();   // the buffer's last use
@@ -347,7 +348,7 @@ __device__ __forceinline__ void block_sums(const NormArgs &p, const Place<LANES,
     const int values = p.per_channel ? ROWS * p.d : p.d;
     for (int c = threadIdx.x; c < values; c += 32 * kWarps) {
         const int r = c / p.d, ch = c - r * p.d, i = ch / 8 / LANES, j = ch / 8 % LANES;
-        float s = 0.f;
+        double s = 0.;
         for (int row = r; row < (p.per_channel ? r + 1 : ROWS); ++row)
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) s += buf[k][row * LANES + j][i][ch % 8];
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 2 : 1) norm_bwd_kernel(
     if (p.partial) {
         constexpr int ROWS = 32 / LANES;
         const long long row = p.per_channel ? static_cast<long long>(ROWS) * p.d : p.d;
-        float *out = p.partial + blockIdx.x * row;
+        double *out = p.partial + blockIdx.x * row;
         block_sums<LANES, NB>(p, at, buf, dw, out);
         block_sums<LANES, NB>(p, at, buf, db, out + gridDim.x * row);
     }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(32 * kWarps, NB == 1 ? 2 : 1) norm_bwd_kernel(
 // [2][blocks][values]: the values of blocks b, b + groups, ... belong to the same heads where
 // each head has weights of its own (groups > 1 only there), else every block has the same ones.
 // 32 channels of a block, one warp-wide row of 32 partial sums each; sums in fp64.
-__global__ void __launch_bounds__(1024) reduce_kernel(const float *partial, unsigned blocks,
+__global__ void __launch_bounds__(1024) reduce_kernel(const double *partial, unsigned blocks,
                                                       int groups, int values, int channels,
                                                       float *dw, float *db) {
     __shared__ double buf[32][33];
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(1024) reduce_kernel(const float *partial, unsi
     double s = 0.;
     if (c < channels) {
         const unsigned group = c / values;
-        const float *from = partial + static_cast<size_t>(blockIdx.y) * blocks * values + c % values;
+        const double *from = partial + static_cast<size_t>(blockIdx.y) * blocks * values + c % values;
         for (unsigned k = group + ry * groups; k < blocks; k += 32 * groups)
             s += from[static_cast<size_t>(k) * values];
     }
@@ -621,7 +622,7 @@ unsigned long gla_group_norm_act_bwd_scratch(int B, int T, int H, int d) {
     if (B <= 0 || T <= 0 || H <= 0 || d <= 0) return 0;
     const int rows = rows_of(d), groups = (H + rows - 1) / rows;
     const long long tb = token_blocks(static_cast<long long>(B) * T, groups, kBwdBlocks, kSumRows);
-    return 2ul * sizeof(float) * tb * groups * rows * d;
+    return 2ul * sizeof(double) * tb * groups * rows * d;
 }
 
 int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
@@ -643,7 +644,7 @@ int gla_group_norm_act_bwd(const void *x, const void *gate, const float *weight,
         if (!scratch || !aligned(scratch, 16)) return GLA_ERR_ARG;
         if (scratch_bytes < gla_group_norm_act_bwd_scratch(B, T, H, d)) return GLA_ERR_SCRATCH;
         if (!aligned(grad_weight, 4) || !aligned(grad_bias, 4)) return GLA_ERR_ARG;
-        a.partial = static_cast<float *>(scratch);
+        a.partial = static_cast<double *>(scratch);
     }
     const int size = options->dtype == GLA_BF16 ? 2 : 4;
     const unsigned long long n = static_cast<unsigned long long>(a.tokens) * H * d;
