@@ -1111,7 +1111,9 @@ def gla_headgate_fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     sequence of ``N + 1`` ints.  ``h0`` is ``[N, H, dk, dv]`` fp32 or None (zero).  Returns
     ``(o, hT)``: ``[T_total, H, dv]`` bf16 and the last states in fp32 (an empty sequence
     keeps its own; None when ``output_final_state`` is False).  ``final_state`` may be ``h0``
-    itself.  For gradients see ``gla_chunk``, which takes ``[B, H, T]`` gates head-first.
+    itself.  An infinite or NaN value of a token may show in the outputs of the up to 127
+    tokens before it in its own sequence, beside all later ones; never in another sequence.
+    For gradients see ``gla_chunk``, which takes ``[B, H, T]`` gates head-first.
     """
     (T, Hk, H, dk, dv), layout, _ = _headgate(q, k, v, log_alpha, torch.bfloat16)
     dev = q.device

@@ -623,7 +623,7 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
  *                (in elements; the last dimension is contiguous)
  *   log_alpha  : [T, H] fp32, <= 0, through strides of its own; a token stride of 0
  *                is a fixed decay for each head.  -infinity is a gate of 0 and cuts
- *                the sequence
+ *                the sequence, as gates below exp(-130) do
  *   o          : [T, H, dv] contiguous, rounded once
  *   states     : fp32 [., H, dk, dv], row index = key channel
  * dk a multiple of 8 up to 128, dv a multiple of 8 up to 256 (GLA_ERR_SHAPE
@@ -644,11 +644,15 @@ int gla_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const fl
  * same time need scratch of their own.  Equal calls give equal bits.
  * Accuracy: the states are held and summed in fp32.  With M the recurrence on |k|, |v|
  * and |h0|, hT is within 2^-24 (264 + T / 32) M and the gates' own roundings of the exact
- * state, o before its rounding within 2^-8 scale |q| M and as many more of 2^-24.  A sequence does not see its neighbours' values,
- * infinite or NaN ones included; an infinite or NaN value of a token may show in the
- * outputs of the up to 127 tokens before it, and does in the later ones.  A bounded
- * device wait that expires leaves the outputs unspecified and is reported by
- * gla_last_device_status (GLA_ERR_TIMEOUT).  Scores |q_t k_i| have to stay below 2^60.
+ * state, o before its rounding within 2^-8 scale |q| M and as many more of 2^-24 (2^-16
+ * for sequences of at most 128 tokens without h0).  The scores |q_t k_i|, and their sums
+ * over 128 tokens with the |v_i|, have to stay below 2^66.
+ * A sequence does not see its neighbours' values, infinite or NaN ones included.  One of
+ * at most 128 tokens has the same bits in any batch; longer ones may be divided otherwise
+ * in another batch, within the accuracy above.  Within a sequence an infinite or NaN
+ * value of a token may show in the outputs of the up to 127 tokens before it, and does
+ * in the later ones.  A bounded device wait that expires leaves the outputs unspecified
+ * and is reported by gla_last_device_status (GLA_ERR_TIMEOUT).
  */
 typedef struct gla_headgate_layout {
     long long q_st, q_sh;   /* strides of q over token (row of a step) and head */

@@ -101,3 +101,17 @@ def test_a_state_behind_steep_gates_falls_as_they_do():
     v[:] = 0
     h0 = 2.0 ** 100 * torch.randn(1, 4, 64, 72, generator=torch.Generator().manual_seed(3)).to(DEV)
     check(q, k, v, la, [0, 300], h0, what="steep")
+
+
+@pytest.mark.parametrize("rate", [0.0, 0.25, 0.3, 0.33, 0.6, 3.0])
+def test_large_values_within_the_stated_range(rate):
+    """Sums over a chunk of |q_t k_i| |v_i| near 2^66, with gates that leave 2^-55 to 2^-60 of a chunk
+    (factors of up to 2^60 on the scores), more and less."""
+    q, k, v, la = make(300)
+    la.mul_(rate / 0.01)
+    q, k, v = q * 2.0 ** 14, k * 2.0 ** 14, v * 2.0 ** 28
+    scores = torch.einsum("thd,shd->hts", q.double(), k.double()).abs()
+    sums = (scores @ v.double().abs().transpose(0, 1)).max() / 300 * 128
+    assert 2.0 ** 65 < sums < 2.0 ** 66
+    check(q, k, v, la, [0, 300], what=f"{rate}")
+    check(q, k, v, la, [0, 100, 128, 300], what=f"{rate}, short ones")
