@@ -12,7 +12,7 @@
 // the scores and 2^(G_t - R_t) on q_t S, so that nothing overflows.
 //
 // What is rounded to bf16: the scores and the copy of the state that q multiplies, once for
-// each output, as the output itself is (scores of batches of one chunk at most enter in two
+// each output, as the output itself is (scores of sequences of one chunk at most enter in two
 // parts instead).  The state does not lose anything by it: 2^(G_n - G_i) v_i enters as the sum
 // of three bf16 numbers, which hold all 24 bits of it, and S' is summed in fp32 registers.
 //
@@ -31,20 +31,26 @@
 //   Q K^T              chunk u - 1 is done
 //   Q S                the copy of S is written, the last chunk's outputs are read
 //   V'2^T K, V'3^T K   onto the first; their parts are written (two slots take turns)
-//   P V, onto Q S      the scores are written
+//   P V, onto Q S      the scores are written, and in a chunk below the floor Q S is scaled
 // Q S comes early so that one tile of Q is enough, which leaves room for a third one of V.
 //
-// HBM's floor for 16,384 tokens, 16 heads of 128 and 128 is 40 us (268 MB); measured on one GB300
-// 58 us (0.68), with 128 of 152 SMs in use.  A chunk's products take 3,120 cycles, shared memory's
-// traffic 3,328 (416 KB at 128 bytes a cycle), the warps' instructions about 3,000 issue slots of
-// a scheduler; it takes about 6,000 in all, with none of the three above 45 % (tensor pipe 45 %,
-// L1 and shared memory 44 %, issue slots 40 %): what is left is the chain from warp to warp.
-// Without the values' splitting it would take 12 % less, without the outputs' stores 13 %,
-// without the work on states, scores or copies 2 to 4 % each.
-// Measured beside it, same case: parts of V' in shared memory and 64 columns a block, 78 us;
-// outputs through shared memory and TMA stores, 60; all outputs read before the first store, 67;
-// the next chunk's tiles pulled into L2 ahead of time, 60 to 63; the same products issued by one
-// lane alone (180-240 cycles each), 113 for 94 in the form with 64 columns.
+// HBM's floor for 16,384 tokens, 16 heads of 128 and 128 is 41 us (278 MB); measured on one GB300
+// 60 us (0.68), with 128 of 152 SMs in use.  Of about 6,000 cycles a chunk its products take 3,120,
+// shared memory's traffic 3,328 (416 KB at 128 bytes a cycle), the warps' instructions about 3,000
+// issue slots of a scheduler.  On the SMs in use the tensor pipe and L1 with shared memory are busy
+// for 51 % of the launch, issue slots for 48 %: what is left is the chain from warp to warp.
+// On an earlier form of this kernel, 60.1 us with two tiles of V, it took 12 % less without the
+// values' splitting, 13 % without the outputs' stores, 2 to 4 % without the work on states,
+// scores or copies.  Measured beside the next one (58 us), same case: parts of V' in shared memory
+// and 64 columns a block, 78 us; outputs through shared memory and TMA stores, 60; all outputs
+// read before the first store, 67; the next chunk's tiles pulled into L2 ahead of time, 60 to
+// 63; the same products issued by one lane alone (180-240 cycles each), 113 for 94 in the form
+// with 64 columns.  The decays in two numbers, what of Q S is left below the floor and scores
+// in two parts by sequence took that to 60.
+//
+// A block has an SM to itself, so blocks run in rounds: 9 such prompts of 2,048 tokens take 65 us, 10
+// take 111, 19 take 121.  Where v has 64 columns or fewer, half of a block's columns are empty:
+// 8 + 16 heads of 128 x 64 take 54 us for the 63 of 128 x 128.
 //
 // Long sequences in small numbers are cut into segments: a first launch walks all but the last
 // one from a state of zero (k and v alone), and each segment then starts from the states before
@@ -919,8 +925,10 @@ int chunks_of(const int *cu, int n) { return (cu[n + 1] - cu[n] + C - 1) / C; }
 int parts_of(int chunks, int most) { return chunks > most ? (chunks + most - 1) / most : 1; }
 
 // How long a launch takes, in chunks: `items` segments (of at most `longest` chunks, `chunks` in all)
-// for each of `lanes` heads and column tiles, longest first, on the SMs.  Where they are all alike
-// they run in whole rounds; where they are not, the shorter ones fill the last round up.
+// for each of `lanes` heads and column tiles, longest first, on the SMs.  The less of whole rounds of
+// the longest, and of everybody's share with half of the longest for an uneven end.  (Of blocks
+// that are all alike somewhat more than a round is more than it says: 10 prompts of 16 chunks
+// and 16 heads come to 28, where two rounds are 36.)
 double launch_time(long long items, int longest, long long chunks, int lanes, double begin) {
     constexpr double kSms = 152;
     const double blocks = static_cast<double>(items) * lanes, most = longest + begin;

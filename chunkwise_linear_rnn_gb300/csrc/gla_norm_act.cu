@@ -15,8 +15,8 @@
 // Bound by HBM where instructions leave it room (6 bytes a bf16 value forward with a gate, 10
 // backward).  Measured on one GB300, bf16, gate: B2 T32768, 16 heads of 256, mean, weights and
 // biases of every channel 252 us (6.4 TB/s of a copy's 6.79); B8 T2048, 16 heads of 128,
-// head-first in, gate in a wider tensor 35.5 us (5.7 TB/s); B4 T4096 of the same forward 35 us and
-// backward 73 us (4.6 TB/s) with its second launch.
+// head-first in, gate in a wider tensor 35.5 us (5.7 TB/s); B4 T4096 of the same forward 36 us and
+// backward 70 us (4.8 TB/s) with its second launch, in fp32 62 us (6.5 TB/s) and 130 us (5.2 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
